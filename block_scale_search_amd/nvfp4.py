@@ -10,6 +10,7 @@ there is no CPU path. Importing this module fails if the library has not been bu
 The convenience wrappers at the end (``diag_hessian``, ``layer_statistics``, ``global_scale``,
 ``scale_search``, ``scale_search_rules``, ``scale_search_proposal``, ``pack``, ``quantize_activations``, ``gptq``,
 ``output_error``) allocate outputs and workspaces with torch and call the entry points.
+``KVCache`` describes a paged key/value cache; the ``kv_*`` wrappers take one and a layer.
 """
 from __future__ import annotations
 
@@ -36,6 +37,15 @@ class SearchRule(ctypes.Structure):
                 ("exhaustive", ctypes.c_int32), ("scales", ctypes.c_void_p),
                 ("packed", ctypes.c_void_p), ("loss", ctypes.c_void_p),
                 ("offset", ctypes.c_void_p)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    """``nvfp4_kv_cache``."""
+    _fields_ = [("pages", ctypes.c_void_p), ("layers", _I64), ("layer_stride", _I64),
+                ("num_pages", _I64), ("page_stride", _I64), ("heads", _I32), ("head_dim", _I32),
+                ("page_size", _I32), ("max_pages", _I32), ("max_slots", _I64),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("S_k", ctypes.c_void_p), ("S_v", ctypes.c_void_p)]
 
 
 _SIGS = {
@@ -72,6 +82,18 @@ _SIGS = {
     "nvfp4_output_error_workspace_size": ([_I64, _I64, _I64], _SZ),
     "nvfp4_output_error": ([_P, _I, _I64, _I64, _I64, _P, _I, _I64, _I64, _P, _P, _P, _P, _I,
                             _P, _SZ, _P], _I),
+    "nvfp4_kv_page_bytes": ([_I32, _I32, _I32], _SZ),
+    "nvfp4_kv_append": ([_P, _I64, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I32,
+                         _I32, _P], _I),
+    "nvfp4_kv_read": ([_P, _I64, _P, _P, _I, _I64, _P, _P, _I64, _P], _I),
+    "nvfp4_kv_attention_workspace_size": ([_P, _I, _I64, _I64, _I64, _I64, _I64], _SZ),
+    "nvfp4_kv_attention": ([_P, _I64, _P, _I, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64,
+                            ctypes.c_float, _I, _I64, _P, _I64, _I64, _P, _P, _SZ, _P], _I),
+    "nvfp4_kv_pages_workspace_size": ([_P, _I64], _SZ),
+    "nvfp4_kv_reserve": ([_P, _P, _P, _I64, _P, _P, _SZ, _P], _I),
+    "nvfp4_kv_fork": ([_P, _P, _P, _I64, _P, _P, _SZ, _P], _I),
+    "nvfp4_kv_free": ([_P, _P, _I64, _P, _P], _I),
+    "nvfp4_kv_compact": ([_P, _P, _P, _SZ, _P], _I),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -401,6 +423,194 @@ def nvfp4_output_error(X, tokens, inp, ldx, W, out, ldw, scales, packed, S, err,
         _stream(stream)), prepare)
 
 
+# --- key/value cache --------------------------------------------------------------------------
+
+KV_DONE, KV_BAD_SLOT, KV_BAD_LENGTH, KV_NO_PAGES = range(4)
+
+
+def nvfp4_kv_page_bytes(heads: int, head_dim: int, page_size: int) -> int:
+    return int(_lib.nvfp4_kv_page_bytes(heads, head_dim, page_size))
+
+
+class KVCache:
+    """A paged NVFP4 key/value cache: the tensors behind ``nvfp4_kv_cache`` (kept alive here).
+
+    pages [layers, num_pages, page_bytes] uint8 (records contiguous), table [max_slots, max_pages], lens [max_slots]
+    and refs [num_pages] int32 (refs may be None where no page call is made), S_k and S_v
+    [layers, heads] float32 (None where only page calls are made). ``KVCache.empty`` allocates a
+    cache with no slot in use."""
+
+    def __init__(self, pages, table, lens, refs, S_k, S_v, heads: int, head_dim: int,
+                 page_size: int):
+        record = nvfp4_kv_page_bytes(heads, head_dim, page_size)
+        if record == 0:
+            raise Nvfp4Error(ERR_SHAPE, "KVCache")
+        if pages.dim() != 3 or pages.shape[2] < record or pages.stride(2) != 1:
+            raise ValueError(f"pages must be [layers, num_pages, >= {record}] with contiguous records")
+        layers, num_pages, _ = pages.shape
+        if table.dim() != 2:
+            raise ValueError("table must be [max_slots, max_pages]")
+        _need(table, table.numel(), "table")
+        _need(lens, table.shape[0], "lens")
+        if refs is not None:
+            _need(refs, num_pages, "refs")
+        for name, S in (("S_k", S_k), ("S_v", S_v)):
+            if S is not None:
+                _need(S, layers * heads, name)
+        i32, f32 = (torch.int32,), (torch.float32,)
+        p = lambda t, name, dt: None if t is None else _dev(t, name, dt).value  # noqa: E731
+        for name, t in (("table", table), ("lens", lens), ("refs", refs), ("S_k", S_k), ("S_v", S_v)):
+            if t is not None and t.device != pages.device:
+                raise ValueError(f"{name} must be on the pages' device")
+        self.pages, self.table, self.lens, self.refs = pages, table, lens, refs
+        self.S_k, self.S_v = S_k, S_v
+        self.heads, self.head_dim, self.page_size = heads, head_dim, page_size
+        self.layers, self.num_pages, self.device = layers, num_pages, pages.device
+        self.struct = KVCacheStruct(
+            p(pages, "pages", (torch.uint8,)), layers, pages.stride(0), num_pages, pages.stride(1),
+            heads, head_dim, page_size, table.shape[1], table.shape[0], p(table, "table", i32),
+            p(lens, "lens", i32), p(refs, "refs", i32), p(S_k, "S_k", f32), p(S_v, "S_v", f32))
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, layers: int, num_pages: int, heads: int, head_dim: int, page_size: int,
+              max_slots: int, max_pages: int, S_k, S_v, device="cuda") -> "KVCache":
+        record = nvfp4_kv_page_bytes(heads, head_dim, page_size)
+        if record == 0:
+            raise Nvfp4Error(ERR_SHAPE, "KVCache.empty")
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.empty((layers, num_pages, record), dtype=torch.uint8, device=device),
+                   torch.full((max_slots, max_pages), -1, **i32), torch.zeros(max_slots, **i32),
+                   torch.zeros(num_pages, **i32), S_k, S_v, heads, head_dim, page_size)
+
+
+class _on:
+    """Makes a cache's device current for a call (the launches go to that device's stream)."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.old = torch.cuda.current_device()
+        if self.index != self.old:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.index != self.old:
+            torch.cuda.set_device(self.old)
+
+
+def _kv_run(cache: KVCache, fname: str, args: tuple, stream, prepare: bool):
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.device != cache.device:
+            raise ValueError(f"{fname}: every tensor must be on the cache's device {cache.device}")
+    s = torch.cuda.current_stream(cache.device) if stream is None else stream
+    args = (cache.ref, *[t.data_ptr() if isinstance(t, torch.Tensor) else t for t in args],
+            s.cuda_stream)
+    f = getattr(_lib, fname)
+
+    def call():
+        with _on(cache.device):
+            _check(f(*args), fname)
+    return call if prepare else call()
+
+
+def _i32(t, numel: int, name: str):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor on the GPU")
+    _need(t, numel, name)
+    return t
+
+
+def _kv_rows(t, heads, dim, name):
+    """A token tensor [tokens, heads, dim] with contiguous rows; its token and head strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a tensor on the GPU")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}] with contiguous rows")
+    return t.stride(0), t.stride(1)
+
+
+def nvfp4_kv_append(cache: KVCache, layer, K, V, cu_tokens, slots, seqs, lo, hi, stream=None,
+                    prepare=False):
+    skt, skh = _kv_rows(K, cache.heads, cache.head_dim, "K")
+    svt, svh = _kv_rows(V, cache.heads, cache.head_dim, "V")
+    if V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("K and V must have the same shape and element type")
+    return _kv_run(cache, "nvfp4_kv_append", (
+        layer, K, V, _wdtype(K), K.shape[0], skt, skh, svt, svh,
+        _i32(cu_tokens, seqs + 1, "cu_tokens"), _i32(slots, seqs, "slots"), seqs, lo, hi),
+        stream, prepare)
+
+
+def nvfp4_kv_read(cache: KVCache, layer, K, V, tokens, cu_tokens, slots, seqs, stream=None,
+                  prepare=False):
+    for name, t in (("K", K), ("V", V)):
+        _kv_rows(t, cache.heads, cache.head_dim, name)
+        _need(t, tokens * cache.heads * cache.head_dim, name)
+    if V.dtype != K.dtype:
+        raise ValueError("K and V must have the same element type")
+    return _kv_run(cache, "nvfp4_kv_read", (
+        layer, K, V, _wdtype(K), tokens, _i32(cu_tokens, seqs + 1, "cu_tokens"),
+        _i32(slots, seqs, "slots"), seqs), stream, prepare)
+
+
+def nvfp4_kv_attention_workspace_size(cache: KVCache, dtype, tokens, q_heads, seqs, max_q,
+                                      max_kv) -> int:
+    """dtype: torch.bfloat16 or torch.float32."""
+    dt = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
+    return int(_lib.nvfp4_kv_attention_workspace_size(cache.ref, dt, tokens, q_heads, seqs, max_q,
+                                                      max_kv))
+
+
+def nvfp4_kv_attention(cache: KVCache, layer, Q, cu_tokens, slots, seqs, max_q, max_kv, scale,
+                       causal, window, O, lse, workspace, stream=None, prepare=False):
+    q_heads = Q.shape[1] if Q.dim() == 3 else 0
+    sqt, sqh = _kv_rows(Q, q_heads, cache.head_dim, "Q")
+    sot, soh = _kv_rows(O, q_heads, cache.head_dim, "O")
+    if O.shape != Q.shape or O.dtype != Q.dtype:
+        raise ValueError("O and Q must have the same shape and element type")
+    if lse is not None:
+        if lse.dtype != torch.float32:
+            raise TypeError("lse must be float32")
+        _need(lse, Q.shape[0] * q_heads, "lse")
+    return _kv_run(cache, "nvfp4_kv_attention", (
+        layer, Q, _wdtype(Q), Q.shape[0], q_heads, sqt, sqh,
+        _i32(cu_tokens, seqs + 1, "cu_tokens"), _i32(slots, seqs, "slots"), seqs, max_q, max_kv,
+        scale, int(causal), window, O, sot, soh, lse, workspace,
+        0 if workspace is None else workspace.numel() * workspace.element_size()), stream, prepare)
+
+
+def nvfp4_kv_pages_workspace_size(cache: KVCache, n: int) -> int:
+    return int(_lib.nvfp4_kv_pages_workspace_size(cache.ref, n))
+
+
+def nvfp4_kv_reserve(cache: KVCache, slots, counts, n, status, workspace, stream=None, prepare=False):
+    return _kv_run(cache, "nvfp4_kv_reserve", (
+        _i32(slots, n, "slots"), _i32(counts, n, "counts"), n, _i32(status, 1, "status"), workspace,
+        workspace.numel() * workspace.element_size()), stream, prepare)
+
+
+def nvfp4_kv_fork(cache: KVCache, parents, children, n, status, workspace, stream=None,
+                  prepare=False):
+    return _kv_run(cache, "nvfp4_kv_fork", (
+        _i32(parents, n, "parents"), _i32(children, n, "children"), n, _i32(status, 1, "status"),
+        workspace, workspace.numel() * workspace.element_size()), stream, prepare)
+
+
+def nvfp4_kv_free(cache: KVCache, slots, n, status, stream=None, prepare=False):
+    return _kv_run(cache, "nvfp4_kv_free", (
+        _i32(slots, n, "slots"), n, _i32(status, 1, "status")), stream, prepare)
+
+
+def nvfp4_kv_compact(cache: KVCache, used, workspace, stream=None, prepare=False):
+    return _kv_run(cache, "nvfp4_kv_compact", (
+        _i32(used, 1, "used"), workspace, workspace.numel() * workspace.element_size()), stream,
+        prepare)
+
+
 # --- convenience wrappers (allocate outputs with torch, then call the entry points) ----------
 
 def _bmat(W: torch.Tensor):
@@ -617,3 +827,75 @@ def pack(W: torch.Tensor, scales: torch.Tensor, S: torch.Tensor, stream=None) ->
     packed = torch.empty(scales.shape[:-1] + (n // 2,), dtype=torch.uint8, device=W.device)
     nvfp4_pack(W, b, o, n, ldw, sw, scales, S, packed, stream)
     return packed
+
+
+def kv_append(cache: KVCache, layer: int, K: torch.Tensor, V: torch.Tensor, cu_tokens: torch.Tensor,
+              slots: torch.Tensor | None = None, lo: int = -3, hi: int = 7, stream=None) -> None:
+    """Quantise new rows K, V [tokens, heads, head_dim] into the pages of their slots: item i's rows
+    cu_tokens[i] .. cu_tokens[i+1] - 1 are the last tokens of slot slots[i] (None: slot i)."""
+    nvfp4_kv_append(cache, layer, K, V, cu_tokens, slots, cu_tokens.numel() - 1, lo, hi, stream)
+
+
+def kv_read(cache: KVCache, layer: int, tokens: int, cu_tokens: torch.Tensor,
+            slots: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16, stream=None):
+    """The cached values of the items' last rows: (K, V), each [tokens, heads, head_dim]."""
+    shape = (tokens, cache.heads, cache.head_dim)
+    K = torch.empty(shape, dtype=dtype, device=cache.device)
+    V = torch.empty(shape, dtype=dtype, device=cache.device)
+    nvfp4_kv_read(cache, layer, K, V, tokens, cu_tokens, slots, cu_tokens.numel() - 1, stream)
+    return K, V
+
+
+def kv_attention(cache: KVCache, layer: int, Q: torch.Tensor, cu_tokens: torch.Tensor,
+                 slots: torch.Tensor | None = None, max_q: int | None = None,
+                 max_kv: int | None = None, scale: float | None = None, causal: bool = True,
+                 window: int = 0, stream=None):
+    """Attention of Q [tokens, q_heads, head_dim] over the cached keys and values; returns
+    (out like Q, lse float32 [tokens, q_heads]). max_q and max_kv bound the items' rows and lengths
+    (None: all rows, the table's capacity; tight bounds split the work better)."""
+    T, q_heads, D = Q.shape
+    seqs = cu_tokens.numel() - 1
+    max_q = T if max_q is None else max_q
+    max_kv = cache.table.shape[1] * cache.page_size if max_kv is None else max_kv
+    out = torch.empty((T, q_heads, D), dtype=Q.dtype, device=Q.device)
+    lse = torch.empty((T, q_heads), dtype=torch.float32, device=Q.device)
+    need = nvfp4_kv_attention_workspace_size(cache, Q.dtype, T, q_heads, seqs, max_q, max_kv)
+    ws = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+    nvfp4_kv_attention(cache, layer, Q, cu_tokens, slots, seqs, max_q, max_kv,
+                       D ** -0.5 if scale is None else scale, causal, window, out, lse, ws, stream)
+    return out, lse
+
+
+def _pages_space(cache: KVCache, n: int):
+    return torch.empty(max(16, nvfp4_kv_pages_workspace_size(cache, n)), dtype=torch.uint8,
+                       device=cache.device)
+
+
+def kv_reserve(cache: KVCache, slots: torch.Tensor, counts: torch.Tensor, stream=None) -> torch.Tensor:
+    """Room for counts[i] more tokens in slots[i]; returns the device status (KV_DONE, ...) [1]."""
+    status = torch.empty(1, dtype=torch.int32, device=cache.device)
+    n = slots.numel()
+    nvfp4_kv_reserve(cache, slots, counts, n, status, _pages_space(cache, n), stream)
+    return status
+
+
+def kv_fork(cache: KVCache, parents: torch.Tensor, children: torch.Tensor, stream=None) -> torch.Tensor:
+    """Empty slots children[i] become copies of parents[i]; returns the device status [1]."""
+    status = torch.empty(1, dtype=torch.int32, device=cache.device)
+    n = parents.numel()
+    nvfp4_kv_fork(cache, parents, children, n, status, _pages_space(cache, n), stream)
+    return status
+
+
+def kv_free(cache: KVCache, slots: torch.Tensor, stream=None) -> torch.Tensor:
+    """Empties slots; returns the device status [1]."""
+    status = torch.empty(1, dtype=torch.int32, device=cache.device)
+    nvfp4_kv_free(cache, slots, slots.numel(), status, stream)
+    return status
+
+
+def kv_compact(cache: KVCache, stream=None) -> torch.Tensor:
+    """Moves the used pages to the lowest numbers; returns how many there are, on the device [1]."""
+    used = torch.empty(1, dtype=torch.int32, device=cache.device)
+    nvfp4_kv_compact(cache, used, _pages_space(cache, 0), stream)
+    return used

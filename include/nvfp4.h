@@ -452,6 +452,166 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
                                 double* err, int accumulate, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Key/value cache in NVFP4 ([SS] Experimental Results: the WAKV and WAKVQ settings quantise the KV
+ * cache with the same sweep as weights and activations). Tokens' keys and values live in pages of
+ * `page_size` tokens as 4-bit codes with one E4M3 scale byte per 16 values; the FP32 global scales
+ * S_k and S_v are per layer and head, fixed by the caller (e.g. nvfp4_global_scale over calibration
+ * keys and values). The host struct below describes a cache; every pointer in it is device memory
+ * owned by the caller, and the struct is read during the call only.
+ *
+ * A slot (a sequence) is a row of `table`: position p of slot s lies in page table[s][p / page_size]
+ * at row p % page_size. lens[s] is the slot's length in tokens. A slot holds exactly
+ * ceil(lens / page_size) pages; the table's other entries are not read. refs[p] is the number of
+ * slots that hold page p (0: free). Full pages may be shared by several slots; a partly filled last
+ * page belongs to one slot alone. A new cache has lens and refs zeroed and table filled with -1;
+ * nvfp4_kv_reserve, _fork, _free and _compact keep these rules.
+ *
+ * One layer of one page is a record of nvfp4_kv_page_bytes(heads, head_dim, page_size) =
+ * heads * page_size * head_dim * 9 / 8 bytes with four regions back to back (H heads, P tokens,
+ * D values per head, E = D / 32 bytes):
+ *   K codes   [H][P][D/2]         two values per byte, the even one in the low nibble
+ *   V codes   [H][P/4][16][4][E]  values n D/16 .. (n+1) D/16 - 1 of token t at [t/4][n][t%4], packed
+ *                                 like K's: four tokens' codes of the same values lie together
+ *   K scales  [H][P][D/16]        E4M3 codes 0..126
+ *   V scales  [H][P/4][D/16][4]   token t's at [t/4][:][t%4]
+ * Record of layer l, page p: pages + l * layer_stride + p * page_stride (bytes).
+ *
+ * Requires head_dim 64, 128 or 256; page_size a multiple of 16; pages 16-byte aligned, strides
+ * multiples of 16 bytes, page_stride >= the record, layer_stride >= num_pages * page_stride when
+ * layers > 1; max_slots <= 65,536; max_pages * page_size, max_slots * max_pages and num_pages
+ * < 2^31 (else NVFP4_ERR_SHAPE / NVFP4_ERR_ALIGN).
+ *
+ * Batch arguments of the token calls: cu_tokens, device int32 [seqs + 1], non-decreasing from 0, gives
+ * item i the rows cu_tokens[i] .. cu_tokens[i+1] - 1 of the token tensors; slots, device int32
+ * [seqs], names its slot (NULL: slot i). An item's n rows are the LAST n tokens of its slot:
+ * row j is position lens[slot] - n + j, so that one nvfp4_kv_reserve makes room for a step's tokens
+ * and every layer's append, read and attention then use the same lengths. The device contents are
+ * checked where a bad one could reach memory outside the cache: an item whose slot is outside
+ * 0 .. max_slots - 1 has length 0, lengths are clamped to 0 .. max_pages * page_size, and a position
+ * that is negative or whose table entry is outside 0 .. num_pages - 1 is not in the cache.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct nvfp4_kv_cache {
+    uint8_t* pages;          /* device, [layers][num_pages] records */
+    int64_t layers;
+    int64_t layer_stride;    /* bytes */
+    int64_t num_pages;
+    int64_t page_stride;     /* bytes */
+    int32_t heads;           /* key/value heads */
+    int32_t head_dim;
+    int32_t page_size;       /* tokens per page */
+    int32_t max_pages;       /* columns of table */
+    int64_t max_slots;       /* rows of table */
+    int32_t* table;          /* device, [max_slots, max_pages] */
+    int32_t* lens;           /* device, [max_slots] */
+    int32_t* refs;           /* device, [num_pages]; only the page calls use it (else may be NULL) */
+    const float* S_k;        /* device, [layers, heads], positive (see nvfp4_scale_search's S); */
+    const float* S_v;        /*   only the token calls use them (else may be NULL) */
+} nvfp4_kv_cache;
+
+/* Bytes of one layer of one page; 0 for a layout that is not supported. */
+size_t nvfp4_kv_page_bytes(int32_t heads, int32_t head_dim, int32_t page_size);
+
+/* Quantise new tokens' keys and values into their pages of one layer. Each group of 16 values of a
+ * token's head gets the codes and scale byte of nvfp4_scale_search (MSE, window lo..hi; [SS]'s
+ * [-3, 7]; lo = hi = 0 is the max-abs rule) with S = S_k[layer, head] or S_v[layer, head], bit for
+ * bit. Positions that are not in the cache are skipped; nothing else is written, so the unused
+ * rows of a page keep their bytes. Pages of the items must be distinct (as the page calls keep them).
+ *
+ * K, V     device, bf16 or f32 [tokens, heads, head_dim], element strides stride_kt / stride_kh and
+ *          stride_vt / stride_vh >= 0, rows 16-byte aligned (strides multiples of 16 bytes).
+ * Requires tokens * head_dim / 16 < 2^31. */
+nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, int64_t layer, const void* K, const void* V,
+                             int dtype, int64_t tokens, int64_t stride_kt, int64_t stride_kh,
+                             int64_t stride_vt, int64_t stride_vh, const int32_t* cu_tokens,
+                             const int32_t* slots, int64_t seqs, int32_t lo, int32_t hi,
+                             void* stream);
+
+/* The values the cache holds for tokens, the inverse of append: fl(S * (level * E4M3(scale))), to
+ * bf16 (rounded to nearest even) or f32, K and V [tokens, heads, head_dim] contiguous, 16-byte
+ * aligned; zeros for positions that are not in the cache. Rows behind cu_tokens[seqs] are left as
+ * they are. Requires tokens * head_dim / 16 < 2^31. */
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, int64_t layer, void* K, void* V, int dtype,
+                           int64_t tokens, const int32_t* cu_tokens, const int32_t* slots,
+                           int64_t seqs, void* stream);
+
+/* Attention of query rows over the cached keys and values of their slots, one layer.
+ *   k, v        = S * (level * E4M3(scale)) of the cached codes
+ *   logit[t, p] = scale * sum_d q[t, d] k[p, d]
+ *   visible     = positions p < lens of the item's slot, in the cache; if causal also p <= pos(t);
+ *                 if window > 0 also p > pos(t) - window
+ *   out[t]      = sum_p exp(logit[t, p]) v[p] / sum_p exp(logit[t, p])   over the visible p
+ *   lse[t]      = ln sum_p exp(logit[t, p])
+ * A row that sees no position gets zeros and lse = -infinity. Query head j reads key/value head
+ * j / (q_heads / heads). Not causal: every row sees the whole slot (e.g. an encoder's states).
+ *
+ * The products run on f16 MFMA with binary32 sums: level * E4M3 has at most 6 significant bits and is
+ * exact in f16; a bf16 query row is exact after a power-of-two scaling of the row; an f32 query
+ * and f32-output probabilities are split into two f16 halves (22 bits); for bf16 the probabilities
+ * are rounded to f16. Softmax statistics and outputs are accumulated in binary32.
+ *
+ * Q, O     device, bf16 or f32 (dtype), [tokens, q_heads, head_dim] with element strides stride_qt /
+ *          stride_qh >= 0 and stride_ot / stride_oh (rows of O must not overlap), 16-byte aligned
+ *          rows. O may not overlap Q.
+ * lse      device float [tokens, q_heads] or NULL.
+ * max_q    at least every item's number of rows; rows at or beyond max_q of an item are not written.
+ * max_kv   at least every item's length; positions at or beyond it are left out.
+ * causal, window   window 0: none; window > 0 needs causal.
+ * scale    positive, finite (commonly 1 / sqrt(head_dim)).
+ * workspace  device, nvfp4_kv_attention_workspace_size(...) bytes with the same sizes, 16-byte
+ *          aligned, no initialisation needed (may be NULL when that is 0).
+ * Rows of O and lse behind cu_tokens[seqs] are left as they are.
+ * Requires heads <= 65,535, q_heads a multiple of heads, tokens * q_heads < 2^31, seqs <= 65,535,
+ * max_q * (q_heads / heads) < 2^24. */
+size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int dtype, int64_t tokens,
+                                         int64_t q_heads, int64_t seqs, int64_t max_q,
+                                         int64_t max_kv);
+
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, int64_t layer, const void* Q, int dtype,
+                                int64_t tokens, int64_t q_heads, int64_t stride_qt,
+                                int64_t stride_qh, const int32_t* cu_tokens, const int32_t* slots,
+                                int64_t seqs, int64_t max_q, int64_t max_kv, float scale,
+                                int causal, int64_t window, void* O, int64_t stride_ot,
+                                int64_t stride_oh, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Page calls: they change table, lens and refs on the device, for all layers at once, without a
+ * host round trip (they can be captured in a graph). status, device int32 [1], is written with
+ * NVFP4_KV_DONE, or with the first reason below that holds, and then nothing else is changed.
+ * The free pages taken are the lowest-numbered ones, in the order of the items and of the positions.
+ * workspace: nvfp4_kv_pages_workspace_size(cache, n) bytes, 16-byte aligned, no initialisation
+ * needed. n <= 65,536. */
+enum {
+    NVFP4_KV_DONE = 0,
+    NVFP4_KV_BAD_SLOT = 1,   /* a slot outside the table or listed twice; fork: a child that is
+                                not empty or is also a parent */
+    NVFP4_KV_BAD_LENGTH = 2, /* reserve: a negative count, or a length beyond max_pages pages */
+    NVFP4_KV_NO_PAGES = 3    /* not enough free pages */
+};
+
+size_t nvfp4_kv_pages_workspace_size(const nvfp4_kv_cache* cache, int64_t n);
+
+/* lens[slots[i]] += counts[i], with pages for the new positions. slots, counts: device int32 [n]. */
+nvfp4_status nvfp4_kv_reserve(const nvfp4_kv_cache* cache, const int32_t* slots,
+                              const int32_t* counts, int64_t n, int32_t* status, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Slot children[i] (empty) becomes a copy of slot parents[i]: full pages are shared, a partly
+ * filled last page is copied in every layer. A parent may be listed several times. */
+nvfp4_status nvfp4_kv_fork(const nvfp4_kv_cache* cache, const int32_t* parents,
+                           const int32_t* children, int64_t n, int32_t* status, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Slots slots[i] give their pages back and become empty (their table entries -1). */
+nvfp4_status nvfp4_kv_free(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t n,
+                           int32_t* status, void* stream);
+
+/* Draw the used pages together: with U pages in use, the k-th used page at or above U moves, in
+ * every layer, to the k-th free page below U, and table and refs follow; pages U .. num_pages - 1
+ * are then free. used, device int32 [1], receives U. workspace as above with n = 0. */
+nvfp4_status nvfp4_kv_compact(const nvfp4_kv_cache* cache, int32_t* used, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
