@@ -26,7 +26,7 @@ int elem_size(int dtype) {
 
 bool layout_ok(int64_t heads, int64_t dim, int64_t page) {
     return heads >= 1 && heads <= 65535 && (dim == 64 || dim == 128 || dim == 256) && page >= 16 &&
-           page % 16 == 0;
+           page % 16 == 0 && nvfp4::kv_record_bytes(heads, dim, page) < kInt32;
 }
 
 // What every call needs of a cache. `tokens`: a token call (S_k, S_v), else a page call (refs).
@@ -36,7 +36,7 @@ nvfp4_status check_cache(const nvfp4_kv_cache* c, bool tokens) {
     const int64_t rec = nvfp4::kv_record_bytes(c->heads, c->head_dim, c->page_size);
     if (c->layers < 1 || c->layers > 65535 || c->num_pages < 0 || c->num_pages >= kInt32 - 4096 ||
         c->max_slots < 0 || c->max_slots > 65536 || c->max_pages < 0 ||
-        (int64_t)c->max_pages * c->page_size >= kInt32 || c->max_slots * c->max_pages >= kInt32)
+        (int64_t)c->max_pages * c->page_size > kInt32 - 65536 || c->max_slots * c->max_pages >= kInt32)
         return NVFP4_ERR_SHAPE;
     if (c->page_stride < rec || !span_ok(c->num_pages, c->page_stride)) return NVFP4_ERR_SHAPE;
     if (c->layers > 1 && (c->layer_stride < c->num_pages * c->page_stride ||

@@ -479,8 +479,8 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  *
  * Requires head_dim 64, 128 or 256; page_size a multiple of 16; pages 16-byte aligned, strides
  * multiples of 16 bytes, page_stride >= the record, layer_stride >= num_pages * page_stride when
- * layers > 1; max_slots <= 65,536; max_pages * page_size, max_slots * max_pages and num_pages
- * < 2^31 (else NVFP4_ERR_SHAPE / NVFP4_ERR_ALIGN).
+ * layers > 1; max_slots <= 65,536; max_pages * page_size <= 2^31 - 65,536; max_slots * max_pages <
+ * 2^31; num_pages < 2^31 - 4,096; one record < 2^31 bytes (else NVFP4_ERR_SHAPE / NVFP4_ERR_ALIGN).
  *
  * Batch arguments of the token calls: cu_tokens, device int32 [seqs + 1], non-decreasing from 0, gives
  * item i the rows cu_tokens[i] .. cu_tokens[i+1] - 1 of the token tensors; slots, device int32
