@@ -22,8 +22,16 @@
 namespace nvfp4 {
 namespace {
 
+#ifndef KV_TARGET
+#define KV_TARGET 2048
+#endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
+#ifndef KV_DEPTH
+#define KV_DEPTH 2
+#endif
+constexpr int kMaxSplits = 512;      // chunks of a row
+constexpr int kDepth = KV_DEPTH;     // tiles of a wave in LDS
 constexpr float kUp = 8.0f;          // log2 of the weights' scale
 constexpr float kSlack = 7.0f;       // how far a logit may exceed the maximum in use, log2
 
@@ -35,48 +43,164 @@ struct HalfTile {
     uint32_t k[W], v[W], ks, vs;
 };
 
-template <int W>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[W]) {
-    if constexpr (W == 2) {
-        const uint2 t = *reinterpret_cast<const uint2*>(p);
-        w[0] = t.x; w[1] = t.y;
-    } else {
+// A tile of 32 positions in LDS, as it is copied from the pages: the codes of [K half 0][K half 1]
+// [V half 0][V half 1], then their scale bytes in the same order. In K's rows the 16-byte pieces
+// are permuted (piece c of row n at c ^ f(n)), so that 16 lanes reading one piece of 16 rows use all
+// banks; the copy's source addresses carry the permutation.
+template <int D>
+struct TileLds {
+    static constexpr int kHalf = 8 * D;                  // code bytes of a half
+    static constexpr int kScales = 4 * kHalf;
+    static constexpr int kBytes = kScales + 4 * D;
+    static constexpr int kCodeLoads = kScales / 1024;    // 64 lanes x 16 bytes each
+    static constexpr int kLoads = kCodeLoads + 1;
+    static constexpr int kPieces = D / 32;               // of a row of K
+    static constexpr int kShift = D == 64 ? 3 : D == 128 ? 2 : 1;
+    static __device__ __forceinline__ int f(int n) { return (n >> kShift) & (kPieces - 1); }
+};
+
+// A lane's source offsets in the records: load j of a tile's codes, and the scales (lane < D / 4).
+template <int D>
+struct CopyOffsets {
+    uint32_t code[TileLds<D>::kCodeLoads], scale;
+};
+
+template <int D>
+__device__ __forceinline__ CopyOffsets<D> copy_offsets(const KvView& kv, int head, int lane) {
+    using T = TileLds<D>;
+    const uint32_t region = (uint32_t)kv_code_bytes(kv);
+    CopyOffsets<D> o;
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-            const uint4 t = reinterpret_cast<const uint4*>(p)[i];
-            w[4 * i] = t.x; w[4 * i + 1] = t.y; w[4 * i + 2] = t.z; w[4 * i + 3] = t.w;
+    for (int j = 0; j < T::kCodeLoads; ++j) {
+        const uint32_t at = 1024 * j + 16 * lane, part = at / T::kHalf;
+        uint32_t in = at % T::kHalf;
+        if (part < 2) {                                  // K: the piece that belongs at this place
+            const uint32_t n = in / (D / 2), c = in % (D / 2) / 16;
+            in = n * (D / 2) + (c ^ T::f(n)) * 16;
+        }
+        o.code[j] = (uint32_t)head * kv.page * (D / 2) + in + (part < 2 ? 0 : region);
+    }
+    const uint32_t at = 16 * lane, part = at / D;
+    o.scale = 2 * region + (uint32_t)head * kv.page * (D / 16) + at % D +
+              (part < 2 ? 0 : region >> 3);
+    return o;
+}
+
+typedef __attribute__((address_space(1))) const void* GlobalPtr;
+typedef __attribute__((address_space(3))) void* LdsPtr;
+
+// 16 bytes a lane from global memory to lds + 16 * lane (lds uniform).
+__device__ __forceinline__ void copy16(const uint8_t* src, uint8_t* lds) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)lds, 16, 0, 0);
+}
+
+// Copies a tile: rec[u] and row[u] are the record and first row of half u (uniform).
+template <int D>
+__device__ __forceinline__ void copy_tile(uint8_t* lds, const uint8_t* rec0, int row0,
+                                          const uint8_t* rec1, int row1, const CopyOffsets<D>& o,
+                                          int lane) {
+    using T = TileLds<D>;
+    const uint8_t* c0 = rec0 + (int64_t)row0 * (D / 2);
+    const uint8_t* c1 = rec1 + (int64_t)row1 * (D / 2);
+#pragma unroll
+    for (int j = 0; j < T::kCodeLoads; ++j) {
+        const bool second = D == 64 ? lane >= 32 : (1024 * j / T::kHalf) & 1;
+        copy16((second ? c1 : c0) + o.code[j], lds + 1024 * j);
+    }
+    const uint8_t* s0 = rec0 + (int64_t)row0 * (D / 16);
+    const uint8_t* s1 = rec1 + (int64_t)row1 * (D / 16);
+    if (lane < D / 4) copy16(((16 * lane / D) & 1 ? s1 : s0) + o.scale, lds + T::kScales);
+}
+
+// A lane's LDS addresses in a tile, for lane (n, g).
+struct ReadOffsets {
+    uint32_t k[2], v, ks, vs;
+};
+
+template <int D>
+__device__ __forceinline__ ReadOffsets read_offsets(int n, int g) {
+    using T = TileLds<D>;
+    ReadOffsets r;
+    if constexpr (D == 64) {
+        r.k[0] = r.k[1] = n * 32 + ((g >> 1) ^ T::f(n)) * 16 + (g & 1) * 8;
+    } else if constexpr (D == 128) {
+        r.k[0] = r.k[1] = n * 64 + (g ^ T::f(n)) * 16;
+    } else {
+        r.k[0] = n * 128 + ((2 * g) ^ T::f(n)) * 16;
+        r.k[1] = n * 128 + ((2 * g + 1) ^ T::f(n)) * 16;
+    }
+    r.v = 2 * T::kHalf + (g * 16 + n) * (D / 8);
+    r.ks = T::kScales + n * (D / 16) + g * (D / 64);
+    r.vs = T::kScales + 2 * D + (g * (D / 16) + n * D / 256) * 4;
+    return r;
+}
+
+// Reads a tile into registers. The reads and their wait are one block: the copies into other tiles of
+// the ring stay in flight, which the compiler's own waits for LDS reads would not allow.
+template <int D>
+__device__ __forceinline__ void read_tile(HalfTile<D> (&h)[2], uint32_t base, const ReadOffsets& o) {
+    constexpr int H = TileLds<D>::kHalf;
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const uint32_t k = base + o.k[0], v = base + o.v, ks = base + o.ks, vs = base + o.vs;
+    if constexpr (D == 64) {
+        u32x2 k0, k1, v0, v1;
+        asm volatile(
+            "ds_read_b64 %0, %8\n ds_read_b64 %1, %8 offset:%c12\n"
+            "ds_read_b64 %2, %9\n ds_read_b64 %3, %9 offset:%c12\n"
+            "ds_read_u8 %4, %10\n ds_read_u8 %5, %10 offset:%c13\n"
+            "ds_read_b32 %6, %11\n ds_read_b32 %7, %11 offset:%c13\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(k0), "=&v"(k1), "=&v"(v0), "=&v"(v1), "=&v"(h[0].ks), "=&v"(h[1].ks),
+              "=&v"(h[0].vs), "=&v"(h[1].vs)
+            : "v"(k), "v"(v), "v"(ks), "v"(vs), "n"(H), "n"(D)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            h[0].k[i] = k0[i]; h[1].k[i] = k1[i]; h[0].v[i] = v0[i]; h[1].v[i] = v1[i];
+        }
+    } else if constexpr (D == 128) {
+        u32x4 k0, k1, v0, v1;
+        asm volatile(
+            "ds_read_b128 %0, %8\n ds_read_b128 %1, %8 offset:%c12\n"
+            "ds_read_u16 %4, %10\n ds_read_u16 %5, %10 offset:%c13\n"
+            "ds_read_b128 %2, %9\n ds_read_b128 %3, %9 offset:%c12\n"
+            "ds_read_b32 %6, %11\n ds_read_b32 %7, %11 offset:%c13\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(k0), "=&v"(k1), "=&v"(v0), "=&v"(v1), "=&v"(h[0].ks), "=&v"(h[1].ks),
+              "=&v"(h[0].vs), "=&v"(h[1].vs)
+            : "v"(k), "v"(v), "v"(ks), "v"(vs), "n"(H), "n"(D)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[0].k[i] = k0[i]; h[1].k[i] = k1[i]; h[0].v[i] = v0[i]; h[1].v[i] = v1[i];
+        }
+    } else {
+        u32x4 k0, k1, k2, k3, v0, v1, v2, v3;
+        const uint32_t kb = base + o.k[1];
+        asm volatile(
+            "ds_read_b128 %0, %12\n ds_read_b128 %1, %13\n"
+            "ds_read_b128 %2, %12 offset:%c17\n ds_read_b128 %3, %13 offset:%c17\n"
+            "ds_read_b32 %8, %15\n ds_read_b32 %9, %15 offset:%c18\n"
+            "ds_read_b128 %4, %14\n ds_read_b128 %5, %14 offset:16\n"
+            "ds_read_b128 %6, %14 offset:%c17\n ds_read_b128 %7, %14 offset:%c19\n"
+            "ds_read_b32 %10, %16\n ds_read_b32 %11, %16 offset:%c18\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(k0), "=&v"(k1), "=&v"(k2), "=&v"(k3), "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3),
+              "=&v"(h[0].ks), "=&v"(h[1].ks), "=&v"(h[0].vs), "=&v"(h[1].vs)
+            : "v"(k), "v"(kb), "v"(v), "v"(ks), "v"(vs), "n"(H), "n"(D), "n"(H + 16)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[0].k[i] = k0[i]; h[0].k[4 + i] = k1[i]; h[1].k[i] = k2[i]; h[1].k[4 + i] = k3[i];
+            h[0].v[i] = v0[i]; h[0].v[4 + i] = v1[i]; h[1].v[i] = v2[i]; h[1].v[4 + i] = v3[i];
         }
     }
 }
 
-// Offsets of a lane's bytes in a record, without the part that depends on the tile's first row.
-struct LaneOffsets {
-    uint32_t k, ks, v, vs;
-};
-
-template <int D>
-__device__ __forceinline__ LaneOffsets lane_offsets(const KvView& kv, int head, int n, int g) {
-    const uint32_t half = (uint32_t)kv_code_bytes(kv);
-    const uint32_t row = (uint32_t)head * kv.page;
-    LaneOffsets o;
-    o.k = (row + n) * (D / 2) + g * (D / 8);
-    o.ks = 2 * half + (row + n) * (D / 16) + g * (D / 64);
-    o.v = half + (((row >> 2) + g) * 16 + n) * (D / 8);
-    o.vs = 2 * half + (half >> 3) + (((row >> 2) + g) * (D / 16) + n * D / 256) * 4;
-    return o;
-}
-
-// rec: the page's record; row: the half tile's first row in it (both uniform).
-template <int D>
-__device__ __forceinline__ void load_half(HalfTile<D>& t, const uint8_t* rec, int row,
-                                          const LaneOffsets& o) {
-    load_words<D / 32>(rec + o.k + row * (D / 2), t.k);
-    const uint8_t* s = rec + o.ks + row * (D / 16);
-    if constexpr (D == 64) t.ks = *s;
-    else if constexpr (D == 128) t.ks = *reinterpret_cast<const uint16_t*>(s);
-    else t.ks = *reinterpret_cast<const uint32_t*>(s);
-    load_words<D / 32>(rec + o.v + row * (D / 2), t.v);
-    t.vs = *reinterpret_cast<const uint32_t*>(rec + o.vs + row * (D / 16));
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("s_waitcnt vmcnt(%c0)" ::"n"(N) : "memory");
 }
 
 // K operand of step s: values 8 s .. 8 s + 7 of the lane's D/4.
@@ -156,31 +280,38 @@ struct QRow {
     float f;                 // logit (log2) of a product
 };
 
+// A lane's query values as they lie in memory (zeros for no row).
 template <int D, bool BF16>
-__device__ __forceinline__ void load_query(QRow<D, BF16>& q, const uint8_t* p, int g, float scale,
-                                           float S) {
+struct RawQuery {
+    static constexpr int W = BF16 ? D / 32 : D / 16;
+    uint4 w[W];
+};
+
+template <int D, bool BF16>
+__device__ __forceinline__ void load_query(RawQuery<D, BF16>& r, const uint8_t* p, bool live, int g) {
+    constexpr int W = RawQuery<D, BF16>::W;
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[g * W + i];
+    }
+}
+
+template <int D, bool BF16>
+__device__ __forceinline__ void convert_query(QRow<D, BF16>& q, const RawQuery<D, BF16>& r, float scale,
+                                              float S) {
     float x[D / 4];
 #pragma unroll
-    for (int i = 0; i < D / 4; ++i) x[i] = 0.0f;
-    if (p) {
-        if constexpr (BF16) {
-            const uint4* s = reinterpret_cast<const uint4*>(p + g * (D / 2));
+    for (int i = 0; i < RawQuery<D, BF16>::W; ++i) {
+        const uint32_t d[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint4 t = s[i];
-                const uint32_t d[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[8 * i + 2 * k] = bf16_lo(d[k]);
-                    x[8 * i + 2 * k + 1] = bf16_hi(d[k]);
-                }
-            }
-        } else {
-            const float4* s = reinterpret_cast<const float4*>(p + g * D);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const float4 t = s[i];
-                x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (BF16) {
+                x[8 * i + 2 * k] = bf16_lo(d[k]);
+                x[8 * i + 2 * k + 1] = bf16_hi(d[k]);
+            } else {
+                x[4 * i + k] = __uint_as_float(d[k]);
             }
         }
     }
@@ -228,11 +359,20 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l > 0.0f ? (m - kUp + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
 }
 
+// Waves a SIMD should hold: as many as the accumulators and two tiles in flight leave room for.
+template <int D, int RT>
+constexpr int kOccupancy = D * RT <= 128 ? 4 : D * RT <= 256 ? 2 : 1;
+
 template <int D, bool BF16, int RT>
-__global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan plan) {
+__global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvAttention a, KvPlan plan) {
     constexpr int R = 16 * RT, NJ = D / 16, NS = D / 32;
     constexpr int JC = NJ < 8 ? NJ : 8;                  // output tiles joined at a time
-    __shared__ float joined[kWaves][16][JC * 16 + 4];
+    using T = TileLds<D>;
+    constexpr int kRing = kDepth * T::kBytes;            // a wave's tiles; later the joined outputs
+    constexpr int kRow = JC * 16 + 4;
+    constexpr int kJoin = 16 * kRow * 4;
+    __shared__ __align__(16) uint8_t space[kWaves * (kRing > kJoin ? kRing : kJoin)];
+    float(*joined)[16][kRow] = reinterpret_cast<float(*)[16][kRow]>(space);
     __shared__ float2 stat[kWaves][R];
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -260,18 +400,16 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
     const int begin = range.begin + split * plan.chunk;
     const int end = min(range.end, begin + plan.chunk);
 
-    QRow<D, BF16> q[RT];
+    RawQuery<D, BF16> raw[RT];
     int low[RT], lim[RT];                                // the lane's row sees low .. lim - 1
     int low_all = 0, lim_all = end;                      // and so does every row
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + 16 * rt + n;
         const bool live = 16 * rt + n < rows;
-        const RowAt at = row_at(first, head, group, live ? row : row0);
-        const uint8_t* p = static_cast<const uint8_t*>(a.q.p) + at.token * a.q.stride_t +
-                           at.head * a.q.stride_h;
-        load_query<D, BF16>(q[rt], live ? p : nullptr, g, a.scale, kv.S_k[head]);
-        const int pos = it.len - all_new + (int)(at.token - first);
+        const RowAt of = row_at(first, head, group, live ? row0 + 16 * rt + n : row0);
+        load_query<D, BF16>(raw[rt], static_cast<const uint8_t*>(a.q.p) + of.token * a.q.stride_t +
+                                         of.head * a.q.stride_h, live, g);
+        const int pos = it.len - all_new + (int)(of.token - first);
         low[rt] = a.window > 0 ? pos - a.window + 1 : 0;
         lim[rt] = a.causal ? min(end, pos + 1) : end;
     }
@@ -293,43 +431,62 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
         for (int j = 0; j < NJ; ++j) o[rt][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    const LaneOffsets off = lane_offsets<D>(kv, head, n, g);
-    const int32_t* table = kv.table + (int64_t)it.slot * kv.max_pages;
-    const uint32_t units = (uint32_t)kv.page >> 4;
-    // page (clamped to a valid one) and first row of 16-token unit u; ok: the table names a page
-    const auto locate = [&](int u, bool& ok, int& row) {
-        const uint32_t col = div_gpr((uint32_t)u, plan.page_magic, plan.page_shift);
-        row = ((uint32_t)u - col * units) << 4;
-        const int page = (int)col < kv.max_pages ? table[col] : -1;
-        ok = (uint32_t)page < (uint32_t)kv.num_pages;
-        return kv.pages + (int64_t)(ok ? page : 0) * kv.page_stride;
-    };
     constexpr int kStep = 32 * kWaves;
-    HalfTile<D> now[2], next[2];
-    bool ok[2], ok_next[2];
-    const auto fetch = [&](int t, HalfTile<D> (&h)[2], bool (&good)[2]) {
+    const CopyOffsets<D> from = copy_offsets<D>(kv, head, lane);
+    const ReadOffsets at = read_offsets<D>(n, g);
+    uint8_t* ring = space + wave * kRing;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(LdsPtr)ring;
+    const int32_t* table = kv.table + (int64_t)it.slot * kv.max_pages;
+    const int32_t units = kv.page >> 4;
+    const int t0 = begin + 32 * wave;
+    const int tiles = t0 < end ? (end - t0 + kStep - 1) / kStep : 0;    // of this wave
+    // Where the wave's next 64 tiles lie, lane i the i-th: page (-1: the table names none) and first row
+    // of each half tile. One vector load of the table every 64 tiles instead of a dependent scalar
+    // load in front of every tile's copies.
+    int32_t page[2], row[2];
+    uint32_t named = 0;                                  // two bits a tile, the latest lowest
+    const auto copy = [&](int i) {
+        if ((i & 63) == 0) {
+            const int64_t t = t0 + (int64_t)(i + lane) * kStep;
+            const bool in = t < end;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int unit = in ? (int)(t >> 4) + u : 0;
+                const int col = (int)div_gpr((uint32_t)unit, plan.page_magic, plan.page_shift);
+                row[u] = (unit - col * units) << 4;
+                page[u] = in && col < kv.max_pages ? table[col] : -1;
+            }
+        }
+        const uint8_t* rec[2];
+        int r[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            int row;
-            const uint8_t* rec = locate((t >> 4) + u, good[u], row);
-            load_half<D>(h[u], rec, row, off);
+            const int pg = __builtin_amdgcn_readlane(page[u], i & 63);
+            const bool ok = (uint32_t)pg < (uint32_t)kv.num_pages;
+            named = named << 1 | (ok ? 1u : 0u);
+            rec[u] = kv.pages + (int64_t)(ok ? pg : 0) * kv.page_stride;
+            r[u] = __builtin_amdgcn_readlane(row[u], i & 63);
         }
+        copy_tile<D>(ring + i % kDepth * T::kBytes, rec[0], r[0], rec[1], r[1], from, lane);
     };
-    int t = begin + 32 * wave;
-    if (t < end) fetch(t, now, ok);
-    for (; t < end; t += kStep) {
-        const bool more = t + kStep < end;
-        if (more) fetch(t + kStep, next, ok_next);
-
+    struct Tile {
+        HalfTile<D> h[2];
+        bool ok[2];
+    };
+    for (int i = 0; i < kDepth - 1 && i < tiles; ++i) copy(i);
+    QRow<D, BF16> q[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) convert_query<D, BF16>(q[rt], raw[rt], a.scale, kv.S_k[head]);
+    const auto process = [&](int t, const Tile& x) {
         f32x4 s[RT][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint32_t scales = now[u].ks & 0x7F7F7F7Fu;
+            const uint32_t scales = x.h[u].ks & 0x7F7F7F7Fu;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) s[rt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             unroll<NS>([&](auto step) {
                 constexpr int S = decltype(step)::value;
-                const half8v k = k_operand<S>(now[u].k, scales);
+                const half8v k = k_operand<S>(x.h[u].k, scales);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     s[rt][u] = mfma(k, q[rt].hi[S], s[rt][u]);
@@ -337,7 +494,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
                 }
             });
         }
-        if (!(ok[0] && ok[1] && t >= low_all && t + 32 <= lim_all)) {
+        if (!(x.ok[0] && x.ok[1] && t >= low_all && t + 32 <= lim_all)) {
+            asm volatile("");                            // a branch, not selects in every tile
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -345,9 +503,11 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int p = t + 16 * u + 4 * g + i;
-                        if (!(ok[u] && p >= low[rt] && p < lim[rt])) s[rt][u][i] = -__builtin_inff();
+                        if (!(x.ok[u] && p >= low[rt] && p < lim[rt]))
+                            s[rt][u][i] = -__builtin_inff();
                     }
         }
+        __builtin_amdgcn_sched_barrier(0);
         Half8 hi[RT], lo[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -377,9 +537,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
                                          (_Float16)(pr[2 * i + 1] - (float)hi[rt].p[i][1])};
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         VPairs<D> vp[2];
-        pair_tokens<D>(vp[0], now[0].v, now[0].vs);
-        pair_tokens<D>(vp[1], now[1].v, now[1].vs);
+        pair_tokens<D>(vp[0], x.h[0].v, x.h[0].vs);
+        pair_tokens<D>(vp[1], x.h[1].v, x.h[1].vs);
         unroll<NJ>([&](auto tile_j) {
             constexpr int J = decltype(tile_j)::value;
             const half8v v = v_operand<D, J>(vp);
@@ -389,12 +550,23 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
                 if constexpr (!BF16) o[rt][J] = mfma(v, lo[rt].v, o[rt][J]);
             }
         });
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            now[u] = next[u];
-            ok[u] = ok_next[u];
+    };
+    // a ring of kDepth tiles a wave: tile i is processed while the next ones are copied
+    for (int i = 0; i < tiles; ++i) {
+        Tile x;
+        const int behind = min(kDepth - 1, tiles - 1 - i);   // tiles in flight after this one
+        if (behind == kDepth - 1) {
+            copy(i + kDepth - 1);                        // its place was read an iteration ago
+            wait_copies<(kDepth - 1) * T::kLoads>();
+        } else {
+            wait_copies<0>();
         }
+        x.ok[0] = (named >> (2 * behind + 1)) & 1u;
+        x.ok[1] = (named >> (2 * behind)) & 1u;
+        read_tile<D>(x.h, ring_at + i % kDepth * T::kBytes, at);
+        process(t0 + i * kStep, x);
     }
+    __syncthreads();                                     // the rings become the joined outputs
 
     // join the waves: the rows' maxima and sums, then the outputs scaled to the joint maximum
 #pragma unroll
@@ -442,12 +614,12 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
                     v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
                 }
                 const int d = (c / JC) * NJ + jc * JC + c % JC;
-                const RowAt at = row_at(first, head, group, row0 + 16 * rt + r);
-                const int64_t row = at.token * a.q_heads + at.head;
+                const RowAt of = row_at(first, head, group, row0 + 16 * rt + r);
+                const int64_t row = of.token * a.q_heads + of.head;
                 if (whole) {
                     const float z = rl > 0.0f ? S_v / rl : 0.0f;
-                    uint8_t* dst = static_cast<uint8_t*>(a.out) + at.token * a.out_stride_t +
-                                   at.head * a.out_stride_h;
+                    uint8_t* dst = static_cast<uint8_t*>(a.out) + of.token * a.out_stride_t +
+                                   of.head * a.out_stride_h;
                     if constexpr (BF16)
                         *reinterpret_cast<uint2*>(dst + 2 * d) =
                             make_uint2(bf16_pair(v.x * z, v.y * z), bf16_pair(v.z * z, v.w * z));
@@ -464,11 +636,14 @@ __global__ __launch_bounds__(kThreads) void k_kv_decode(KvAttention a, KvPlan pl
     }
 }
 
-// Joins the chunks of a row: one workgroup per (token row, query head), its waves over the chunks.
+// Joins the chunks of a row: one workgroup per (token row, query head). The chunks' factors go to LDS
+// first; then lanes of D / 4 columns, kThreads / (D / 4) chunks at a time, four loads in flight each.
 template <int D, bool BF16>
 __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan) {
-    constexpr int E = D / 64;
-    __shared__ float acc[kWaves][D];
+    constexpr int C = D / 4, P = kThreads / C;           // column lanes, chunks at a time
+    __shared__ float factor[kMaxSplits];
+    __shared__ float red[kWaves], sums[kWaves];
+    __shared__ float4 acc[P][C];
     const KvView& kv = a.kv;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x;
@@ -488,60 +663,83 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan
     const int row0 = r / plan.tile_rows * plan.tile_rows;
     const int rows = min(plan.tile_rows, min(n_new, a.max_q) * group - row0);
     const KvRange range = tile_range(a, it.len, all_new, group, row0, rows);
-    const int chunks = (range.end - range.begin + plan.chunk - 1) / plan.chunk;
+    const int chunks = min((range.end - range.begin + plan.chunk - 1) / plan.chunk, plan.splits);
     if (chunks <= 1) return;                              // already written
+    const float2* stat = part_stat(a, plan.splits, row, 0, D);
     float mm = -__builtin_inff();
-    for (int s = lane; s < chunks; s += 64) mm = fmaxf(mm, part_stat(a, plan.splits, row, s, D)->x);
+    for (int s = threadIdx.x; s < chunks; s += kThreads) mm = fmaxf(mm, stat[s].x);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
-    float l = 0.0f, v[E];
+    if (lane == 0) red[wave] = mm;
+    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.0f;
-    for (int s = wave; s < chunks; s += kWaves) {
-        const float2 st = *part_stat(a, plan.splits, row, s, D);
+    for (int k = 0; k < kWaves; ++k) mm = fmaxf(mm, red[k]);
+    float l = 0.0f;
+    for (int s = threadIdx.x; s < chunks; s += kThreads) {
+        const float2 st = stat[s];
         const float f = st.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.x - mm);
-        const float* p = part_out(a, plan.splits, row, s, D) + lane * E;
-        l += st.y * f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = __builtin_fmaf(p[e], f, v[e]);
+        factor[s] = f;
+        l = __builtin_fmaf(st.y, f, l);
     }
-    __shared__ float sums[kWaves];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[wave][lane * E + e] = v[e];
+    for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
     if (lane == 0) sums[wave] = l;
     __syncthreads();
     l = 0.0f;
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) l += sums[k];
+    const int c = threadIdx.x % C, p = threadIdx.x / C;
+    const float4* part = reinterpret_cast<const float4*>(part_out(a, plan.splits, row, 0, D)) + c;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const auto add = [&](const float4& x, float f) {
+        v.x = __builtin_fmaf(x.x, f, v.x);
+        v.y = __builtin_fmaf(x.y, f, v.y);
+        v.z = __builtin_fmaf(x.z, f, v.z);
+        v.w = __builtin_fmaf(x.w, f, v.w);
+    };
+    int s = p;
+    for (; s + 3 * P < chunks; s += 4 * P) {
+        float4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = part[(int64_t)(s + k * P) * C];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) add(x[k], factor[s + k * P]);
+    }
+    for (; s < chunks; s += P) add(part[(int64_t)s * C], factor[s]);
+    acc[p][c] = v;
+    __syncthreads();
+    if (p > 0) return;
+    v = acc[0][c];
+#pragma unroll
+    for (int k = 1; k < P; ++k) {
+        const float4 x = acc[k][c];
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
     const float z = l > 0.0f ? kv.S_v[head] / l : 0.0f;
     uint8_t* dst = static_cast<uint8_t*>(a.out) + token * a.out_stride_t + hq * a.out_stride_h;
-    for (int d = threadIdx.x; d < D / 2; d += kThreads) {
-        float x = 0.0f, y = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
-            x += acc[k][2 * d];
-            y += acc[k][2 * d + 1];
-        }
-        if constexpr (BF16) reinterpret_cast<uint32_t*>(dst)[d] = bf16_pair(x * z, y * z);
-        else reinterpret_cast<float2*>(dst)[d] = make_float2(x * z, y * z);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = row_lse(mm, l);
+    if constexpr (BF16)
+        reinterpret_cast<uint2*>(dst)[c] =
+            make_uint2(bf16_pair(v.x * z, v.y * z), bf16_pair(v.z * z, v.w * z));
+    else
+        reinterpret_cast<float4*>(dst)[c] = make_float4(v.x * z, v.y * z, v.z * z, v.w * z);
+    if (a.lse && c == 0) a.lse[row] = row_lse(mm, l);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Row tiles of 16 or 32 rows; chunks so that about 1024 workgroups (four on each compute unit) share
-// the positions.
+// Row tiles of 16 or 32 rows; chunks so that about KV_TARGET workgroups share the positions.
 KvPlan plan_of(int64_t heads, int64_t q_heads, int64_t seqs, int64_t max_q, int64_t max_kv) {
-    const int64_t rows = max_q * (q_heads / heads);
+    const int64_t rows = max_q * (q_heads / heads), step = 32 * kWaves;
     KvPlan p{};
     p.tile_rows = rows <= 16 ? 16 : 32;
     p.tiles = (int32_t)ceil_div(rows, p.tile_rows);
-    const int64_t base = seqs * heads * p.tiles;
-    const int64_t want = ceil_div(1024, base > 0 ? base : 1);
-    int64_t chunk = ceil_div(ceil_div(max_kv > 0 ? max_kv : 1, want), 32 * kWaves) * 32 * kWaves;
-    p.chunk = (int32_t)(chunk < ((int64_t)1 << 30) ? chunk : (int64_t)1 << 30);
-    p.splits = (int32_t)ceil_div(max_kv > 0 ? max_kv : 1, p.chunk);
+    const int64_t span = max_kv > 0 ? max_kv : 1;
+    int64_t base = seqs * heads * p.tiles;
+    base = base > 0 ? base : 1;
+    int64_t want = ceil_div(KV_TARGET, base);
+    want = want < kMaxSplits ? want : kMaxSplits;
+    p.chunk = (int32_t)(ceil_div(ceil_div(span, want), step) * step);
+    p.splits = (int32_t)ceil_div(span, p.chunk);
     return p;
 }
 

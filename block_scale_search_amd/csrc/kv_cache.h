@@ -85,14 +85,15 @@ __device__ __forceinline__ int64_t kv_code_bytes(const KvView& kv) {
     return (int64_t)kv.heads * kv.page * (kv.dim >> 1);
 }
 
-// Slot of item i and its length, clamped to what the table can hold; 0 for a slot outside it.
+// Slot of item i and its length, clamped to what the table can hold; 0 for a slot outside it and for a
+// cache without pages.
 struct KvItem {
     int32_t slot, len;
 };
 __device__ __forceinline__ KvItem kv_item(const KvView& kv, const KvBatch& b, int i) {
     KvItem it;
     it.slot = b.slots ? b.slots[i] : i;
-    const bool ok = (uint32_t)it.slot < (uint32_t)kv.max_slots;
+    const bool ok = (uint32_t)it.slot < (uint32_t)kv.max_slots && kv.num_pages > 0;
     it.slot = ok ? it.slot : 0;
     const int32_t cap = kv.max_pages * kv.page;
     it.len = ok ? min(max(kv.lens[it.slot], 0), cap) : 0;
