@@ -107,6 +107,8 @@ nvfp4_status check_rows(const void* p, int esz, int64_t tokens, int64_t heads, i
     return NVFP4_OK;
 }
 
+int64_t planned_q(int64_t tokens, int64_t max_q) { return max_q < tokens ? max_q : tokens; }
+
 nvfp4_status check_attention_sizes(const nvfp4_kv_cache* c, int64_t tokens, int64_t q_heads,
                                    int64_t seqs, int64_t max_q, int64_t max_kv) {
     if (tokens < 0 || seqs < 0 || seqs > 65535 || max_q < 0 || max_kv < 0 || q_heads < 1 ||
@@ -114,6 +116,8 @@ nvfp4_status check_attention_sizes(const nvfp4_kv_cache* c, int64_t tokens, int6
         return NVFP4_ERR_SHAPE;
     if (tokens >= kInt32 / q_heads || max_kv >= kInt32 || max_q >= kInt32 ||
         max_q * (q_heads / c->heads) >= (1 << 24))
+        return NVFP4_ERR_SHAPE;
+    if (!nvfp4::kv_attention_fits(c->heads, q_heads, seqs, planned_q(tokens, max_q)))
         return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }
@@ -123,8 +127,6 @@ int64_t planned_kv(const nvfp4_kv_cache* c, int64_t max_kv) {
     const int64_t cap = (int64_t)c->max_pages * c->page_size;
     return max_kv < cap ? max_kv : cap;
 }
-
-int64_t planned_q(int64_t tokens, int64_t max_q) { return max_q < tokens ? max_q : tokens; }
 
 }  // namespace
 
@@ -184,9 +186,9 @@ size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int dtype,
         !layout_ok(cache->heads, cache->head_dim, cache->page_size) || cache->max_pages < 0 ||
         check_attention_sizes(cache, tokens, q_heads, seqs, max_q, max_kv) != NVFP4_OK)
         return 0;
-    return nvfp4::kv_attention_workspace_bytes(cache->heads, cache->head_dim,
-                                               dtype == NVFP4_DTYPE_BF16, tokens, q_heads, seqs,
-                                               planned_q(tokens, max_q), planned_kv(cache, max_kv));
+    return nvfp4::kv_attention_workspace_bytes(cache->heads, cache->head_dim, tokens, q_heads,
+                                               seqs, planned_q(tokens, max_q),
+                                               planned_kv(cache, max_kv));
 }
 
 nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, int64_t layer, const void* Q, int dtype,
@@ -234,8 +236,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, int64_t layer, cons
     a.out_stride_h = stride_oh * esz;
     a.lse = lse;
     a.workspace = workspace;
-    const size_t need = nvfp4::kv_attention_workspace_bytes(cache->heads, D, a.bf16, tokens, q_heads,
-                                                            seqs, a.max_q, a.max_kv);
+    const size_t need = nvfp4::kv_attention_workspace_bytes(cache->heads, D, tokens, q_heads, seqs,
+                                                            a.max_q, a.max_kv);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
     return hip_status(nvfp4::launch_kv_attention(a, static_cast<hipStream_t>(stream)));

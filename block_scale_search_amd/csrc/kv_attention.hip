@@ -23,14 +23,17 @@ namespace nvfp4 {
 namespace {
 
 #ifndef KV_TARGET
-#define KV_TARGET 2048
+#define KV_TARGET 1024
+#endif
+#ifndef KV_FULL
+#define KV_FULL 4096
 #endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 #ifndef KV_DEPTH
 #define KV_DEPTH 2
 #endif
-constexpr int kMaxSplits = 512;      // chunks of a row
+constexpr int kMaxSplits = 1024;     // chunks of a row
 constexpr int kDepth = KV_DEPTH;     // tiles of a wave in LDS
 constexpr float kUp = 8.0f;          // log2 of the weights' scale
 constexpr float kSlack = 7.0f;       // how far a logit may exceed the maximum in use, log2
@@ -343,17 +346,6 @@ __device__ __forceinline__ RowAt row_at(int64_t first, int head, int group, int 
     return RowAt{first + j, head * group + row - j * group};
 }
 
-// Workspace of split sequences: O (binary32, scaled like the weights) of every row and chunk, then
-// (maximum, sum) of every row and chunk.
-__device__ __forceinline__ float* part_out(const KvAttention& a, int splits, int64_t row, int s, int D) {
-    return static_cast<float*>(a.workspace) + (row * splits + s) * D;
-}
-__device__ __forceinline__ float2* part_stat(const KvAttention& a, int splits, int64_t row, int s,
-                                             int D) {
-    float* end = static_cast<float*>(a.workspace) + a.b.tokens * a.q_heads * (int64_t)splits * D;
-    return reinterpret_cast<float2*>(end) + row * splits + s;
-}
-
 // lse of a row from its maximum (log2, the weights' scale of 2^kUp apart) and sum.
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l > 0.0f ? (m - kUp + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
@@ -378,27 +370,18 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const KvView& kv = a.kv;
 
-    // work of this workgroup: head fastest, then item, row tile, chunk
-    uint32_t w = blockIdx.x;
-    const int head = w % (uint32_t)kv.heads;
-    w /= (uint32_t)kv.heads;
-    const int item = w % (uint32_t)a.b.seqs;
-    w /= (uint32_t)a.b.seqs;
-    const int tile = w % (uint32_t)plan.tiles, split = w / (uint32_t)plan.tiles;
+    // work of this workgroup: head fastest
+    const int task = (int)(blockIdx.x / (uint32_t)kv.heads);
+    const int head = (int)(blockIdx.x - (uint32_t)task * (uint32_t)kv.heads);
     const int group = a.q_heads / kv.heads;
-    const int64_t total = min((int64_t)a.b.cu[a.b.seqs], a.b.tokens);
-    const int64_t first = a.b.cu[item];
-    const int n_new = (int)min((int64_t)a.b.cu[item + 1], total) - (int)first;
-    const int all_new = a.b.cu[item + 1] - (int)first;
-    const int row0 = tile * R;
-    const int rows = min(R, min(n_new, a.max_q) * group - row0);
-    if (first < 0 || rows <= 0) return;
-    const KvItem it = kv_item(kv, a.b, item);
-    const KvRange range = tile_range(a, it.len, all_new, group, row0, rows);
-    const int chunks = (range.end - range.begin + plan.chunk - 1) / plan.chunk;
-    if (split > 0 && split >= chunks) return;
-    const int begin = range.begin + split * plan.chunk;
-    const int end = min(range.end, begin + plan.chunk);
+    KvTask job;
+    if (!find_task(a, plan, task, job)) return;
+    const int64_t first = job.work.first;
+    const int all_new = job.work.all_new, row0 = job.row0, rows = job.rows;
+    const int begin = job.begin, end = job.end;
+    const bool whole = job.chunks <= 1;
+    if (plan.target > 0 && head == 0 && job.chunk == 0 && job.tile == 0 && threadIdx.x == 0)
+        item_info(a)[job.item] = make_int2(job.base, job.chunks);
 
     RawQuery<D, BF16> raw[RT];
     int low[RT], lim[RT];                                // the lane's row sees low .. lim - 1
@@ -409,13 +392,13 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
         const RowAt of = row_at(first, head, group, live ? row0 + 16 * rt + n : row0);
         load_query<D, BF16>(raw[rt], static_cast<const uint8_t*>(a.q.p) + of.token * a.q.stride_t +
                                          of.head * a.q.stride_h, live, g);
-        const int pos = it.len - all_new + (int)(of.token - first);
+        const int pos = job.work.len - all_new + (int)(of.token - first);
         low[rt] = a.window > 0 ? pos - a.window + 1 : 0;
         lim[rt] = a.causal ? min(end, pos + 1) : end;
     }
     {
-        const int p0 = it.len - all_new + row0 / group;
-        const int p1 = it.len - all_new + (row0 + rows - 1) / group;
+        const int p0 = job.work.len - all_new + row0 / group;
+        const int p1 = job.work.len - all_new + (row0 + rows - 1) / group;
         if (a.causal) lim_all = min(end, p0 + 1);
         if (a.window > 0) low_all = p1 - a.window + 1;
     }
@@ -436,7 +419,7 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
     const ReadOffsets at = read_offsets<D>(n, g);
     uint8_t* ring = space + wave * kRing;
     const uint32_t ring_at = (uint32_t)(uintptr_t)(LdsPtr)ring;
-    const int32_t* table = kv.table + (int64_t)it.slot * kv.max_pages;
+    const int32_t* table = kv.table + (int64_t)job.work.slot * kv.max_pages;
     const int32_t units = kv.page >> 4;
     const int t0 = begin + 32 * wave;
     const int tiles = t0 < end ? (end - t0 + kStep - 1) / kStep : 0;    // of this wave
@@ -576,7 +559,6 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
     }
     __syncthreads();
     const float S_v = kv.S_v[head];
-    const bool whole = chunks <= 1;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         float mm = -__builtin_inff();
@@ -615,8 +597,8 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
                 }
                 const int d = (c / JC) * NJ + jc * JC + c % JC;
                 const RowAt of = row_at(first, head, group, row0 + 16 * rt + r);
-                const int64_t row = of.token * a.q_heads + of.head;
                 if (whole) {
+                    const int64_t row = of.token * a.q_heads + of.head;
                     const float z = rl > 0.0f ? S_v / rl : 0.0f;
                     uint8_t* dst = static_cast<uint8_t*>(a.out) + of.token * a.out_stride_t +
                                    of.head * a.out_stride_h;
@@ -628,8 +610,8 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
                             make_float4(v.x * z, v.y * z, v.z * z, v.w * z);
                     if (a.lse && d == 0) a.lse[row] = row_lse(rm, rl);
                 } else {
-                    *reinterpret_cast<float4*>(part_out(a, plan.splits, row, split, D) + d) = v;
-                    if (d == 0) *part_stat(a, plan.splits, row, split, D) = make_float2(rm, rl);
+                    *reinterpret_cast<float4*>(part_out(a, plan, task, head) + (16 * rt + r) * D + d) = v;
+                    if (d == 0) part_stat(a, plan, task, head)[16 * rt + r] = make_float2(rm, rl);
                 }
             }
         }
@@ -646,28 +628,45 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan
     __shared__ float4 acc[P][C];
     const KvView& kv = a.kv;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x;
-    const int64_t token = row / a.q_heads;
-    const int hq = (int)(row - token * a.q_heads);
+    const int64_t at = blockIdx.x / (uint32_t)a.q_heads;
+    const int hq = (int)(blockIdx.x - (uint32_t)at * (uint32_t)a.q_heads);
     const int group = a.q_heads / kv.heads, head = hq / group;
     const int64_t total = min((int64_t)a.b.cu[a.b.seqs], a.b.tokens);
-    if (token >= total) return;
-    const int item = kv_find_item(a.b.cu, a.b.seqs, token);
+    int item;
+    int64_t j;
+    if (plan.by_item) {
+        item = (int)(at / a.max_q);
+        j = at - (int64_t)item * a.max_q;
+    } else {
+        if (at >= total) return;
+        item = kv_find_item(a.b.cu, a.b.seqs, at);
+        j = at - a.b.cu[item];
+    }
+    const int2 info = item_info(a)[item];
     const int64_t first = a.b.cu[item];
-    const int64_t j = token - first;
-    if (j < 0 || j >= a.max_q) return;
-    const int all_new = a.b.cu[item + 1] - (int)first;
     const int n_new = (int)min((int64_t)a.b.cu[item + 1], total) - (int)first;
-    const KvItem it = kv_item(kv, a.b, item);
+    if (first < 0 || j < 0 || j >= min(n_new, a.max_q)) return;
+    const int64_t token = first + j, row = token * a.q_heads + hq;
     const int r = (int)j * group + hq - head * group;
-    const int row0 = r / plan.tile_rows * plan.tile_rows;
-    const int rows = min(plan.tile_rows, min(n_new, a.max_q) * group - row0);
-    const KvRange range = tile_range(a, it.len, all_new, group, row0, rows);
-    const int chunks = min((range.end - range.begin + plan.chunk - 1) / plan.chunk, plan.splits);
+    const int tile = r / plan.tile_rows, r_in = r - tile * plan.tile_rows;
+    const int rows = min(n_new, a.max_q) * group;
+    const int tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
+    // chunk s of this row's tile: task info.x + s * tiles + (tiles - 1 - tile)
+    const int task0 = info.x + tiles - 1 - tile;
+    const int chunks = min(min(info.y, kMaxSplits), (plan.tasks - task0 + tiles - 1) / tiles);
     if (chunks <= 1) return;                              // already written
-    const float2* stat = part_stat(a, plan.splits, row, 0, D);
+    const int64_t stat_step = (int64_t)tiles * kv.heads * plan.tile_rows;
+    const float2* stat = part_stat(a, plan, task0, head) + r_in;
+    // the first chunks' outputs are on their way while the factors are made
+    const int c = threadIdx.x % C, p = threadIdx.x / C;
+    const float4* part = reinterpret_cast<const float4*>(part_out(a, plan, task0, head) + r_in * D) + c;
+    const int64_t step = stat_step * C;
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        x[k] = p + k * P < chunks ? part[(p + k * P) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float mm = -__builtin_inff();
-    for (int s = threadIdx.x; s < chunks; s += kThreads) mm = fmaxf(mm, stat[s].x);
+    for (int s = threadIdx.x; s < chunks; s += kThreads) mm = fmaxf(mm, stat[s * stat_step].x);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
     if (lane == 0) red[wave] = mm;
@@ -676,7 +675,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan
     for (int k = 0; k < kWaves; ++k) mm = fmaxf(mm, red[k]);
     float l = 0.0f;
     for (int s = threadIdx.x; s < chunks; s += kThreads) {
-        const float2 st = stat[s];
+        const float2 st = stat[s * stat_step];
         const float f = st.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.x - mm);
         factor[s] = f;
         l = __builtin_fmaf(st.y, f, l);
@@ -688,32 +687,30 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan
     l = 0.0f;
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) l += sums[k];
-    const int c = threadIdx.x % C, p = threadIdx.x / C;
-    const float4* part = reinterpret_cast<const float4*>(part_out(a, plan.splits, row, 0, D)) + c;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const auto add = [&](const float4& x, float f) {
-        v.x = __builtin_fmaf(x.x, f, v.x);
-        v.y = __builtin_fmaf(x.y, f, v.y);
-        v.z = __builtin_fmaf(x.z, f, v.z);
-        v.w = __builtin_fmaf(x.w, f, v.w);
-    };
-    int s = p;
-    for (; s + 3 * P < chunks; s += 4 * P) {
-        float4 x[4];
+    for (int s = p; s < chunks; s += 4 * P) {
+        if (s > p) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = part[(int64_t)(s + k * P) * C];
+            for (int k = 0; k < 4; ++k)
+                x[k] = s + k * P < chunks ? part[(s + k * P) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add(x[k], factor[s + k * P]);
+        for (int k = 0; k < 4; ++k) {
+            const float f = s + k * P < chunks ? factor[s + k * P] : 0.0f;
+            v.x = __builtin_fmaf(x[k].x, f, v.x);
+            v.y = __builtin_fmaf(x[k].y, f, v.y);
+            v.z = __builtin_fmaf(x[k].z, f, v.z);
+            v.w = __builtin_fmaf(x[k].w, f, v.w);
+        }
     }
-    for (; s < chunks; s += P) add(part[(int64_t)s * C], factor[s]);
     acc[p][c] = v;
     __syncthreads();
     if (p > 0) return;
     v = acc[0][c];
 #pragma unroll
     for (int k = 1; k < P; ++k) {
-        const float4 x = acc[k][c];
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        const float4 y = acc[k][c];
+        v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
     }
     const float z = l > 0.0f ? kv.S_v[head] / l : 0.0f;
     uint8_t* dst = static_cast<uint8_t*>(a.out) + token * a.out_stride_t + hq * a.out_stride_h;
@@ -727,33 +724,52 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Row tiles of 16 or 32 rows; chunks so that about KV_TARGET workgroups share the positions.
-KvPlan plan_of(int64_t heads, int64_t q_heads, int64_t seqs, int64_t max_q, int64_t max_kv) {
-    const int64_t rows = max_q * (q_heads / heads), step = 32 * kWaves;
+// Row tiles of 16 or 32 rows; a batch that does not fill the chip by its tiles alone is split.
+// span: the most positions a row tile sees.
+KvPlan plan_of(int64_t heads, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,
+               int64_t span) {
+    const int64_t group = q_heads / heads, rows = max_q * group;
     KvPlan p{};
     p.tile_rows = rows <= 16 ? 16 : 32;
     p.tiles = (int32_t)ceil_div(rows, p.tile_rows);
-    const int64_t span = max_kv > 0 ? max_kv : 1;
-    int64_t base = seqs * heads * p.tiles;
-    base = base > 0 ? base : 1;
-    int64_t want = ceil_div(KV_TARGET, base);
-    want = want < kMaxSplits ? want : kMaxSplits;
-    p.chunk = (int32_t)(ceil_div(ceil_div(span, want), step) * step);
-    p.splits = (int32_t)ceil_div(span, p.chunk);
+    p.tiles = p.tiles > 0 ? p.tiles : 1;
+    int64_t most = seqs * p.tiles;                       // tiles of all items, a head
+    const int64_t by_rows = seqs + ceil_div(tokens * group, p.tile_rows);
+    if (seqs <= kMaxScan) {
+        most = most < by_rows ? most : by_rows;
+        if (most * heads < KV_FULL && span > kUnit) {
+            const int64_t target = ceil_div(KV_TARGET, heads);
+            p.target = (int32_t)(target < kMaxSplits ? target : kMaxSplits);
+        }
+    }
+    if (p.target > 0) {
+        // no tile has more chunks than units
+        const int64_t units = ceil_div(span, kUnit);
+        p.tasks = (int32_t)(most + p.target < most * units ? most + p.target : most * units);
+        p.by_item = seqs * max_q <= 2 * tokens;
+    } else {
+        p.tasks = (int32_t)(seqs * p.tiles);
+    }
     return p;
+}
+
+size_t space_of(const KvPlan& p, int64_t heads, int64_t dim, int64_t seqs) {
+    if (p.target == 0) return 0;
+    return (size_t)((seqs + 1) / 2 * 2) * 8 +
+           (size_t)p.tasks * (size_t)heads * (size_t)p.tile_rows * (size_t)(8 + 4 * dim);
 }
 
 template <int D, bool BF16>
 hipError_t launch(const KvAttention& a, const KvPlan& p, hipStream_t stream) {
-    const int64_t blocks = (int64_t)a.kv.heads * a.b.seqs * p.tiles * p.splits;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    const dim3 grid((uint32_t)blocks);
+    const dim3 grid((uint32_t)((int64_t)a.kv.heads * p.tasks));
     if (p.tile_rows == 16)
         hipLaunchKernelGGL((k_kv_decode<D, BF16, 1>), grid, dim3(kThreads), 0, stream, a, p);
     else
         hipLaunchKernelGGL((k_kv_decode<D, BF16, 2>), grid, dim3(kThreads), 0, stream, a, p);
-    if (p.splits > 1)
-        hipLaunchKernelGGL((k_kv_join<D, BF16>), dim3((uint32_t)(a.b.tokens * a.q_heads)),
+    if (p.target > 0)
+        hipLaunchKernelGGL((k_kv_join<D, BF16>),
+                           dim3((uint32_t)((p.by_item ? (int64_t)a.b.seqs * a.max_q : a.b.tokens) *
+                                           a.q_heads)),
                            dim3(kThreads), 0, stream, a, p);
     return hipGetLastError();
 }
@@ -767,16 +783,21 @@ hipError_t launch_dim(const KvAttention& a, const KvPlan& p, hipStream_t stream)
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int64_t heads, int64_t dim, bool bf16, int64_t tokens,
-                                    int64_t q_heads, int64_t seqs, int64_t max_q, int64_t max_kv) {
-    (void)bf16;
-    const KvPlan p = plan_of(heads, q_heads, seqs, max_q, max_kv);
-    if (p.splits <= 1) return 0;
-    return (size_t)(tokens * q_heads * (int64_t)p.splits) * (dim * 4 + 8);
+bool kv_attention_fits(int64_t heads, int64_t q_heads, int64_t seqs, int64_t max_q) {
+    const int64_t tiles = ceil_div(max_q * (q_heads / heads), 16);
+    return seqs * (tiles > 0 ? tiles : 1) + kMaxSplits < ((int64_t)1 << 31) / heads;
+}
+
+size_t kv_attention_workspace_bytes(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads,
+                                    int64_t seqs, int64_t max_q, int64_t max_kv) {
+    return space_of(plan_of(heads, tokens, q_heads, seqs, max_q, max_kv), heads, dim, seqs);
 }
 
 hipError_t launch_kv_attention(const KvAttention& a, hipStream_t stream) {
-    KvPlan p = plan_of(a.kv.heads, a.q_heads, a.b.seqs, a.max_q, a.max_kv);
+    // a window bounds what a tile sees; the workspace is sized without it and so never too small
+    int64_t span = a.max_kv;
+    if (a.window > 0 && (int64_t)a.window + a.max_q + 31 < span) span = (int64_t)a.window + a.max_q + 31;
+    KvPlan p = plan_of(a.kv.heads, a.b.tokens, a.q_heads, a.b.seqs, a.max_q, span);
     gpr_divisor(a.kv.page / 16, p.page_magic, p.page_shift);
     return a.bf16 ? launch_dim<true>(a, p, stream) : launch_dim<false>(a, p, stream);
 }

@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_formats.h"
 #include "kv_cache.h"
 
@@ -83,13 +85,22 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return r(a) | (r(b) << 16);
 }
 
-// Work split: the (item, head) pairs' query rows in tiles, the visible positions of a tile in chunks.
-// Rows of an item and head: (token j, query head of the group), row = j * group + head.
+// Work split. Rows of an item and head: (token j, query head of the group), row = j * group + head,
+// in tiles; the positions a tile sees in chunks. Lengths are known on the device only, and in a batch
+// they differ widely, so each workgroup finds its task itself: a wave sums the positions of all
+// tiles, which gives the chunk size that makes about `target` tasks a head, and then finds its
+// own in the prefix sum of the items' tasks. (A grid made for the longest item left most workgroups
+// without work and the others unevenly spread: 4 sequences of up to 131072 positions took 81 us
+// that way and 57 us so.)
+constexpr int kUnit = 128;       // positions by which chunks are cut
+constexpr int kMaxScan = 1024;   // items up to which a task is found by scanning them
+
 struct KvPlan {
     int32_t tile_rows;       // query rows of a workgroup
     int32_t tiles;           // row tiles of the largest item
-    int32_t splits;          // chunks of the largest span
-    int32_t chunk;           // positions of a chunk, a multiple of 32
+    int32_t target;          // tasks a head aimed at; 0: no splitting, task = item * tiles + tile
+    int32_t tasks;           // tasks a head at most
+    int32_t by_item;         // join: workgroups by (item, row of max_q) instead of by token row
     uint64_t page_magic;     // division of a 16-token unit by the units of a page
     uint32_t page_shift;
 };
@@ -109,6 +120,145 @@ __device__ __forceinline__ KvRange tile_range(const KvAttention& a, int len, int
     if (a.window > 0) r.begin = max(0, first - a.window + 1) & ~31;
     r.end = max(r.end, r.begin);
     return r;
+}
+
+__device__ __forceinline__ int units_of(const KvRange& r) {
+    return (int)(((int64_t)r.end - r.begin + kUnit - 1) / kUnit);
+}
+
+// An item as the kernels use it: its first row and its rows (all of them, and those that exist and are
+// asked for), query rows, slot and length.
+struct KvWork {
+    int32_t first, all_new, rows, slot, len;
+};
+
+__device__ __forceinline__ KvWork work_of(const KvAttention& a, int i, int group) {
+    KvWork w{0, 0, 0, 0, 0};
+    if (i >= a.b.seqs) return w;
+    const int32_t total = (int32_t)min((int64_t)a.b.cu[a.b.seqs], a.b.tokens);
+    const int32_t next = a.b.cu[i + 1];
+    w.first = a.b.cu[i];
+    w.all_new = next - w.first;
+    const KvItem it = kv_item(a.kv, a.b, i);
+    w.slot = it.slot;
+    w.len = it.len;
+    w.rows = w.first < 0 ? 0 : max(0, min(min(next, total) - w.first, a.max_q)) * group;
+    return w;
+}
+
+// Inclusive prefix sum over the wave's lanes by lane shifts inside rows of 16, then across them.
+template <typename T>
+__device__ __forceinline__ T wave_prefix(T v) {
+    static_assert(sizeof(T) == 4, "one register");
+    const auto shifted = [](T x, auto control, auto rows) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(
+            0, __builtin_bit_cast(int, x), decltype(control)::value, decltype(rows)::value, 0xF, false));
+    };
+    using I = std::integral_constant<int, 0xF>;
+    v += shifted(v, std::integral_constant<int, 0x111>{}, I{});     // row_shr:1
+    v += shifted(v, std::integral_constant<int, 0x112>{}, I{});
+    v += shifted(v, std::integral_constant<int, 0x114>{}, I{});
+    v += shifted(v, std::integral_constant<int, 0x118>{}, I{});
+    v += shifted(v, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row_bcast:15
+    v += shifted(v, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // row_bcast:31
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ T last_lane(T v) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+struct KvTask {
+    KvWork work;
+    int32_t item, tile, chunk, chunks;
+    int32_t base;            // the item's first task
+    int32_t row0, rows;      // of the tile
+    int32_t begin, end;      // positions of the chunk
+};
+
+// The task of number w (uniform), found by the whole wave; false if there is none.
+__device__ __forceinline__ bool find_task(const KvAttention& a, const KvPlan& p, int w, KvTask& t) {
+    const int lane = threadIdx.x & 63;
+    const int group = a.q_heads / a.kv.heads;
+    KvWork mine;
+    int inside;
+    if (p.target == 0) {
+        t.item = w / p.tiles;
+        mine = work_of(a, t.item, group);
+        t.work = mine;
+        inside = w - t.item * p.tiles;
+        t.base = t.item * p.tiles;
+        t.chunks = 1;
+    } else {
+        float sum = 0.0f;
+        int units = 0, tiles = 0;
+        for (int i0 = 0; i0 < a.b.seqs; i0 += 64) {
+            mine = work_of(a, i0 + lane, group);
+            tiles = (mine.rows + p.tile_rows - 1) / p.tile_rows;
+            units = mine.rows > 0 ? units_of(tile_range(a, mine.len, mine.all_new, group, 0, mine.rows)) : 0;
+            sum += (float)units * (float)tiles;
+        }
+        // units a chunk: above sum / target whatever binary32 rounded, so that no item has more than
+        // `target` chunks and all have at most `target` more than their tiles
+        const float share = last_lane(wave_prefix(sum)) / (float)p.target;
+        const int chunk = (int)min(share * 1.001f, 1e9f) + 1;
+        int before = 0;
+        bool found = false;
+        for (int i0 = 0; i0 < a.b.seqs && !found; i0 += 64) {
+            if (a.b.seqs > 64) {
+                mine = work_of(a, i0 + lane, group);
+                tiles = (mine.rows + p.tile_rows - 1) / p.tile_rows;
+                units = mine.rows > 0 ? units_of(tile_range(a, mine.len, mine.all_new, group, 0, mine.rows)) : 0;
+            }
+            const int chunks = max(1, (int)(((int64_t)units + chunk - 1) / chunk));
+            const int tasks = tiles * chunks;
+            const int incl = wave_prefix(tasks);
+            const uint64_t past = __ballot(before + incl > w);
+            if (past != 0) {
+                const int src = __builtin_ctzll(past);
+                found = true;
+                t.item = i0 + src;
+                t.base = before + __builtin_amdgcn_readlane(incl - tasks, src);
+                t.chunks = __builtin_amdgcn_readlane(chunks, src);
+                t.work.first = __builtin_amdgcn_readlane(mine.first, src);
+                t.work.all_new = __builtin_amdgcn_readlane(mine.all_new, src);
+                t.work.rows = __builtin_amdgcn_readlane(mine.rows, src);
+                t.work.slot = __builtin_amdgcn_readlane(mine.slot, src);
+                t.work.len = __builtin_amdgcn_readlane(mine.len, src);
+            }
+            before += last_lane(incl);
+        }
+        if (!found) return false;
+        inside = w - t.base;
+    }
+    // the last tile of a causal item sees the most: it comes first
+    const int tiles = (t.work.rows + p.tile_rows - 1) / p.tile_rows;
+    t.chunk = tiles > 0 ? inside / tiles : 0;
+    t.tile = tiles - 1 - (inside - t.chunk * tiles);
+    if (t.tile < 0 || t.chunk >= t.chunks) return false;
+    t.row0 = t.tile * p.tile_rows;
+    t.rows = min(p.tile_rows, t.work.rows - t.row0);
+    const KvRange r = tile_range(a, t.work.len, t.work.all_new, group, t.row0, t.rows);
+    const int64_t units = units_of(r);
+    t.begin = r.begin + (int)(units * t.chunk / t.chunks) * kUnit;
+    t.end = t.chunk + 1 == t.chunks ? r.end
+                                    : min(r.end, r.begin + (int)(units * (t.chunk + 1) / t.chunks) * kUnit);
+    return true;
+}
+
+// Workspace of a split batch: (first task, chunks) of every item; then for every task and head the tile's
+// (maximum, sum) of each row, and its outputs (binary32, scaled like the weights).
+__device__ __forceinline__ int2* item_info(const KvAttention& a) {
+    return static_cast<int2*>(a.workspace);
+}
+__device__ __forceinline__ float2* part_stat(const KvAttention& a, const KvPlan& p, int task, int head) {
+    return reinterpret_cast<float2*>(static_cast<int2*>(a.workspace) + (a.b.seqs + 1) / 2 * 2) +
+           ((int64_t)task * a.kv.heads + head) * p.tile_rows;
+}
+__device__ __forceinline__ float* part_out(const KvAttention& a, const KvPlan& p, int task, int head) {
+    float* out = reinterpret_cast<float*>(part_stat(a, p, p.tasks, 0));
+    return out + ((int64_t)task * a.kv.heads + head) * p.tile_rows * a.kv.dim;
 }
 
 }  // namespace nvfp4

@@ -466,6 +466,7 @@ class KVCache:
         self.S_k, self.S_v = S_k, S_v
         self.heads, self.head_dim, self.page_size = heads, head_dim, page_size
         self.layers, self.num_pages, self.device = layers, num_pages, pages.device
+        self.index = pages.get_device()
         self.struct = KVCacheStruct(
             p(pages, "pages", (torch.uint8,)), layers, pages.stride(0), num_pages, pages.stride(1),
             heads, head_dim, page_size, table.shape[1], table.shape[0], p(table, "table", i32),
@@ -484,131 +485,129 @@ class KVCache:
                    torch.zeros(num_pages, **i32), S_k, S_v, heads, head_dim, page_size)
 
 
-class _on:
-    """Makes a cache's device current for a call (the launches go to that device's stream)."""
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.old = torch.cuda.current_device()
-        if self.index != self.old:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.index != self.old:
-            torch.cuda.set_device(self.old)
-
-
 def _kv_run(cache: KVCache, fname: str, args: tuple, stream, prepare: bool):
-    for t in args:
-        if isinstance(t, torch.Tensor) and t.device != cache.device:
-            raise ValueError(f"{fname}: every tensor must be on the cache's device {cache.device}")
-    s = torch.cuda.current_stream(cache.device) if stream is None else stream
-    args = (cache.ref, *[t.data_ptr() if isinstance(t, torch.Tensor) else t for t in args],
-            s.cuda_stream)
+    """Calls a cache entry point with pointers and numbers in `args`, on `stream` (None: the current
+    stream of the cache's device), with that device current."""
+    index = cache.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     f = getattr(_lib, fname)
 
     def call():
-        with _on(cache.device):
-            _check(f(*args), fname)
+        old = torch._C._cuda_getDevice()
+        if old == index:
+            return _check(f(cache.ref, *args, s), fname)
+        torch.cuda.set_device(index)
+        try:
+            _check(f(cache.ref, *args, s), fname)
+        finally:
+            torch.cuda.set_device(old)
     return call if prepare else call()
 
 
-def _i32(t, numel: int, name: str):
+def _kv_ptr(cache: KVCache, t, name: str, dtype=None, numel: int | None = None):
+    """Address of a tensor on the cache's device, of this dtype and (contiguous) at least numel elements."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
-        raise TypeError(f"{name} must be an int32 tensor on the GPU")
-    _need(t, numel, name)
-    return t
-
-
-def _kv_rows(t, heads, dim, name):
-    """A token tensor [tokens, heads, dim] with contiguous rows; its token and head strides."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a tensor on the GPU")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}] with contiguous rows")
-    return t.stride(0), t.stride(1)
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} must be on the cache's device {cache.device}")
+    if numel is not None:
+        _need(t, numel, name)
+    return t.data_ptr()
+
+
+def _kv_rows(cache: KVCache, t, heads, dtype, name):
+    """A token tensor [tokens, heads, head_dim] with contiguous rows: address, token and head strides."""
+    p = _kv_ptr(cache, t, name, dtype)
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, {heads}, {cache.head_dim}] with contiguous rows")
+    return p, t.stride(0), t.stride(1)
 
 
 def nvfp4_kv_append(cache: KVCache, layer, K, V, cu_tokens, slots, seqs, lo, hi, stream=None,
                     prepare=False):
-    skt, skh = _kv_rows(K, cache.heads, cache.head_dim, "K")
-    svt, svh = _kv_rows(V, cache.heads, cache.head_dim, "V")
-    if V.shape != K.shape or V.dtype != K.dtype:
-        raise ValueError("K and V must have the same shape and element type")
+    k, skt, skh = _kv_rows(cache, K, cache.heads, None, "K")
+    v, svt, svh = _kv_rows(cache, V, cache.heads, K.dtype, "V")
+    if V.shape[0] != K.shape[0]:
+        raise ValueError("K and V must have the same shape")
     return _kv_run(cache, "nvfp4_kv_append", (
-        layer, K, V, _wdtype(K), K.shape[0], skt, skh, svt, svh,
-        _i32(cu_tokens, seqs + 1, "cu_tokens"), _i32(slots, seqs, "slots"), seqs, lo, hi),
-        stream, prepare)
+        layer, k, v, _wdtype(K), K.shape[0], skt, skh, svt, svh,
+        _kv_ptr(cache, cu_tokens, "cu_tokens", torch.int32, seqs + 1),
+        _kv_ptr(cache, slots, "slots", torch.int32, seqs), seqs, lo, hi), stream, prepare)
 
 
 def nvfp4_kv_read(cache: KVCache, layer, K, V, tokens, cu_tokens, slots, seqs, stream=None,
                   prepare=False):
-    for name, t in (("K", K), ("V", V)):
-        _kv_rows(t, cache.heads, cache.head_dim, name)
-        _need(t, tokens * cache.heads * cache.head_dim, name)
-    if V.dtype != K.dtype:
-        raise ValueError("K and V must have the same element type")
+    numel = tokens * cache.heads * cache.head_dim
     return _kv_run(cache, "nvfp4_kv_read", (
-        layer, K, V, _wdtype(K), tokens, _i32(cu_tokens, seqs + 1, "cu_tokens"),
-        _i32(slots, seqs, "slots"), seqs), stream, prepare)
+        layer, _kv_ptr(cache, K, "K", None, numel), _kv_ptr(cache, V, "V", K.dtype, numel),
+        _wdtype(K), tokens, _kv_ptr(cache, cu_tokens, "cu_tokens", torch.int32, seqs + 1),
+        _kv_ptr(cache, slots, "slots", torch.int32, seqs), seqs), stream, prepare)
 
 
 def nvfp4_kv_attention_workspace_size(cache: KVCache, dtype, tokens, q_heads, seqs, max_q,
                                       max_kv) -> int:
     """dtype: torch.bfloat16 or torch.float32."""
     dt = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
-    return int(_lib.nvfp4_kv_attention_workspace_size(cache.ref, dt, tokens, q_heads, seqs, max_q,
-                                                      max_kv))
+    return _lib.nvfp4_kv_attention_workspace_size(cache.ref, dt, tokens, q_heads, seqs, max_q, max_kv)
 
 
 def nvfp4_kv_attention(cache: KVCache, layer, Q, cu_tokens, slots, seqs, max_q, max_kv, scale,
                        causal, window, O, lse, workspace, stream=None, prepare=False):
     q_heads = Q.shape[1] if Q.dim() == 3 else 0
-    sqt, sqh = _kv_rows(Q, q_heads, cache.head_dim, "Q")
-    sot, soh = _kv_rows(O, q_heads, cache.head_dim, "O")
-    if O.shape != Q.shape or O.dtype != Q.dtype:
-        raise ValueError("O and Q must have the same shape and element type")
-    if lse is not None:
-        if lse.dtype != torch.float32:
-            raise TypeError("lse must be float32")
-        _need(lse, Q.shape[0] * q_heads, "lse")
+    q, sqt, sqh = _kv_rows(cache, Q, q_heads, None, "Q")
+    o, sot, soh = _kv_rows(cache, O, q_heads, Q.dtype, "O")
+    tokens = Q.shape[0]
+    if O.shape[0] != tokens:
+        raise ValueError("O and Q must have the same shape")
     return _kv_run(cache, "nvfp4_kv_attention", (
-        layer, Q, _wdtype(Q), Q.shape[0], q_heads, sqt, sqh,
-        _i32(cu_tokens, seqs + 1, "cu_tokens"), _i32(slots, seqs, "slots"), seqs, max_q, max_kv,
-        scale, int(causal), window, O, sot, soh, lse, workspace,
-        0 if workspace is None else workspace.numel() * workspace.element_size()), stream, prepare)
+        layer, q, _wdtype(Q), tokens, q_heads, sqt, sqh,
+        _kv_ptr(cache, cu_tokens, "cu_tokens", torch.int32, seqs + 1),
+        _kv_ptr(cache, slots, "slots", torch.int32, seqs), seqs, max_q, max_kv, scale, int(causal),
+        window, o, sot, soh, _kv_ptr(cache, lse, "lse", torch.float32, tokens * q_heads),
+        *_kv_space(cache, workspace)), stream, prepare)
+
+
+def _kv_space(cache: KVCache, t):
+    """Address and bytes of a workspace tensor."""
+    if t is None:
+        return None, 0
+    return _kv_ptr(cache, t, "workspace", None, 0), t.numel() * t.element_size()
 
 
 def nvfp4_kv_pages_workspace_size(cache: KVCache, n: int) -> int:
-    return int(_lib.nvfp4_kv_pages_workspace_size(cache.ref, n))
+    return _lib.nvfp4_kv_pages_workspace_size(cache.ref, n)
 
 
 def nvfp4_kv_reserve(cache: KVCache, slots, counts, n, status, workspace, stream=None, prepare=False):
+    i32 = torch.int32
     return _kv_run(cache, "nvfp4_kv_reserve", (
-        _i32(slots, n, "slots"), _i32(counts, n, "counts"), n, _i32(status, 1, "status"), workspace,
-        workspace.numel() * workspace.element_size()), stream, prepare)
+        _kv_ptr(cache, slots, "slots", i32, n), _kv_ptr(cache, counts, "counts", i32, n), n,
+        _kv_ptr(cache, status, "status", i32, 1), *_kv_space(cache, workspace)), stream, prepare)
 
 
 def nvfp4_kv_fork(cache: KVCache, parents, children, n, status, workspace, stream=None,
                   prepare=False):
+    i32 = torch.int32
     return _kv_run(cache, "nvfp4_kv_fork", (
-        _i32(parents, n, "parents"), _i32(children, n, "children"), n, _i32(status, 1, "status"),
-        workspace, workspace.numel() * workspace.element_size()), stream, prepare)
+        _kv_ptr(cache, parents, "parents", i32, n), _kv_ptr(cache, children, "children", i32, n), n,
+        _kv_ptr(cache, status, "status", i32, 1), *_kv_space(cache, workspace)), stream, prepare)
 
 
 def nvfp4_kv_free(cache: KVCache, slots, n, status, stream=None, prepare=False):
+    i32 = torch.int32
     return _kv_run(cache, "nvfp4_kv_free", (
-        _i32(slots, n, "slots"), n, _i32(status, 1, "status")), stream, prepare)
+        _kv_ptr(cache, slots, "slots", i32, n), n, _kv_ptr(cache, status, "status", i32, 1)),
+        stream, prepare)
 
 
 def nvfp4_kv_compact(cache: KVCache, used, workspace, stream=None, prepare=False):
     return _kv_run(cache, "nvfp4_kv_compact", (
-        _i32(used, 1, "used"), workspace, workspace.numel() * workspace.element_size()), stream,
-        prepare)
+        _kv_ptr(cache, used, "used", torch.int32, 1), *_kv_space(cache, workspace)), stream, prepare)
 
 
 # --- convenience wrappers (allocate outputs with torch, then call the entry points) ----------

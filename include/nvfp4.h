@@ -562,7 +562,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, int64_t layer, void* K, 
  *          aligned, no initialisation needed (may be NULL when that is 0).
  * Rows of O and lse behind cu_tokens[seqs] are left as they are.
  * Requires heads <= 65,535, q_heads a multiple of heads, tokens * q_heads < 2^31, seqs <= 65,535,
- * max_q * (q_heads / heads) < 2^24. */
+ * max_q * (q_heads / heads) < 2^24, seqs * heads * ceil(max_q * (q_heads / heads) / 16) < 2^31 -
+ * 1,024 * heads (max_q here at most tokens). */
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int dtype, int64_t tokens,
                                          int64_t q_heads, int64_t seqs, int64_t max_q,
                                          int64_t max_kv);
