@@ -25,6 +25,9 @@ namespace {
 #ifndef KV_TARGET
 #define KV_TARGET 1024
 #endif
+#ifndef KV_FEW
+#define KV_FEW 32
+#endif
 #ifndef KV_FULL
 #define KV_FULL 4096
 #endif
@@ -35,16 +38,6 @@ constexpr int kThreads = 64 * kWaves;
 #endif
 constexpr int kMaxSplits = 1024;     // chunks of a row
 constexpr int kDepth = KV_DEPTH;     // tiles of a wave in LDS
-constexpr float kUp = 8.0f;          // log2 of the weights' scale
-constexpr float kSlack = 7.0f;       // how far a logit may exceed the maximum in use, log2
-
-// A lane's bytes of one 16-token half tile. K: D/4 values of its token and their scale bytes. V:
-// D/16 values of 4 tokens, and those tokens' scale bytes.
-template <int D>
-struct HalfTile {
-    static constexpr int W = D / 32;          // code words
-    uint32_t k[W], v[W], ks, vs;
-};
 
 // A tile of 32 positions in LDS, as it is copied from the pages: the codes of [K half 0][K half 1]
 // [V half 0][V half 1], then their scale bytes in the same order. In K's rows the 16-byte pieces
@@ -206,51 +199,6 @@ __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%c0)" ::"n"(N) : "memory");
 }
 
-// K operand of step s: values 8 s .. 8 s + 7 of the lane's D/4.
-template <int S, int W>
-__device__ __forceinline__ half8v k_operand(const uint32_t (&w)[W], uint32_t scales) {
-    Half8 r;
-    const half2v e = scale_twice<S / 2>(scales);
-    r.p[0] = dequant2<0>(w[S], e);
-    r.p[1] = dequant2<1>(w[S], e);
-    r.p[2] = dequant2<2>(w[S], e);
-    r.p[3] = dequant2<3>(w[S], e);
-    return r.v;
-}
-
-// V's codes with two tokens' values of one column in a byte: pair[q][c] byte b holds column
-// 8 (c / 2) + 2 b + c % 2 of tokens 2 q (low nibble) and 2 q + 1.
-template <int D>
-struct VPairs {
-    static constexpr int C = D == 64 ? 2 : D / 64;      // words per pair of tokens
-    uint32_t w[2][C];
-    half2v e[2];
-};
-
-template <int D>
-__device__ __forceinline__ void pair_tokens(VPairs<D>& r, const uint32_t (&v)[D / 32], uint32_t scales) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        constexpr int X = D == 64 ? 1 : D / 128;        // words of a token
-#pragma unroll
-        for (int x = 0; x < X; ++x) {
-            uint32_t a, b;
-            if constexpr (D == 64) {
-                a = v[q];
-                b = v[q] >> 16;
-            } else {
-                a = v[2 * q * X + x];
-                b = v[(2 * q + 1) * X + x];
-            }
-            r.w[q][2 * x] = select_bits(0x0F0F0F0Fu, a, b << 4);
-            r.w[q][2 * x + 1] = select_bits(0x0F0F0F0Fu, a >> 4, b);
-        }
-    }
-    scales &= 0x7F7F7F7Fu;
-    r.e[0] = scale_pair<0>(scales);
-    r.e[1] = scale_pair<1>(scales);
-}
-
 // V operand of output tile J: column J of the lane's D/16, tokens 4g .. 4g + 3 of both half tiles.
 template <int D, int J>
 __device__ __forceinline__ half8v v_operand(const VPairs<D> (&h)[2]) {
@@ -261,14 +209,6 @@ __device__ __forceinline__ half8v v_operand(const VPairs<D> (&h)[2]) {
     r.p[2] = dequant2<b>(h[1].w[0][c], h[1].e[0]);
     r.p[3] = dequant2<b>(h[1].w[1][c], h[1].e[1]);
     return r.v;
-}
-
-template <int N, typename F, int I = 0>
-__device__ __forceinline__ void unroll(F&& f) {
-    if constexpr (I < N) {
-        f(std::integral_constant<int, I>{});
-        unroll<N, F, I + 1>(static_cast<F&&>(f));
-    }
 }
 
 __device__ __forceinline__ f32x4 mfma(half8v a, half8v b, f32x4 c) {
@@ -334,21 +274,6 @@ __device__ __forceinline__ void convert_query(QRow<D, BF16>& q, const RawQuery<D
     }
     // at least the smallest normal number: a masked logit of -infinity times it stays -infinity
     q.f = fmaxf(__builtin_ldexpf(scale, -k) * (S * kLog2e), 0x1p-126f);
-}
-
-// Row row of the item's (token, query head) rows: its byte offset in Q or O, and in lse.
-struct RowAt {
-    int64_t token;
-    int32_t head;
-};
-__device__ __forceinline__ RowAt row_at(int64_t first, int head, int group, int row) {
-    const int j = row / group;
-    return RowAt{first + j, head * group + row - j * group};
-}
-
-// lse of a row from its maximum (log2, the weights' scale of 2^kUp apart) and sum.
-__device__ __forceinline__ float row_lse(float m, float l) {
-    return l > 0.0f ? (m - kUp + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
 }
 
 // Waves a SIMD should hold: as many as the accumulators and two tiles in flight leave room for.
@@ -730,7 +655,7 @@ KvPlan plan_of(int64_t heads, int64_t tokens, int64_t q_heads, int64_t seqs, int
                int64_t span) {
     const int64_t group = q_heads / heads, rows = max_q * group;
     KvPlan p{};
-    p.tile_rows = rows <= 16 ? 16 : 32;
+    p.tile_rows = rows <= 16 ? 16 : rows <= KV_FEW ? 32 : kPrefillRows;
     p.tiles = (int32_t)ceil_div(rows, p.tile_rows);
     p.tiles = p.tiles > 0 ? p.tiles : 1;
     int64_t most = seqs * p.tiles;                       // tiles of all items, a head
@@ -764,8 +689,10 @@ hipError_t launch(const KvAttention& a, const KvPlan& p, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.kv.heads * p.tasks));
     if (p.tile_rows == 16)
         hipLaunchKernelGGL((k_kv_decode<D, BF16, 1>), grid, dim3(kThreads), 0, stream, a, p);
-    else
+    else if (p.tile_rows == 32)
         hipLaunchKernelGGL((k_kv_decode<D, BF16, 2>), grid, dim3(kThreads), 0, stream, a, p);
+    else
+        launch_kv_prefill(a, p, stream);
     if (p.target > 0)
         hipLaunchKernelGGL((k_kv_join<D, BF16>),
                            dim3((uint32_t)((p.by_item ? (int64_t)a.b.seqs * a.max_q : a.b.tokens) *

@@ -85,6 +85,85 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return r(a) | (r(b) << 16);
 }
 
+constexpr float kUp = 8.0f;          // log2 of the weights' scale
+constexpr float kSlack = 7.0f;       // how far a logit may exceed the maximum in use, log2
+
+// A lane's bytes of 16 tokens (a unit). K: D/4 values of its token and their scale bytes. V:
+// D/16 values of 4 tokens, and those tokens' scale bytes.
+template <int D>
+struct HalfTile {
+    static constexpr int W = D / 32;          // code words
+    uint32_t k[W], v[W], ks, vs;
+};
+
+// K operand of step s: values 8 s .. 8 s + 7 of the lane's D/4.
+template <int S, int W>
+__device__ __forceinline__ half8v k_operand(const uint32_t (&w)[W], uint32_t scales) {
+    Half8 r;
+    const half2v e = scale_twice<S / 2>(scales);
+    r.p[0] = dequant2<0>(w[S], e);
+    r.p[1] = dequant2<1>(w[S], e);
+    r.p[2] = dequant2<2>(w[S], e);
+    r.p[3] = dequant2<3>(w[S], e);
+    return r.v;
+}
+
+// V's codes with two tokens' values of one column in a byte: pair[q][c] byte b holds column
+// 8 (c / 2) + 2 b + c % 2 of tokens 2 q (low nibble) and 2 q + 1.
+template <int D>
+struct VPairs {
+    static constexpr int C = D == 64 ? 2 : D / 64;      // words per pair of tokens
+    uint32_t w[2][C];
+    half2v e[2];
+};
+
+template <int D>
+__device__ __forceinline__ void pair_tokens(VPairs<D>& r, const uint32_t (&v)[D / 32], uint32_t scales) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        constexpr int X = D == 64 ? 1 : D / 128;        // words of a token
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+            uint32_t a, b;
+            if constexpr (D == 64) {
+                a = v[q];
+                b = v[q] >> 16;
+            } else {
+                a = v[2 * q * X + x];
+                b = v[(2 * q + 1) * X + x];
+            }
+            r.w[q][2 * x] = select_bits(0x0F0F0F0Fu, a, b << 4);
+            r.w[q][2 * x + 1] = select_bits(0x0F0F0F0Fu, a >> 4, b);
+        }
+    }
+    scales &= 0x7F7F7F7Fu;
+    r.e[0] = scale_pair<0>(scales);
+    r.e[1] = scale_pair<1>(scales);
+}
+
+template <int N, typename F, int I = 0>
+__device__ __forceinline__ void unroll(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll<N, F, I + 1>(static_cast<F&&>(f));
+    }
+}
+
+// Row row of the item's (token, query head) rows: its byte offset in Q or O, and in lse.
+struct RowAt {
+    int64_t token;
+    int32_t head;
+};
+__device__ __forceinline__ RowAt row_at(int64_t first, int head, int group, int row) {
+    const int j = row / group;
+    return RowAt{first + j, head * group + row - j * group};
+}
+
+// lse of a row from its maximum (log2, the weights' scale of 2^kUp apart) and sum.
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l > 0.0f ? (m - kUp + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
+}
+
 // Work split. Rows of an item and head: (token j, query head of the group), row = j * group + head,
 // in tiles; the positions a tile sees in chunks. Lengths are known on the device only, and in a batch
 // they differ widely, so each workgroup finds its task itself: a wave sums the positions of all
@@ -104,6 +183,9 @@ struct KvPlan {
     uint64_t page_magic;     // division of a 16-token unit by the units of a page
     uint32_t page_shift;
 };
+
+constexpr int kPrefillRows = 128;   // of a workgroup of kv_prefill.hip
+void launch_kv_prefill(const KvAttention& a, const KvPlan& p, hipStream_t stream);
 
 // What one tile of an item sees: positions begin .. end - 1 (begin a multiple of 32).
 struct KvRange {
