@@ -20,6 +20,12 @@
 namespace nvfp4 {
 namespace {
 
+#ifndef KV_AHEAD
+#define KV_AHEAD 8
+#endif
+#ifndef KV_PV
+#define KV_PV 4
+#endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 64;            // positions of a tile: one 16-token unit a wave
@@ -95,27 +101,43 @@ __device__ __forceinline__ void load_unit(HalfTile<D>& u, const uint8_t* rec, in
     u.vs = *reinterpret_cast<const uint32_t*>(scales + o.vs);
 }
 
-// Converts a wave's unit (number `wave` of the tile) into a buffer.
+// Conversion of a wave's unit (number `wave` of the tile) into a buffer, in kPieces pieces that the
+// caller spreads between matrix instructions: D/32 pieces of K (8 values of a token), then D/16 of V (4
+// tokens of a value).
 template <int D>
-__device__ __forceinline__ void store_unit(uint8_t* buf, const HalfTile<D>& u, int wave, int lane) {
-    const uint32_t scales = u.ks & 0x7F7F7F7Fu;
-    const int t = 16 * wave + (lane >> 2), piece = (lane & 3) * (D / 32);
-    unroll<D / 32>([&](auto step) {
-        constexpr int S = decltype(step)::value;
-        *reinterpret_cast<half8v*>(buf + Lds<D>::k(t, piece + S)) = k_operand<S>(u.k, scales);
-    });
-    VPairs<D> p;
-    pair_tokens<D>(p, u.v, u.vs);
-    const int n = lane & 15, block = lane >> 4;
-    const int c = 2 * wave + (block & 1), high = (block >> 1) * 8;
-    unroll<D / 16>([&](auto column) {
-        constexpr int J = decltype(column)::value;
-        constexpr int w = 2 * (J / 8) + (J & 1), b = (J & 7) >> 1;
-        const half2v x = dequant2<b>(p.w[0][w], p.e[0]), y = dequant2<b>(p.w[1][w], p.e[1]);
-        *reinterpret_cast<u32x2*>(buf + Lds<D>::v(J * 16 + n, c) + high) =
-            u32x2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
-    });
-}
+struct UnitStore {
+    static constexpr int kPieces = D / 32 + D / 16;
+    uint8_t* buf;
+    const HalfTile<D>& u;
+    VPairs<D> v;
+    uint32_t scales;
+    int t, first, n, c, high;
+
+    __device__ __forceinline__ UnitStore(uint8_t* to, const HalfTile<D>& unit, int wave, int lane)
+        : buf(to), u(unit) {
+        scales = unit.ks & 0x7F7F7F7Fu;
+        pair_tokens<D>(v, unit.v, unit.vs);
+        t = 16 * wave + (lane >> 2);
+        first = (lane & 3) * (D / 32);
+        n = lane & 15;
+        c = 2 * wave + ((lane >> 4) & 1);
+        high = (lane >> 5) * 8;
+    }
+    template <int I>
+    __device__ __forceinline__ void piece() {
+        if constexpr (I < D / 32) {
+            *reinterpret_cast<half8v*>(buf + Lds<D>::k(t, first + I)) = k_operand<I>(u.k, scales);
+        } else {
+            constexpr int J = I - D / 32, w = 2 * (J / 8) + (J & 1), b = (J & 7) >> 1;
+            const half2v x = dequant2<b>(v.w[0][w], v.e[0]), y = dequant2<b>(v.w[1][w], v.e[1]);
+            *reinterpret_cast<u32x2*>(buf + Lds<D>::v(J * 16 + n, c) + high) =
+                u32x2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
+        }
+    }
+    __device__ __forceinline__ void all() {
+        unroll<kPieces>([&](auto i) { piece<decltype(i)::value>(); });
+    }
+};
 
 // Values 16 s + 8 h .. + 7 of a row as f16 operands, and the logit (log2) of a product.
 template <int D, bool BF16>
@@ -254,28 +276,39 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
         for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
     float m = -__builtin_inff(), sub = 0.0f, l = 0.0f;
 
-    if (tiles > 0) store_unit<D>(space, raw, wave, lane);
+    if (tiles > 0) UnitStore<D>(space, raw, wave, lane).all();
     uint32_t ok = named & 15u;
     if (tiles > 1) load(1);
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
         const uint8_t* buf = space + (i & 1) * Lds<D>::kBuffer;
+        uint8_t* other = space + (~i & 1) * Lds<D>::kBuffer;   // of tile i + 1; after the last one unused
+        const uint32_t next = named & 15u;
         const int t = begin + i * kTile;
         if (t < lim_any && t + kTile > low_any) {        // the wave sees something of the tile
+            // the first products of this tile, and in their shadow the conversion of the next: three
+            // pieces to four steps. The operands are read kAhead steps ahead of their use.
+            constexpr int kSteps = 2 * NS, kAhead = kSteps < KV_AHEAD ? kSteps : KV_AHEAD;
+            UnitStore<D> store(other, raw, wave, lane);
+            half8v k[kSteps];
+            const auto read_k = [&](int z) {
+                k[z] = *reinterpret_cast<const half8v*>(buf + Lds<D>::k(32 * (z & 1) + n, 2 * (z >> 1) + h));
+            };
             f32x16 s[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) s[u][k] = 0.0f;
+                for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int st = 0; st < NS; ++st) {
-                    const half8v k = *reinterpret_cast<const half8v*>(
-                        buf + Lds<D>::k(32 * u + n, 2 * st + h));
-                    s[u] = mfma(k, q.hi[st], s[u]);
-                    if constexpr (!BF16) s[u] = mfma(k, q.lo[st], s[u]);
-                }
+            for (int z = 0; z < kAhead; ++z) read_k(z);
+            unroll<kSteps>([&](auto step) {
+                constexpr int Z = decltype(step)::value;
+                s[Z & 1] = mfma(k[Z], q.hi[Z >> 1], s[Z & 1]);
+                if constexpr (!BF16) s[Z & 1] = mfma(k[Z], q.lo[Z >> 1], s[Z & 1]);
+                if constexpr (Z + kAhead < kSteps) read_k(Z + kAhead);
+                if constexpr (Z % 4 != 3) store.template piece<Z / 4 * 3 + Z % 4>();
+                __builtin_amdgcn_sched_barrier(0);
+            });
             if (!(ok == 15u && t >= low_all && t + kTile <= lim_all)) {
                 asm volatile("");                        // a branch, not selects in every tile
 #pragma unroll
@@ -301,6 +334,7 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) o[j] *= al;
             }
+            if (i + 2 < tiles) load(i + 2);
             Half8 hi[4], lo[4];
             float sum = 0.0f;
 #pragma unroll
@@ -328,12 +362,19 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
                     o[j] = mfma(v, hi[u].v, o[j]);
                     if constexpr (!BF16) o[j] = mfma(v, lo[u].v, o[j]);
                 }
-        }
-        if (i + 1 < tiles) {
-            store_unit<D>(space + ((i + 1) & 1) * Lds<D>::kBuffer, raw, wave, lane);
-            ok = named & 15u;
+#if KV_PV > 0
+            __builtin_amdgcn_sched_group_barrier(0x100, KV_PV, 0);
+#pragma unroll
+            for (int z = 0; z < 4 * NJ; ++z) {
+                __builtin_amdgcn_sched_group_barrier(0x8, BF16 ? 1 : 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+#endif
+        } else {
+            UnitStore<D>(other, raw, wave, lane).all();
             if (i + 2 < tiles) load(i + 2);
         }
+        ok = next;
         __syncthreads();
     }
 
