@@ -3,10 +3,13 @@
 //
 // The bookkeeping of reserve, fork and free is one workgroup: it checks every item before it changes
 // anything (slots listed twice are found in a bit map in LDS), ranks the pages the items need with a
-// prefix sum, collects that many free pages in ascending order, and hands them out one wave per
-// item. Fork's partly filled pages are then copied by a second launch. Compact needs the whole of
-// refs: workgroups of kChunk pages count, then rank, then move, in three launches. Reference counts
-// change by integer atomics, whose result does not depend on their order.
+// prefix sum, collects that many free pages in ascending order, and hands them out. What bounds it is
+// the chain of dependent loads (slot, length, table entry), so every step is made for all items at
+// once and the first reference counts are on their way from the start. Fork's rows and partly filled
+// pages are copied by a second launch. Compact ranks all pages in one workgroup, or, beyond kOne
+// pages, in workgroups of kChunk that count and then rank, and moves the records in a last launch, at
+// the rate of a copy. Reference counts change by integer atomics, whose result does not depend on
+// their order.
 #include <hip/hip_runtime.h>
 
 #include "../../include/nvfp4.h"
@@ -18,7 +21,10 @@ namespace {
 constexpr int kBook = 1024;          // threads of the bookkeeping workgroup
 constexpr int kWaves = kBook / 64;
 constexpr int kSlotWords = 65536 / 32;
-constexpr int kChunk = 4096;         // pages per workgroup of compact's counting
+constexpr int kFirst = 8;            // reference counts a thread loads ahead
+constexpr int kBatch = 8;            // table rows a wave has in flight
+constexpr int kOne = 16 * kBook;     // pages that one workgroup ranks for compact
+constexpr int kChunk = 1024;         // pages per workgroup of compact's counting
 constexpr int kCopyThreads = 256;
 constexpr int kCopyLoads = 4;        // 16-byte loads in flight per lane
 constexpr int kPart = kCopyThreads * kCopyLoads * 16;   // bytes of a record per step
@@ -61,6 +67,11 @@ __device__ __forceinline__ int length_of(const KvPool& p, int slot) {
     return min(max(p.lens[slot], 0), p.max_pages * p.page);
 }
 
+__device__ __forceinline__ void clear_map(const KvPool& p, uint32_t* map) {
+    for (int i = threadIdx.x; i < (p.max_slots + 31) / 32; i += kBook) map[i] = 0u;
+    __syncthreads();
+}
+
 // Adds the items' slots to the bit map; true (for this thread) if one is outside the table or listed
 // twice.
 __device__ __forceinline__ bool mark_slots(const KvPool& p, const int32_t* slots, int n,
@@ -78,27 +89,29 @@ __device__ __forceinline__ bool mark_slots(const KvPool& p, const int32_t* slots
     return bad;
 }
 
+// The thread's kFirst pages from page p0 on: which are free, as bits.
+__device__ __forceinline__ uint32_t free_bits(const KvPool& p, int p0) {
+    const int q = p0 + kFirst * (int)threadIdx.x;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int r = q + i < p.num_pages ? p.refs[q + i] : 1;
+        bits |= r <= 0 ? 1u << i : 0u;
+    }
+    return bits;
+}
+
 // The lowest `need` free pages in ascending order into list[]; returns how many were found (at most
-// need).
-__device__ __forceinline__ int take_free(const KvPool& p, int need, int32_t* list, int* sums) {
+// need). bits: free_bits(p, 0), loaded ahead.
+__device__ __forceinline__ int take_free(const KvPool& p, int need, uint32_t bits, int32_t* list,
+                                         int* sums) {
     int found = 0;
-    for (int p0 = 0; p0 < p.num_pages && found < need; p0 += 4 * kBook) {
-        const int q = p0 + 4 * (int)threadIdx.x;
-        int r[4], free = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            r[i] = q + i < p.num_pages ? p.refs[q + i] : 1;
-            free += r[i] <= 0;
-        }
+    for (int p0 = 0; p0 < p.num_pages && found < need; p0 += kFirst * kBook) {
+        if (p0 > 0) bits = free_bits(p, p0);
         int total;
-        int k = found + block_exclusive<kWaves>(free, sums, total);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (r[i] <= 0) {
-                if (k < need) list[k] = q + i;
-                ++k;
-            }
-        }
+        int k = found + block_exclusive<kWaves>(__popc(bits), sums, total);
+        for (uint32_t left = bits; left != 0 && k < need; left &= left - 1)
+            list[k++] = p0 + kFirst * (int)threadIdx.x + __builtin_ctz(left);
         found += total;
     }
     return min(found, need);
@@ -113,14 +126,14 @@ __global__ __launch_bounds__(kBook) void k_kv_reserve(KvPool p, const int32_t* _
     __shared__ uint32_t map[kSlotWords];
     __shared__ int sums[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kSlotWords; i += kBook) map[i] = 0u;
-    __syncthreads();
+    const uint32_t bits = free_bits(p, 0);
+    clear_map(p, map);
     if (__syncthreads_or(mark_slots(p, slots, n, map))) {
         if (threadIdx.x == 0) *status = NVFP4_KV_BAD_SLOT;
         return;
     }
-    bool bad = false;
-    int64_t need = 0;
+    bool bad = false, many = false;
+    int need = 0;                        // the slots are distinct, so all their pages are < 2^31
     for (int i0 = 0; i0 < n; i0 += kBook) {
         const int i = i0 + threadIdx.x;
         int add = 0;
@@ -130,35 +143,55 @@ __global__ __launch_bounds__(kBook) void k_kv_reserve(KvPool p, const int32_t* _
             if (counts[i] < 0 || now > (int64_t)p.max_pages * p.page) bad = true;
             else add = pages_of(now, p.page) - pages_of(old, p.page);
         }
+        many |= add > 1;
         int total;
         const int before = block_exclusive<kWaves>(add, sums, total);
-        // beyond num_pages the call fails anyway: ranks are kept inside int32
-        if (i < n) first[i] = (int)min(need + before, (int64_t)p.num_pages + 1);
+        if (i < n) first[i] = need + before;
         need += total;
     }
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) *status = NVFP4_KV_BAD_LENGTH;
         return;
     }
-    if (need > p.num_pages || take_free(p, (int)need, list, sums) < (int)need) {
+    if (need > p.num_pages || take_free(p, need, bits, list, sums) < need) {
         if (threadIdx.x == 0) *status = NVFP4_KV_NO_PAGES;
         return;
     }
-    __syncthreads();
-    for (int i = wave; i < n; i += kWaves) {
-        const int s = slots[i];
-        const int old = length_of(p, s);
-        const int now = old + counts[i];
-        const int have = pages_of(old, p.page), add = pages_of(now, p.page) - have;
-        for (int k = lane; k < add; k += 64) {
-            const int page = list[first[i] + k];
-            p.table[(int64_t)s * p.max_pages + have + k] = page;
+    // an item's first page by its thread; the others, where an item takes more, one wave an item.
+    // Lengths are written when every item's old one has been used.
+    const bool any_many = __syncthreads_or(many);
+    for (int i = threadIdx.x; i < n; i += kBook) {
+        const int s = slots[i], old = length_of(p, s), now = old + counts[i];
+        const int have = pages_of(old, p.page);
+        if (pages_of(now, p.page) > have) {
+            const int page = list[first[i]];
+            p.table[(int64_t)s * p.max_pages + have] = page;
             p.refs[page] = 1;
         }
-        if (lane == 0) p.lens[s] = now;
+        if (!any_many) p.lens[s] = now;
+    }
+    if (any_many) {
+        for (int i = wave; i < n; i += kWaves) {
+            const int s = slots[i], old = length_of(p, s), now = old + counts[i];
+            const int have = pages_of(old, p.page), add = pages_of(now, p.page) - have;
+            for (int k = lane + 1; k < add; k += 64) {
+                const int page = list[first[i] + k];
+                p.table[(int64_t)s * p.max_pages + have + k] = page;
+                p.refs[page] = 1;
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kBook) {
+            const int s = slots[i];
+            p.lens[s] = length_of(p, s) + counts[i];
+        }
     }
     if (threadIdx.x == 0) *status = NVFP4_KV_DONE;
 }
+
+// Checks a fork and gives every item the record to copy: src[i] its page (kRowOnly: none), kNothing
+// for all where the fork is refused, and dst[i].
+constexpr int kRowOnly = -1, kNothing = -2;
 
 __global__ __launch_bounds__(kBook) void k_kv_fork(KvPool p, const int32_t* __restrict__ parents,
                                                    const int32_t* __restrict__ children, int n,
@@ -166,10 +199,8 @@ __global__ __launch_bounds__(kBook) void k_kv_fork(KvPool p, const int32_t* __re
                                                    int32_t* src, int32_t* dst) {
     __shared__ uint32_t map[kSlotWords];
     __shared__ int sums[kWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kSlotWords; i += kBook) map[i] = 0u;
-    for (int i = threadIdx.x; i < n; i += kBook) src[i] = -1;      // nothing to copy yet
-    __syncthreads();
+    const uint32_t bits = free_bits(p, 0);
+    clear_map(p, map);
     bool bad = mark_slots(p, children, n, map);
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kBook) {
@@ -178,68 +209,81 @@ __global__ __launch_bounds__(kBook) void k_kv_fork(KvPool p, const int32_t* __re
         else bad |= ((map[a >> 5] >> (a & 31)) & 1u) != 0;
         if ((uint32_t)c < (uint32_t)p.max_slots) bad |= p.lens[c] != 0;
     }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) *status = NVFP4_KV_BAD_SLOT;
-        return;
-    }
+    int reason = __syncthreads_or(bad) ? NVFP4_KV_BAD_SLOT : NVFP4_KV_DONE;
     int need = 0;                                                  // at most n <= 65,536
-    for (int i0 = 0; i0 < n; i0 += kBook) {
-        const int i = i0 + threadIdx.x;
-        const int part = i < n && length_of(p, parents[i]) % p.page != 0;
-        int total;
-        const int before = block_exclusive<kWaves>(part, sums, total);
-        if (i < n) first[i] = need + before;
-        need += total;
-    }
-    if (take_free(p, need, list, sums) < need) {
-        if (threadIdx.x == 0) *status = NVFP4_KV_NO_PAGES;
-        return;
+    if (reason == NVFP4_KV_DONE) {
+        for (int i0 = 0; i0 < n; i0 += kBook) {
+            const int i = i0 + threadIdx.x;
+            const int part = i < n && length_of(p, parents[i]) % p.page != 0;
+            int total;
+            const int before = block_exclusive<kWaves>(part, sums, total);
+            if (i < n) first[i] = need + before;
+            need += total;
+        }
+        if (take_free(p, need, bits, list, sums) < need) reason = NVFP4_KV_NO_PAGES;
     }
     __syncthreads();
-    for (int i = wave; i < n; i += kWaves) {
-        const int len = length_of(p, parents[i]);
-        const int full = len / p.page;
-        const int32_t* from = p.table + (int64_t)parents[i] * p.max_pages;
-        int32_t* to = p.table + (int64_t)children[i] * p.max_pages;
-        for (int k = lane; k < full; k += 64) {
-            const int page = from[k];
-            to[k] = page;
-            if ((uint32_t)page < (uint32_t)p.num_pages) atomicAdd(&p.refs[page], 1);
-        }
-        if (lane == 0) {
+    for (int i = threadIdx.x; i < n; i += kBook) {
+        int from = kNothing;
+        if (reason == NVFP4_KV_DONE) {
+            const int len = length_of(p, parents[i]), full = len / p.page;
+            from = kRowOnly;
             if (len % p.page != 0) {
+                const int old = p.table[(int64_t)parents[i] * p.max_pages + full];
                 const int page = list[first[i]];
-                to[full] = page;
-                p.refs[page] = 1;
                 dst[i] = page;
-                src[i] = (uint32_t)from[full] < (uint32_t)p.num_pages ? from[full] : -1;
+                p.refs[page] = 1;
+                p.table[(int64_t)children[i] * p.max_pages + full] = page;
+                from = (uint32_t)old < (uint32_t)p.num_pages ? old : kRowOnly;
             }
             p.lens[children[i]] = len;
         }
+        src[i] = from;
     }
-    if (threadIdx.x == 0) *status = NVFP4_KV_DONE;
+    if (threadIdx.x == 0) *status = reason;
 }
 
 __global__ __launch_bounds__(kBook) void k_kv_free(KvPool p, const int32_t* __restrict__ slots,
                                                    int n, int32_t* status) {
     __shared__ uint32_t map[kSlotWords];
+    __shared__ int slot[kBook], held[kBook];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kSlotWords; i += kBook) map[i] = 0u;
-    __syncthreads();
+    clear_map(p, map);
     if (__syncthreads_or(mark_slots(p, slots, n, map))) {
         if (threadIdx.x == 0) *status = NVFP4_KV_BAD_SLOT;
         return;
     }
-    for (int i = wave; i < n; i += kWaves) {
-        const int s = slots[i];
-        const int held = pages_of(length_of(p, s), p.page);
-        int32_t* row = p.table + (int64_t)s * p.max_pages;
-        for (int k = lane; k < held; k += 64) {
-            const int page = row[k];
-            row[k] = -1;
-            if ((uint32_t)page < (uint32_t)p.num_pages) atomicSub(&p.refs[page], 1);
+    for (int i0 = 0; i0 < n; i0 += kBook) {
+        const int m = min(kBook, n - i0);
+        __syncthreads();
+        if ((int)threadIdx.x < m) {
+            const int s = slots[i0 + threadIdx.x];
+            slot[threadIdx.x] = s;
+            held[threadIdx.x] = pages_of(length_of(p, s), p.page);
+            p.lens[s] = 0;
         }
-        if (lane == 0) p.lens[s] = 0;
+        __syncthreads();
+        // kBatch rows of a wave at a time, 64 entries of each: all loads, then all changes
+        for (int j0 = wave * kBatch; j0 < m; j0 += kWaves * kBatch) {
+            int most = 0;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) most = max(most, j0 + j < m ? held[j0 + j] : 0);
+            for (int k = lane; k - lane < most; k += 64) {
+                int page[kBatch];
+                int32_t* at[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const bool in = j0 + j < m && k < held[j0 + j];
+                    at[j] = in ? p.table + (int64_t)slot[j0 + j] * p.max_pages + k : nullptr;
+                    page[j] = in ? *at[j] : -1;
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    if (at[j]) *at[j] = -1;
+                    if ((uint32_t)page[j] < (uint32_t)p.num_pages) atomicSub(&p.refs[page[j]], 1);
+                }
+            }
+        }
     }
     if (threadIdx.x == 0) *status = NVFP4_KV_DONE;
 }
@@ -262,14 +306,30 @@ __device__ __forceinline__ void copy_part(const uint8_t* __restrict__ s, uint8_t
     }
 }
 
-// Fork's copies: item blockIdx.y, layer blockIdx.z, the record's parts over blockIdx.x.
-__global__ __launch_bounds__(kCopyThreads) void k_kv_copy(KvPool p, const int32_t* __restrict__ src,
-                                                          const int32_t* __restrict__ dst) {
-    const int a = src[blockIdx.y];
+// Fork's copies: item blockIdx.x, the parts of its record over blockIdx.y, layer blockIdx.z; the first
+// workgroup of an item also copies its table row of full pages.
+__global__ __launch_bounds__(kCopyThreads) void k_kv_copy(KvPool p, const int32_t* __restrict__ parents,
+                                                          const int32_t* __restrict__ children,
+                                                          const int32_t* __restrict__ src,
+                                                          const int32_t* __restrict__ dst, int parts) {
+    const int i = blockIdx.x;
+    const int a = src[i];
+    if (a == kNothing) return;
+    if (blockIdx.y == 0 && blockIdx.z == 0) {
+        const int full = length_of(p, parents[i]) / p.page;
+        const int32_t* from = p.table + (int64_t)parents[i] * p.max_pages;
+        int32_t* to = p.table + (int64_t)children[i] * p.max_pages;
+        for (int k = threadIdx.x; k < full; k += kCopyThreads) {
+            const int page = from[k];
+            to[k] = page;
+            if ((uint32_t)page < (uint32_t)p.num_pages) atomicAdd(&p.refs[page], 1);
+        }
+    }
     if (a < 0) return;
     uint8_t* base = p.pages + (int64_t)blockIdx.z * p.layer_stride;
-    copy_part(base + (int64_t)a * p.page_stride, base + (int64_t)dst[blockIdx.y] * p.page_stride,
-              (int64_t)blockIdx.x * kPart, p.record);
+    for (int64_t part = blockIdx.y; part < parts; part += gridDim.y)
+        copy_part(base + (int64_t)a * p.page_stride, base + (int64_t)dst[i] * p.page_stride,
+                  part * kPart, p.record);
 }
 
 // Compact's workspace: head[2] = (used pages, pages to move), counts[chunks], src[], dst[] by rank,
@@ -283,26 +343,68 @@ struct CompactSpace {
 };
 
 constexpr int kCountThreads = 256;
+constexpr int kEach = kChunk / kCountThreads;            // consecutive pages of a thread
 
-// Used pages of a chunk.
-__device__ __forceinline__ int used_in(const KvPool& p, int begin, int end, int* sums) {
-    int used = 0;
-    for (int q = begin + threadIdx.x; q < end; q += kCountThreads) used += p.refs[q] > 0;
-    int total;
-    block_exclusive<kCountThreads / 64>(used, sums, total);
-    return total;
+// Which of N consecutive pages from q on (below end) are used, as bits.
+template <int N>
+__device__ __forceinline__ uint32_t used_bits(const KvPool& p, int q, int end) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) bits |= q + i < end && p.refs[q + i] > 0 ? 1u << i : 0u;
+    return bits;
+}
+
+// Ranks N consecutive pages from q on, `before` used ones before them, U used in all, `below` of them
+// below page U: used pages at or above U move to the free pages below it, in order.
+template <int N>
+__device__ __forceinline__ void rank_pages(const KvPool& p, const CompactSpace& w, int q, uint32_t bits,
+                                           int before, int U, int below) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (q + i >= p.num_pages) break;
+        const bool used = (bits >> i) & 1u;
+        int r = -1;
+        if (used && q + i >= U) {
+            r = before - below;
+            w.src[r] = q + i;
+        } else if (!used && q + i < U) {
+            w.dst[q + i - before] = q + i;
+        }
+        w.rank[q + i] = r;
+        before += used;
+    }
+}
+
+// All of at most kOne pages.
+__global__ __launch_bounds__(kBook) void k_kv_rank_all(KvPool p, CompactSpace w) {
+    constexpr int N = kOne / kBook;
+    __shared__ int sums[kWaves];
+    const int q = N * (int)threadIdx.x;
+    const uint32_t bits = used_bits<N>(p, q, p.num_pages);
+    int U, below;
+    const int before = block_exclusive<kWaves>(__popc(bits), sums, U);
+    const int inside = min(max(U - q, 0), N);            // pages of the thread below U
+    block_exclusive<kWaves>(__popc(bits & ((1u << inside) - 1u)), sums, below);
+    if (threadIdx.x == 0) {
+        w.head[0] = U;
+        w.head[1] = U - below;
+    }
+    rank_pages<N>(p, w, q, bits, before, U, below);
 }
 
 __global__ __launch_bounds__(kCountThreads) void k_kv_count(KvPool p, CompactSpace w) {
     __shared__ int sums[kCountThreads / 64];
-    const int begin = blockIdx.x * kChunk;
-    const int total = used_in(p, begin, min(begin + kChunk, p.num_pages), sums);
+    const int q = blockIdx.x * kChunk + kEach * (int)threadIdx.x;
+    int total;
+    block_exclusive<kCountThreads / 64>(__popc(used_bits<kEach>(p, q, p.num_pages)), sums, total);
     if (threadIdx.x == 0) w.counts[blockIdx.x] = total;
 }
 
 __global__ __launch_bounds__(kCountThreads) void k_kv_rank(KvPool p, CompactSpace w, int chunks) {
     __shared__ int sums[kCountThreads / 64];
     constexpr int W = kCountThreads / 64;
+    const int q = blockIdx.x * kChunk + kEach * (int)threadIdx.x;
+    const uint32_t bits = used_bits<kEach>(p, q, p.num_pages);
     // used pages in all chunks, before this chunk, and before the chunk that holds page U
     int all = 0, mine = 0;
     for (int c = threadIdx.x; c < chunks; c += kCountThreads) {
@@ -310,37 +412,20 @@ __global__ __launch_bounds__(kCountThreads) void k_kv_rank(KvPool p, CompactSpac
         all += v;
         mine += c < (int)blockIdx.x ? v : 0;
     }
-    int U, before;
+    int U, before, below, in_chunk, ahead;
     block_exclusive<W>(all, sums, U);
     block_exclusive<W>(mine, sums, before);
     const int cu = min(U / kChunk, chunks - 1);
     int low = 0;
     for (int c = threadIdx.x; c < cu; c += kCountThreads) low += w.counts[c];
-    int below;                                    // used pages below U
-    block_exclusive<W>(low, sums, below);
-    below += used_in(p, cu * kChunk, min(U, p.num_pages), sums);
+    low += __popc(used_bits<kEach>(p, cu * kChunk + kEach * (int)threadIdx.x, min(U, p.num_pages)));
+    block_exclusive<W>(low, sums, below);                // used pages below U
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         w.head[0] = U;
         w.head[1] = U - below;
     }
-    const int begin = blockIdx.x * kChunk, end = min(begin + kChunk, p.num_pages);
-    for (int q0 = begin; q0 < end; q0 += kCountThreads) {
-        const int q = q0 + threadIdx.x;
-        const int used = q < end && p.refs[q] > 0;
-        int total;
-        const int k = before + block_exclusive<W>(used, sums, total);   // used pages before q
-        if (q < end) {
-            int r = -1;
-            if (used && q >= U) {
-                r = k - below;
-                w.src[r] = q;
-            } else if (!used && q < U) {
-                w.dst[q - k] = q;
-            }
-            w.rank[q] = r;
-        }
-        before += total;
-    }
+    ahead = block_exclusive<W>(__popc(bits), sums, in_chunk);
+    rank_pages<kEach>(p, w, q, bits, before + ahead, U, below);
 }
 
 // Moves the records, and (first workgroups) rewrites table and refs.
@@ -402,9 +487,10 @@ hipError_t launch_kv_fork(const KvPool& p, const int32_t* parents, const int32_t
     int32_t *src = first + words(n), *dst = src + words(n), *list = dst + words(n);
     hipLaunchKernelGGL(k_kv_fork, dim3(1), dim3(kBook), 0, stream, p, parents, children, n, status,
                        first, list, src, dst);
-    if (n > 0 && p.layers > 0 && p.record > 0)
-        hipLaunchKernelGGL(k_kv_copy, dim3((uint32_t)parts_of(p), (uint32_t)n, (uint32_t)p.layers),
-                           dim3(kCopyThreads), 0, stream, p, src, dst);
+    const int64_t parts = parts_of(p);
+    if (n > 0)
+        hipLaunchKernelGGL(k_kv_copy, dim3((uint32_t)n, (uint32_t)(parts < 64 ? parts : 64),
+                                           (uint32_t)p.layers), dim3(kCopyThreads), 0, stream, p, parents, children, src, dst, (int)parts);
     return hipGetLastError();
 }
 
@@ -422,8 +508,12 @@ hipError_t launch_kv_compact(const KvPool& p, int32_t* used, void* workspace, hi
     w.src = w.counts + words(chunks);
     w.dst = w.src + words(p.num_pages);
     w.rank = w.dst + words(p.num_pages);
-    hipLaunchKernelGGL(k_kv_count, dim3(chunks), dim3(kCountThreads), 0, stream, p, w);
-    hipLaunchKernelGGL(k_kv_rank, dim3(chunks), dim3(kCountThreads), 0, stream, p, w, chunks);
+    if (p.num_pages <= kOne) {
+        hipLaunchKernelGGL(k_kv_rank_all, dim3(1), dim3(kBook), 0, stream, p, w);
+    } else {
+        hipLaunchKernelGGL(k_kv_count, dim3(chunks), dim3(kCountThreads), 0, stream, p, w);
+        hipLaunchKernelGGL(k_kv_rank, dim3(chunks), dim3(kCountThreads), 0, stream, p, w, chunks);
+    }
     // the number of moves is known on the device only: a grid that fills the chip strides over them
     const int64_t most = (int64_t)(p.num_pages / 2) * p.layers * parts_of(p);
     const uint32_t grid = (uint32_t)(most < 2048 ? (most > 16 ? most : 16) : 2048);
