@@ -22,22 +22,16 @@
 namespace nvfp4 {
 namespace {
 
-#ifndef KV_TARGET
-#define KV_TARGET 1024
-#endif
-#ifndef KV_FEW
-#define KV_FEW 32
-#endif
-#ifndef KV_FULL
-#define KV_FULL 4096
-#endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-#ifndef KV_DEPTH
-#define KV_DEPTH 2
-#endif
+constexpr int kDepth = 2;            // tiles of a wave in LDS: 3 leave room for half the waves, 10% slower
 constexpr int kMaxSplits = 1024;     // chunks of a row
-constexpr int kDepth = KV_DEPTH;     // tiles of a wave in LDS
+// Rows up to which k_kv_decode takes an item (in tiles of 16 or 32). Above, kv_prefill.hip shares the
+// conversion of a tile: 112 rows over 10596 positions take 1.1 times as long here.
+constexpr int kFewRows = 32;
+// The join gives a row a workgroup below this many rows, a wave above: 1536 rows of a few chunks take 5.2 us
+// instead of 9, 256 rows of 30 chunks 8 instead of 5.
+constexpr int kWideJoin = 1024;
 
 // A tile of 32 positions in LDS, as it is copied from the pages: the codes of [K half 0][K half 1]
 // [V half 0][V half 1], then their scale bytes in the same order. In K's rows the 16-byte pieces
@@ -543,134 +537,210 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
     }
 }
 
-// Joins the chunks of a row: one workgroup per (token row, query head). The chunks' factors go to LDS
-// first; then lanes of D / 4 columns, kThreads / (D / 4) chunks at a time, four loads in flight each.
-template <int D, bool BF16>
-__global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan) {
-    constexpr int C = D / 4, P = kThreads / C;           // column lanes, chunks at a time
-    __shared__ float factor[kMaxSplits];
-    __shared__ float red[kWaves], sums[kWaves];
-    __shared__ float4 acc[P][C];
+// What joins a row's chunks: where its outputs go, its chunks' statistics and outputs (chunk s at
+// s * stat_step and s * stat_step * D).
+struct JoinRow {
+    int64_t row;
+    uint8_t* dst;
+    const float2* stat;
+    const float* part;
+    int64_t stat_step;
+    int head, chunks;
+};
+
+// Number `index` of the rows to join (uniform); false if there is none or it has one chunk, which is
+// already its output.
+__device__ __forceinline__ bool find_row(const KvAttention& a, const KvPlan& plan, uint32_t index,
+                                         JoinRow& r) {
     const KvView& kv = a.kv;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t at = blockIdx.x / (uint32_t)a.q_heads;
-    const int hq = (int)(blockIdx.x - (uint32_t)at * (uint32_t)a.q_heads);
-    const int group = a.q_heads / kv.heads, head = hq / group;
+    const int64_t at = index / (uint32_t)a.q_heads;
+    const int hq = (int)(index - (uint32_t)at * (uint32_t)a.q_heads);
+    const int group = a.q_heads / kv.heads;
+    r.head = hq / group;
     const int64_t total = min((int64_t)a.b.cu[a.b.seqs], a.b.tokens);
     int item;
     int64_t j;
     if (plan.by_item) {
         item = (int)(at / a.max_q);
+        if (item >= a.b.seqs) return false;
         j = at - (int64_t)item * a.max_q;
     } else {
-        if (at >= total) return;
+        if (at >= total) return false;
         item = kv_find_item(a.b.cu, a.b.seqs, at);
         j = at - a.b.cu[item];
     }
     const int2 info = item_info(a)[item];
     const int64_t first = a.b.cu[item];
     const int n_new = (int)min((int64_t)a.b.cu[item + 1], total) - (int)first;
-    if (first < 0 || j < 0 || j >= min(n_new, a.max_q)) return;
-    const int64_t token = first + j, row = token * a.q_heads + hq;
-    const int r = (int)j * group + hq - head * group;
-    const int tile = r / plan.tile_rows, r_in = r - tile * plan.tile_rows;
-    const int rows = min(n_new, a.max_q) * group;
-    const int tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
+    if (first < 0 || j < 0 || j >= min(n_new, a.max_q)) return false;
+    const int64_t token = first + j;
+    r.row = token * a.q_heads + hq;
+    r.dst = static_cast<uint8_t*>(a.out) + token * a.out_stride_t + hq * a.out_stride_h;
+    const int q = (int)j * group + hq - r.head * group;
+    const int tile = q / plan.tile_rows, inside = q - tile * plan.tile_rows;
+    const int tiles = (min(n_new, a.max_q) * group + plan.tile_rows - 1) / plan.tile_rows;
     // chunk s of this row's tile: task info.x + s * tiles + (tiles - 1 - tile)
     const int task0 = info.x + tiles - 1 - tile;
-    const int chunks = min(min(info.y, kMaxSplits), (plan.tasks - task0 + tiles - 1) / tiles);
-    if (chunks <= 1) return;                              // already written
-    const int64_t stat_step = (int64_t)tiles * kv.heads * plan.tile_rows;
-    const float2* stat = part_stat(a, plan, task0, head) + r_in;
-    // the first chunks' outputs are on their way while the factors are made
-    const int c = threadIdx.x % C, p = threadIdx.x / C;
-    const float4* part = reinterpret_cast<const float4*>(part_out(a, plan, task0, head) + r_in * D) + c;
-    const int64_t step = stat_step * C;
-    float4 x[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        x[k] = p + k * P < chunks ? part[(p + k * P) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float mm = -__builtin_inff();
-    for (int s = threadIdx.x; s < chunks; s += kThreads) mm = fmaxf(mm, stat[s * stat_step].x);
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
-    if (lane == 0) red[wave] = mm;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) mm = fmaxf(mm, red[k]);
-    float l = 0.0f;
-    for (int s = threadIdx.x; s < chunks; s += kThreads) {
-        const float2 st = stat[s * stat_step];
-        const float f = st.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.x - mm);
-        factor[s] = f;
-        l = __builtin_fmaf(st.y, f, l);
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
-    if (lane == 0) sums[wave] = l;
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) l += sums[k];
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = p; s < chunks; s += 4 * P) {
-        if (s > p) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                x[k] = s + k * P < chunks ? part[(s + k * P) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float f = s + k * P < chunks ? factor[s + k * P] : 0.0f;
-            v.x = __builtin_fmaf(x[k].x, f, v.x);
-            v.y = __builtin_fmaf(x[k].y, f, v.y);
-            v.z = __builtin_fmaf(x[k].z, f, v.z);
-            v.w = __builtin_fmaf(x[k].w, f, v.w);
-        }
-    }
-    acc[p][c] = v;
-    __syncthreads();
-    if (p > 0) return;
-    v = acc[0][c];
-#pragma unroll
-    for (int k = 1; k < P; ++k) {
-        const float4 y = acc[k][c];
-        v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
-    }
-    const float z = l > 0.0f ? kv.S_v[head] / l : 0.0f;
-    uint8_t* dst = static_cast<uint8_t*>(a.out) + token * a.out_stride_t + hq * a.out_stride_h;
+    r.chunks = min(min(info.y, kMaxSplits), (plan.tasks - task0 + tiles - 1) / tiles);
+    if (r.chunks <= 1) return false;
+    r.stat_step = (int64_t)tiles * kv.heads * plan.tile_rows;
+    r.stat = part_stat(a, plan, task0, r.head) + inside;
+    r.part = part_out(a, plan, task0, r.head) + inside * kv.dim;
+    return true;
+}
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 fma4(float4 a, float f, float4 b) {
+    return make_float4(__builtin_fmaf(a.x, f, b.x), __builtin_fmaf(a.y, f, b.y),
+                       __builtin_fmaf(a.z, f, b.z), __builtin_fmaf(a.w, f, b.w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_row(const KvAttention& a, const JoinRow& r, int c, float4 v, float m,
+                                          float l) {
+    const float z = l > 0.0f ? a.kv.S_v[r.head] / l : 0.0f;
     if constexpr (BF16)
-        reinterpret_cast<uint2*>(dst)[c] =
+        reinterpret_cast<uint2*>(r.dst)[c] =
             make_uint2(bf16_pair(v.x * z, v.y * z), bf16_pair(v.z * z, v.w * z));
     else
-        reinterpret_cast<float4*>(dst)[c] = make_float4(v.x * z, v.y * z, v.z * z, v.w * z);
-    if (a.lse && c == 0) a.lse[row] = row_lse(mm, l);
+        reinterpret_cast<float4*>(r.dst)[c] = make_float4(v.x * z, v.y * z, v.z * z, v.w * z);
+    if (a.lse && c == 0) a.lse[r.row] = row_lse(m, l);
+}
+
+// Joins the chunks of a row. WIDE: one workgroup a row, for few rows of many chunks; else one wave a row. Its
+// lanes own D / 4 columns, (lanes) / (D / 4) chunks at a time, four loads in flight each, and the first
+// chunks' outputs are on their way while the factors are made.
+template <int D, bool BF16, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan) {
+    constexpr int C = D / 4, P = (WIDE ? kThreads : 64) / C;   // column lanes, chunks at a time
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    JoinRow r;
+    if (!find_row(a, plan, WIDE ? blockIdx.x : blockIdx.x * kWaves + wave, r)) return;
+    const int c = (WIDE ? (int)threadIdx.x : lane) % C, p = (WIDE ? (int)threadIdx.x : lane) / C;
+    const float4* part = reinterpret_cast<const float4*>(r.part) + c;
+    const int64_t step = r.stat_step * C;
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 x[4], v = none;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = p + k * P < r.chunks ? part[(p + k * P) * step] : none;
+    if constexpr (WIDE) {
+        __shared__ float factor[kMaxSplits], red[kWaves], sums[kWaves];
+        __shared__ float4 acc[P][C];
+        float mm = -__builtin_inff(), l = 0.0f;
+        for (int s = threadIdx.x; s < r.chunks; s += kThreads) mm = fmaxf(mm, r.stat[s * r.stat_step].x);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
+        if (lane == 0) red[wave] = mm;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) mm = fmaxf(mm, red[k]);
+        for (int s = threadIdx.x; s < r.chunks; s += kThreads) {
+            const float2 st = r.stat[s * r.stat_step];
+            const float f = st.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.x - mm);
+            factor[s] = f;
+            l = __builtin_fmaf(st.y, f, l);
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
+        if (lane == 0) sums[wave] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) l += sums[k];
+        for (int s = p; s < r.chunks; s += 4 * P) {
+            if (s > p) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[k] = s + k * P < r.chunks ? part[(s + k * P) * step] : none;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v = fma4(x[k], s + k * P < r.chunks ? factor[s + k * P] : 0.0f, v);
+        }
+        acc[p][c] = v;
+        __syncthreads();
+        if (p > 0) return;
+        v = acc[0][c];
+#pragma unroll
+        for (int k = 1; k < P; ++k) v = add4(v, acc[k][c]);
+        store_row<BF16>(a, r, c, v, mm, l);
+    } else {
+        // 64 chunks a round, a lane's statistics in registers
+        float m = -__builtin_inff(), l = 0.0f;
+        for (int s0 = 0; s0 < r.chunks; s0 += 64) {
+            const float2 st = s0 + lane < r.chunks ? r.stat[(s0 + lane) * r.stat_step]
+                                                   : make_float2(-__builtin_inff(), 0.0f);
+            float mn = st.x;
+#pragma unroll
+            for (int o = 32; o >= 1; o >>= 1) mn = fmaxf(mn, __shfl_xor(mn, o, 64));
+            mn = fmaxf(m, mn);
+            const float al = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - mn);
+            const float f = st.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.x - mn);
+            m = mn;
+            l = __builtin_fmaf(l, al, st.y * f);
+            v = make_float4(v.x * al, v.y * al, v.z * al, v.w * al);
+            const int n = min(64, r.chunks - s0);
+            for (int s1 = 0; s1 < n; s1 += 4 * P) {          // uniform: every lane joins each shuffle
+                const int s = s1 + p;
+                if (s0 + s1 > 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[k] = s + k * P < n ? part[(s0 + s + k * P) * step] : none;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float w = __shfl(f, (s + k * P) & 63, 64);
+                    v = fma4(x[k], s + k * P < n ? w : 0.0f, v);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
+#pragma unroll
+        for (int o = C; o < 64; o <<= 1)
+            v = add4(v, make_float4(__shfl_xor(v.x, o, 64), __shfl_xor(v.y, o, 64),
+                                    __shfl_xor(v.z, o, 64), __shfl_xor(v.w, o, 64)));
+        if (p == 0) store_row<BF16>(a, r, c, v, m, l);
+    }
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Row tiles of 16 or 32 rows; a batch that does not fill the chip by its tiles alone is split.
-// span: the most positions a row tile sees.
-KvPlan plan_of(int64_t heads, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,
+// How a batch is split: row tiles of 16, 32 or (prompts) 128 rows, and where these alone do not fill the chip,
+// chunks of positions. span: the most positions a row tile sees. Splitting costs the join: a decode batch
+// is split whenever its tiles leave workgroup slots empty (64 rows over up to 8192 positions: 63 us, not
+// split 165). A prompt's tiles are 128 rows whose partial outputs outweigh a few hundred positions: it
+// is split below 256 tiles and from 6 units on, into at least 2 units each (56 rows of 9 items over 496
+// positions: 25 us, split 38; one 2088-position item of 200 rows: 44 us, not split 70).
+KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,
                int64_t span) {
     const int64_t group = q_heads / heads, rows = max_q * group;
     KvPlan p{};
-    p.tile_rows = rows <= 16 ? 16 : rows <= KV_FEW ? 32 : kPrefillRows;
+    p.tile_rows = rows <= 16 ? 16 : rows <= kFewRows ? 32 : kPrefillRows;
     p.tiles = (int32_t)ceil_div(rows, p.tile_rows);
     p.tiles = p.tiles > 0 ? p.tiles : 1;
+    const bool prefill = p.tile_rows == kPrefillRows;
+    // workgroups that 256 compute units hold at once (registers and LDS)
+    const int64_t slots = 256 * (prefill ? (dim <= 128 ? 2 : 1)
+                                 : dim * p.tile_rows <= 128 * 16 ? 4 : dim * p.tile_rows <= 256 * 16 ? 2 : 1);
+    p.least = prefill ? 2 : 1;
     int64_t most = seqs * p.tiles;                       // tiles of all items, a head
     const int64_t by_rows = seqs + ceil_div(tokens * group, p.tile_rows);
     if (seqs <= kMaxScan) {
         most = most < by_rows ? most : by_rows;
-        if (most * heads < KV_FULL && span > kUnit) {
-            const int64_t target = ceil_div(KV_TARGET, heads);
-            p.target = (int32_t)(target < kMaxSplits ? target : kMaxSplits);
+        if (prefill ? most * heads < 256 && span > 6 * kUnit : most * heads < slots && span > kUnit) {
+            const int64_t target = (prefill ? 512 : slots) / heads, fit = slots / heads;
+            p.target = (int32_t)(target < 1 ? 1 : target < kMaxSplits ? target : kMaxSplits);
+            // tiles of a causal prompt differ in length: there more tasks than slots even out
+            p.fit = (int32_t)(p.tiles == 1 ? fit : 0);
         }
     }
     if (p.target > 0) {
-        // no tile has more chunks than units
-        const int64_t units = ceil_div(span, kUnit);
-        p.tasks = (int32_t)(most + p.target < most * units ? most + p.target : most * units);
+        // no tile has more chunks than its units allow
+        const int64_t chunks = ceil_div(ceil_div(span, kUnit), p.least);
+        p.tasks = (int32_t)(most + p.target < most * chunks ? most + p.target : most * chunks);
         p.by_item = seqs * max_q <= 2 * tokens;
     } else {
         p.tasks = (int32_t)(seqs * p.tiles);
@@ -693,11 +763,15 @@ hipError_t launch(const KvAttention& a, const KvPlan& p, hipStream_t stream) {
         hipLaunchKernelGGL((k_kv_decode<D, BF16, 2>), grid, dim3(kThreads), 0, stream, a, p);
     else
         launch_kv_prefill(a, p, stream);
-    if (p.target > 0)
-        hipLaunchKernelGGL((k_kv_join<D, BF16>),
-                           dim3((uint32_t)((p.by_item ? (int64_t)a.b.seqs * a.max_q : a.b.tokens) *
-                                           a.q_heads)),
-                           dim3(kThreads), 0, stream, a, p);
+    if (p.target > 0) {
+        const int64_t rows = (p.by_item ? (int64_t)a.b.seqs * a.max_q : a.b.tokens) * a.q_heads;
+        if (rows < kWideJoin)
+            hipLaunchKernelGGL((k_kv_join<D, BF16, true>), dim3((uint32_t)rows), dim3(kThreads), 0, stream,
+                               a, p);
+        else
+            hipLaunchKernelGGL((k_kv_join<D, BF16, false>), dim3((uint32_t)ceil_div(rows, kWaves)),
+                               dim3(kThreads), 0, stream, a, p);
+    }
     return hipGetLastError();
 }
 
@@ -717,14 +791,14 @@ bool kv_attention_fits(int64_t heads, int64_t q_heads, int64_t seqs, int64_t max
 
 size_t kv_attention_workspace_bytes(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads,
                                     int64_t seqs, int64_t max_q, int64_t max_kv) {
-    return space_of(plan_of(heads, tokens, q_heads, seqs, max_q, max_kv), heads, dim, seqs);
+    return space_of(plan_of(heads, dim, tokens, q_heads, seqs, max_q, max_kv), heads, dim, seqs);
 }
 
 hipError_t launch_kv_attention(const KvAttention& a, hipStream_t stream) {
     // a window bounds what a tile sees; the workspace is sized without it and so never too small
     int64_t span = a.max_kv;
     if (a.window > 0 && (int64_t)a.window + a.max_q + 31 < span) span = (int64_t)a.window + a.max_q + 31;
-    KvPlan p = plan_of(a.kv.heads, a.b.tokens, a.q_heads, a.b.seqs, a.max_q, span);
+    KvPlan p = plan_of(a.kv.heads, a.kv.dim, a.b.tokens, a.q_heads, a.b.seqs, a.max_q, span);
     gpr_divisor(a.kv.page / 16, p.page_magic, p.page_shift);
     return a.bf16 ? launch_dim<true>(a, p, stream) : launch_dim<false>(a, p, stream);
 }

@@ -167,8 +167,8 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // Work split. Rows of an item and head: (token j, query head of the group), row = j * group + head,
 // in tiles; the positions a tile sees in chunks. Lengths are known on the device only, and in a batch
 // they differ widely, so each workgroup finds its task itself: a wave sums the positions of all
-// tiles, which gives the chunk size that makes about `target` tasks a head, and then finds its
-// own in the prefix sum of the items' tasks. (A grid made for the longest item left most workgroups
+// tiles, which gives the chunk size that makes about `target` tasks a head (as many as run at once),
+// and then finds its own in the prefix sum of the items' tasks. (A grid made for the longest item left most workgroups
 // without work and the others unevenly spread: 4 sequences of up to 131072 positions took 81 us
 // that way and 57 us so.)
 constexpr int kUnit = 128;       // positions by which chunks are cut
@@ -179,6 +179,8 @@ struct KvPlan {
     int32_t tiles;           // row tiles of the largest item
     int32_t target;          // tasks a head aimed at; 0: no splitting, task = item * tiles + tile
     int32_t tasks;           // tasks a head at most
+    int32_t fit;             // tasks a head that run at once, where one round is wanted (else 0)
+    int32_t least;           // units of a chunk at least
     int32_t by_item;         // join: workgroups by (item, row of max_q) instead of by token row
     uint64_t page_magic;     // division of a 16-token unit by the units of a page
     uint32_t page_shift;
@@ -259,6 +261,10 @@ struct KvTask {
     int32_t begin, end;      // positions of the chunk
 };
 
+__device__ __forceinline__ int chunks_of(int units, int chunk) {
+    return max(1, (int)(((uint32_t)units + (uint32_t)chunk - 1u) / (uint32_t)chunk));
+}
+
 // The task of number w (uniform), found by the whole wave; false if there is none.
 __device__ __forceinline__ bool find_task(const KvAttention& a, const KvPlan& p, int w, KvTask& t) {
     const int lane = threadIdx.x & 63;
@@ -284,7 +290,15 @@ __device__ __forceinline__ bool find_task(const KvAttention& a, const KvPlan& p,
         // units a chunk: above sum / target whatever binary32 rounded, so that no item has more than
         // `target` chunks and all have at most `target` more than their tiles
         const float share = last_lane(wave_prefix(sum)) / (float)p.target;
-        const int chunk = (int)min(share * 1.001f, 1e9f) + 1;
+        int chunk = max((int)min(share * 1.001f, 1e9f) + 1, p.least);
+        // every item's chunks are rounded up: larger ones until all tasks run at once, if they can
+        if (p.fit > 0 && a.b.seqs <= 64 && last_lane(wave_prefix(tiles)) < p.fit) {
+            for (int i = 0; i < 16; ++i) {
+                const int all = last_lane(wave_prefix(tiles * chunks_of(units, chunk)));
+                if (all <= p.fit) break;
+                chunk += max(1, chunk >> 3);
+            }
+        }
         int before = 0;
         bool found = false;
         for (int i0 = 0; i0 < a.b.seqs && !found; i0 += 64) {
@@ -293,7 +307,7 @@ __device__ __forceinline__ bool find_task(const KvAttention& a, const KvPlan& p,
                 tiles = (mine.rows + p.tile_rows - 1) / p.tile_rows;
                 units = mine.rows > 0 ? units_of(tile_range(a, mine.len, mine.all_new, group, 0, mine.rows)) : 0;
             }
-            const int chunks = max(1, (int)(((int64_t)units + chunk - 1) / chunk));
+            const int chunks = chunks_of(units, chunk);
             const int tasks = tiles * chunks;
             const int incl = wave_prefix(tasks);
             const uint64_t past = __ballot(before + incl > w);

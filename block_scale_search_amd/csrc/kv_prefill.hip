@@ -20,12 +20,6 @@
 namespace nvfp4 {
 namespace {
 
-#ifndef KV_AHEAD
-#define KV_AHEAD 8
-#endif
-#ifndef KV_PV
-#define KV_PV 4
-#endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 64;            // positions of a tile: one 16-token unit a wave
@@ -288,7 +282,7 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
         if (t < lim_any && t + kTile > low_any) {        // the wave sees something of the tile
             // the first products of this tile, and in their shadow the conversion of the next: three
             // pieces to four steps. The operands are read kAhead steps ahead of their use.
-            constexpr int kSteps = 2 * NS, kAhead = kSteps < KV_AHEAD ? kSteps : KV_AHEAD;
+            constexpr int kSteps = 2 * NS, kAhead = kSteps < 4 ? kSteps : 4;
             UnitStore<D> store(other, raw, wave, lane);
             half8v k[kSteps];
             const auto read_k = [&](int z) {
@@ -362,14 +356,13 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
                     o[j] = mfma(v, hi[u].v, o[j]);
                     if constexpr (!BF16) o[j] = mfma(v, lo[u].v, o[j]);
                 }
-#if KV_PV > 0
-            __builtin_amdgcn_sched_group_barrier(0x100, KV_PV, 0);
+            // order of the block above: four LDS reads ahead, then one with each step's products
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
             for (int z = 0; z < 4 * NJ; ++z) {
                 __builtin_amdgcn_sched_group_barrier(0x8, BF16 ? 1 : 2, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
-#endif
         } else {
             UnitStore<D>(other, raw, wave, lane).all();
             if (i + 2 < tiles) load(i + 2);
