@@ -24,13 +24,13 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kDepth = 2;            // tiles of a wave in LDS: 3 leave room for half the waves, 10% slower
+constexpr int kDepth = 2;            // tiles of a wave in LDS (3: half the waves, 4 x 131072 positions 63 us, not 58)
 constexpr int kMaxSplits = 1024;     // chunks of a row
 // Rows up to which k_kv_decode takes an item (in tiles of 16 or 32). Above, kv_prefill.hip shares the
-// conversion of a tile: 112 rows over 10596 positions take 1.1 times as long here.
+// conversion of a tile: 46 items of 112 rows over 10596 positions 249 us, here 273.
 constexpr int kFewRows = 32;
-// The join gives a row a workgroup below this many rows, a wave above: 1536 rows of a few chunks take 5.2 us
-// instead of 9, 256 rows of 30 chunks 8 instead of 5.
+// The join gives a row a workgroup below this many rows, a wave above: 256 rows of 30 chunks 58.1 us in all
+// (a wave each 61.8), 1920 rows of 3 chunks 18 us (a workgroup each 22).
 constexpr int kWideJoin = 1024;
 
 // A tile of 32 positions in LDS, as it is copied from the pages: the codes of [K half 0][K half 1]
@@ -709,11 +709,12 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a batch is split: row tiles of 16, 32 or (prompts) 128 rows, and where these alone do not fill the chip,
-// chunks of positions. span: the most positions a row tile sees. Splitting costs the join: a decode batch
-// is split whenever its tiles leave workgroup slots empty (64 rows over up to 8192 positions: 63 us, not
-// split 165). A prompt's tiles are 128 rows whose partial outputs outweigh a few hundred positions: it
-// is split below 256 tiles and from 6 units on, into at least 2 units each (56 rows of 9 items over 496
-// positions: 25 us, split 38; one 2088-position item of 200 rows: 44 us, not split 70).
+// chunks of positions. span: the most positions a row tile sees. Splitting costs the join, about 5 us:
+// a decode batch is split where its tiles leave workgroup slots empty and a tile has more than 10 units
+// of work (64 rows over up to 8192 positions 63 us, not split 84; 4 over up to 131072 58, not split
+// 853; but 16 x 5 rows behind a window of 1024 18, not split 14). A prompt's tiles are 128 rows whose
+// partial outputs outweigh a few hundred positions: it is split below 256 tiles and from 6 units on, into
+// at least 2 units each (4 items of 200 rows over 2088 positions 41 us, not split 54).
 KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,
                int64_t span) {
     const int64_t group = q_heads / heads, rows = max_q * group;
@@ -730,7 +731,7 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
     const int64_t by_rows = seqs + ceil_div(tokens * group, p.tile_rows);
     if (seqs <= kMaxScan) {
         most = most < by_rows ? most : by_rows;
-        if (prefill ? most * heads < 256 && span > 6 * kUnit : most * heads < slots && span > kUnit) {
+        if (prefill ? most * heads < 256 && span > 6 * kUnit : most * heads < slots && span > (dim <= 128 ? 10 : 5) * kUnit) {
             const int64_t target = (prefill ? 512 : slots) / heads, fit = slots / heads;
             p.target = (int32_t)(target < 1 ? 1 : target < kMaxSplits ? target : kMaxSplits);
             // tiles of a causal prompt differ in length: there more tasks than slots even out
