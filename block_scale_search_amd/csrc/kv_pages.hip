@@ -134,19 +134,27 @@ __global__ __launch_bounds__(kBook) void k_kv_reserve(KvPool p, const int32_t* _
     }
     bool bad = false, many = false;
     int need = 0;                        // the slots are distinct, so all their pages are < 2^31
+    // the thread's item of the last batch, kept for the common call of one batch
+    int slot = 0, have = 0, add = 0, now = 0, rank = 0;
     for (int i0 = 0; i0 < n; i0 += kBook) {
         const int i = i0 + threadIdx.x;
-        int add = 0;
+        add = 0;
         if (i < n) {
-            const int old = length_of(p, slots[i]);
-            const int64_t now = (int64_t)old + counts[i];
-            if (counts[i] < 0 || now > (int64_t)p.max_pages * p.page) bad = true;
-            else add = pages_of(now, p.page) - pages_of(old, p.page);
+            slot = slots[i];
+            const int count = counts[i], old = length_of(p, slot);
+            const int64_t len = (int64_t)old + count;
+            if (count < 0 || len > (int64_t)p.max_pages * p.page) {
+                bad = true;
+            } else {
+                now = (int)len;
+                have = pages_of(old, p.page);
+                add = pages_of(now, p.page) - have;
+            }
         }
         many |= add > 1;
         int total;
-        const int before = block_exclusive<kWaves>(add, sums, total);
-        if (i < n) first[i] = need + before;
+        rank = need + block_exclusive<kWaves>(add, sums, total);
+        if (i < n) first[i] = rank;
         need += total;
     }
     if (__syncthreads_or(bad)) {
@@ -160,12 +168,24 @@ __global__ __launch_bounds__(kBook) void k_kv_reserve(KvPool p, const int32_t* _
     // an item's first page by its thread; the others, where an item takes more, one wave an item.
     // Lengths are written when every item's old one has been used.
     const bool any_many = __syncthreads_or(many);
+    if (n <= kBook && !any_many) {
+        if ((int)threadIdx.x < n) {
+            if (add > 0) {
+                const int page = list[rank];
+                p.table[(int64_t)slot * p.max_pages + have] = page;
+                p.refs[page] = 1;
+            }
+            p.lens[slot] = now;
+        }
+        if (threadIdx.x == 0) *status = NVFP4_KV_DONE;
+        return;
+    }
     for (int i = threadIdx.x; i < n; i += kBook) {
         const int s = slots[i], old = length_of(p, s), now = old + counts[i];
-        const int have = pages_of(old, p.page);
-        if (pages_of(now, p.page) > have) {
+        const int held = pages_of(old, p.page);
+        if (pages_of(now, p.page) > held) {
             const int page = list[first[i]];
-            p.table[(int64_t)s * p.max_pages + have] = page;
+            p.table[(int64_t)s * p.max_pages + held] = page;
             p.refs[page] = 1;
         }
         if (!any_many) p.lens[s] = now;
@@ -173,10 +193,10 @@ __global__ __launch_bounds__(kBook) void k_kv_reserve(KvPool p, const int32_t* _
     if (any_many) {
         for (int i = wave; i < n; i += kWaves) {
             const int s = slots[i], old = length_of(p, s), now = old + counts[i];
-            const int have = pages_of(old, p.page), add = pages_of(now, p.page) - have;
-            for (int k = lane + 1; k < add; k += 64) {
+            const int held = pages_of(old, p.page), more = pages_of(now, p.page) - held;
+            for (int k = lane + 1; k < more; k += 64) {
                 const int page = list[first[i] + k];
-                p.table[(int64_t)s * p.max_pages + have + k] = page;
+                p.table[(int64_t)s * p.max_pages + held + k] = page;
                 p.refs[page] = 1;
             }
         }
