@@ -107,6 +107,12 @@ nvfp4_status check_rows(const void* p, int esz, int64_t tokens, int64_t heads, i
     return NVFP4_OK;
 }
 
+// Positions a plan has to cover: what the caller says, and no more than the table holds.
+int64_t planned_kv(const nvfp4_kv_cache* c, int64_t max_kv) {
+    const int64_t cap = (int64_t)c->max_pages * c->page_size;
+    return max_kv < cap ? max_kv : cap;
+}
+
 int64_t planned_q(int64_t tokens, int64_t max_q) { return max_q < tokens ? max_q : tokens; }
 
 nvfp4_status check_attention_sizes(const nvfp4_kv_cache* c, int64_t tokens, int64_t q_heads,
@@ -117,16 +123,12 @@ nvfp4_status check_attention_sizes(const nvfp4_kv_cache* c, int64_t tokens, int6
     if (tokens >= kInt32 / q_heads || max_kv >= kInt32 || max_q >= kInt32 ||
         max_q * (q_heads / c->heads) >= (1 << 24))
         return NVFP4_ERR_SHAPE;
-    if (!nvfp4::kv_attention_fits(c->heads, q_heads, seqs, planned_q(tokens, max_q)))
+    if (!nvfp4::kv_attention_fits(c->heads, c->head_dim, tokens, q_heads, seqs, planned_q(tokens, max_q),
+                                  planned_kv(c, max_kv)))
         return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }
 
-// Positions a plan has to cover: what the caller says, and no more than the table holds.
-int64_t planned_kv(const nvfp4_kv_cache* c, int64_t max_kv) {
-    const int64_t cap = (int64_t)c->max_pages * c->page_size;
-    return max_kv < cap ? max_kv : cap;
-}
 
 }  // namespace
 

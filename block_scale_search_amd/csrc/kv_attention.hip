@@ -26,6 +26,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kDepth = 2;            // tiles of a wave in LDS (3: half the waves, 4 x 131072 positions 63 us, not 58)
 constexpr int kMaxSplits = 1024;     // chunks of a row
+constexpr int64_t kMaxGrid = (int64_t)1 << 24;   // workgroups: 2^32 threads a launch
 // Rows up to which k_kv_decode takes an item (in tiles of 16 or 32). Above, kv_prefill.hip shares the
 // conversion of a tile: 46 items of 112 rows over 10596 positions 249 us, here 273.
 constexpr int kFewRows = 32;
@@ -312,14 +313,14 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
         load_query<D, BF16>(raw[rt], static_cast<const uint8_t*>(a.q.p) + of.token * a.q.stride_t +
                                          of.head * a.q.stride_h, live, g);
         const int pos = job.work.len - all_new + (int)(of.token - first);
-        low[rt] = a.window > 0 ? pos - a.window + 1 : 0;
+        low[rt] = a.window > 0 ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
         lim[rt] = a.causal ? min(end, pos + 1) : end;
     }
     {
         const int p0 = job.work.len - all_new + row0 / group;
         const int p1 = job.work.len - all_new + (row0 + rows - 1) / group;
         if (a.causal) lim_all = min(end, p0 + 1);
-        if (a.window > 0) low_all = p1 - a.window + 1;
+        if (a.window > 0) low_all = (int)max((int64_t)p1 - a.window + 1, (int64_t)0);
     }
 
     f32x4 o[RT][NJ];
@@ -727,25 +728,30 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
     const int64_t slots = 256 * (prefill ? (dim <= 128 ? 2 : 1)
                                  : dim * p.tile_rows <= 128 * 16 ? 4 : dim * p.tile_rows <= 256 * 16 ? 2 : 1);
     p.least = prefill ? 2 : 1;
-    int64_t most = seqs * p.tiles;                       // tiles of all items, a head
+    // tiles of all items, a head: numbered by item and tile, or without gaps where bounds that are too wide
+    // would leave most of those numbers empty
+    int64_t most = seqs * p.tiles;
     const int64_t by_rows = seqs + ceil_div(tokens * group, p.tile_rows);
     if (seqs <= kMaxScan) {
+        p.scan = by_rows < most / 2;
         most = most < by_rows ? most : by_rows;
-        if (prefill ? most * heads < 256 && span > 6 * kUnit : most * heads < slots && span > (dim <= 128 ? 10 : 5) * kUnit) {
+        if (prefill ? most * heads < 256 && span > 6 * kUnit
+                    : most * heads < slots && span > (dim <= 128 ? 10 : 5) * kUnit) {
             const int64_t target = (prefill ? 512 : slots) / heads, fit = slots / heads;
             p.target = (int32_t)(target < 1 ? 1 : target < kMaxSplits ? target : kMaxSplits);
+            p.scan = 1;
             // tiles of a causal prompt differ in length: there more tasks than slots even out
             p.fit = (int32_t)(p.tiles == 1 ? fit : 0);
         }
     }
+    int64_t tasks = p.scan ? most : seqs * p.tiles;
     if (p.target > 0) {
         // no tile has more chunks than its units allow
         const int64_t chunks = ceil_div(ceil_div(span, kUnit), p.least);
-        p.tasks = (int32_t)(most + p.target < most * chunks ? most + p.target : most * chunks);
+        tasks = most + p.target < most * chunks ? most + p.target : most * chunks;
         p.by_item = seqs * max_q <= 2 * tokens;
-    } else {
-        p.tasks = (int32_t)(seqs * p.tiles);
     }
+    p.tasks = tasks < kMaxGrid / heads ? (int32_t)tasks : -1;
     return p;
 }
 
@@ -785,9 +791,9 @@ hipError_t launch_dim(const KvAttention& a, const KvPlan& p, hipStream_t stream)
 
 }  // namespace
 
-bool kv_attention_fits(int64_t heads, int64_t q_heads, int64_t seqs, int64_t max_q) {
-    const int64_t tiles = ceil_div(max_q * (q_heads / heads), 16);
-    return seqs * (tiles > 0 ? tiles : 1) + kMaxSplits < ((int64_t)1 << 31) / heads;
+bool kv_attention_fits(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs,
+                       int64_t max_q, int64_t max_kv) {
+    return plan_of(heads, dim, tokens, q_heads, seqs, max_q, max_kv).tasks >= 0;
 }
 
 size_t kv_attention_workspace_bytes(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads,

@@ -177,7 +177,8 @@ constexpr int kMaxScan = 1024;   // items up to which a task is found by scannin
 struct KvPlan {
     int32_t tile_rows;       // query rows of a workgroup
     int32_t tiles;           // row tiles of the largest item
-    int32_t target;          // tasks a head aimed at; 0: no splitting, task = item * tiles + tile
+    int32_t target;          // tasks a head aimed at; 0: no splitting
+    int32_t scan;            // tasks are numbered without gaps; else task = item * tiles + tile
     int32_t tasks;           // tasks a head at most
     int32_t fit;             // tasks a head that run at once, where one round is wanted (else 0)
     int32_t least;           // units of a chunk at least
@@ -201,7 +202,7 @@ __device__ __forceinline__ KvRange tile_range(const KvAttention& a, int len, int
     r.end = min(len, a.max_kv);
     const int first = len - rows_new + row0 / group;
     if (a.causal) r.end = min(r.end, len - rows_new + (row0 + rows - 1) / group + 1);
-    if (a.window > 0) r.begin = max(0, first - a.window + 1) & ~31;
+    if (a.window > 0) r.begin = (int)max((int64_t)0, (int64_t)first - a.window + 1) & ~31;
     r.end = max(r.end, r.begin);
     return r;
 }
@@ -271,7 +272,7 @@ __device__ __forceinline__ bool find_task(const KvAttention& a, const KvPlan& p,
     const int group = a.q_heads / a.kv.heads;
     KvWork mine;
     int inside;
-    if (p.target == 0) {
+    if (!p.scan) {
         t.item = w / p.tiles;
         mine = work_of(a, t.item, group);
         t.work = mine;
@@ -289,8 +290,8 @@ __device__ __forceinline__ bool find_task(const KvAttention& a, const KvPlan& p,
         }
         // units a chunk: above sum / target whatever binary32 rounded, so that no item has more than
         // `target` chunks and all have at most `target` more than their tiles
-        const float share = last_lane(wave_prefix(sum)) / (float)p.target;
-        int chunk = max((int)min(share * 1.001f, 1e9f) + 1, p.least);
+        const float share = last_lane(wave_prefix(sum)) / (float)max(p.target, 1);
+        int chunk = p.target > 0 ? max((int)min(share * 1.001f, 1e9f) + 1, p.least) : 0x7FFFFFFF;
         // every item's chunks are rounded up: larger ones until all tasks run at once, if they can
         if (p.fit > 0 && a.b.seqs <= 64 && last_lane(wave_prefix(tiles)) < p.fit) {
             for (int i = 0; i < 16; ++i) {

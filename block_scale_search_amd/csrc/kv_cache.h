@@ -57,8 +57,9 @@ struct KvAttention {
     float* lse;              // or null
     void* workspace;
 };
-// Whether the tasks of such a batch can be numbered in 31 bits.
-bool kv_attention_fits(int64_t heads, int64_t q_heads, int64_t seqs, int64_t max_q);
+// Whether such a batch fits one launch.
+bool kv_attention_fits(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs,
+                       int64_t max_q, int64_t max_kv);
 size_t kv_attention_workspace_bytes(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads,
                                     int64_t seqs, int64_t max_q, int64_t max_kv);
 hipError_t launch_kv_attention(const KvAttention& a, hipStream_t stream);

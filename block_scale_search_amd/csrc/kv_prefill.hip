@@ -246,7 +246,7 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
     load_query<D, BF16>(q, static_cast<const uint8_t*>(a.q.p) + of.token * a.q.stride_t + of.head * a.q.stride_h,
                         live, h, a.scale, kv.S_k[head]);
     const int pos = job.work.len - job.work.all_new + (int)(of.token - job.work.first);
-    const int low = a.window > 0 ? pos - a.window + 1 : 0;
+    const int low = a.window > 0 ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
     const int lim = a.causal ? min(end, pos + 1) : end;
     // every row of the wave sees low_all .. lim_all - 1, none anything outside low_any .. lim_any - 1
     int low_all = 0, lim_all = end, low_any = 0, lim_any = rows > 0 ? end : begin;
@@ -258,8 +258,8 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
             lim_any = min(end, p1 + 1);
         }
         if (a.window > 0) {
-            low_all = p1 - a.window + 1;
-            low_any = p0 - a.window + 1;
+            low_all = (int)max((int64_t)p1 - a.window + 1, (int64_t)0);
+            low_any = (int)max((int64_t)p0 - a.window + 1, (int64_t)0);
         }
     }
 

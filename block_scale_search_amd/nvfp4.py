@@ -101,6 +101,7 @@ for _name, (_args, _res) in _SIGS.items():
     _f.restype = _res
 
 EXPORTS = tuple(_SIGS)
+_KV = {n: getattr(_lib, n) for n in _SIGS if n.startswith("nvfp4_kv_")}
 
 
 class Nvfp4Error(RuntimeError):
@@ -467,6 +468,7 @@ class KVCache:
         self.heads, self.head_dim, self.page_size = heads, head_dim, page_size
         self.layers, self.num_pages, self.device = layers, num_pages, pages.device
         self.index = pages.get_device()
+        self.sizes = {}                      # workspace bytes by sizes: a pure function of them
         self.struct = KVCacheStruct(
             p(pages, "pages", (torch.uint8,)), layers, pages.stride(0), num_pages, pages.stride(1),
             heads, head_dim, page_size, table.shape[1], table.shape[0], p(table, "table", i32),
@@ -490,12 +492,15 @@ def _kv_run(cache: KVCache, fname: str, args: tuple, stream, prepare: bool):
     stream of the cache's device), with that device current."""
     index = cache.index
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    f = getattr(_lib, fname)
+    f = _KV[fname]
+    if not prepare and torch._C._cuda_getDevice() == index:
+        status = f(cache.ref, *args, s)
+        if status:
+            raise Nvfp4Error(status, fname)
+        return None
 
     def call():
         old = torch._C._cuda_getDevice()
-        if old == index:
-            return _check(f(cache.ref, *args, s), fname)
         torch.cuda.set_device(index)
         try:
             _check(f(cache.ref, *args, s), fname)
@@ -508,13 +513,14 @@ def _kv_ptr(cache: KVCache, t, name: str, dtype=None, numel: int | None = None):
     """Address of a tensor on the cache's device, of this dtype and (contiguous) at least numel elements."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a tensor on the GPU")
-    if dtype is not None and t.dtype is not dtype:
+    if not (isinstance(t, torch.Tensor) and t.get_device() == cache.index
+            and (dtype is None or t.dtype is dtype)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a tensor on the GPU")
+        if t.get_device() != cache.index:
+            raise ValueError(f"{name} must be on the cache's device {cache.device}")
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.get_device() != cache.index:
-        raise ValueError(f"{name} must be on the cache's device {cache.device}")
-    if numel is not None:
+    if numel is not None and (not t.is_contiguous() or t.numel() < numel):
         _need(t, numel, name)
     return t.data_ptr()
 
@@ -552,8 +558,15 @@ def nvfp4_kv_read(cache: KVCache, layer, K, V, tokens, cu_tokens, slots, seqs, s
 def nvfp4_kv_attention_workspace_size(cache: KVCache, dtype, tokens, q_heads, seqs, max_q,
                                       max_kv) -> int:
     """dtype: torch.bfloat16 or torch.float32."""
-    dt = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
-    return _lib.nvfp4_kv_attention_workspace_size(cache.ref, dt, tokens, q_heads, seqs, max_q, max_kv)
+    key = (dtype, tokens, q_heads, seqs, max_q, max_kv)
+    size = cache.sizes.get(key)
+    if size is None:
+        dt = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
+        size = _lib.nvfp4_kv_attention_workspace_size(cache.ref, dt, tokens, q_heads, seqs, max_q, max_kv)
+        if len(cache.sizes) >= 4096:
+            cache.sizes.clear()
+        cache.sizes[key] = size
+    return size
 
 
 def nvfp4_kv_attention(cache: KVCache, layer, Q, cu_tokens, slots, seqs, max_q, max_kv, scale,
@@ -580,7 +593,10 @@ def _kv_space(cache: KVCache, t):
 
 
 def nvfp4_kv_pages_workspace_size(cache: KVCache, n: int) -> int:
-    return _lib.nvfp4_kv_pages_workspace_size(cache.ref, n)
+    size = cache.sizes.get(n)
+    if size is None:
+        size = cache.sizes[n] = _lib.nvfp4_kv_pages_workspace_size(cache.ref, n)
+    return size
 
 
 def nvfp4_kv_reserve(cache: KVCache, slots, counts, n, status, workspace, stream=None, prepare=False):
@@ -828,6 +844,14 @@ def pack(W: torch.Tensor, scales: torch.Tensor, S: torch.Tensor, stream=None) ->
     return packed
 
 
+def _kv_empty(cache: KVCache, shape, dtype, stream):
+    """A tensor on the cache's device that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+
+
 def kv_append(cache: KVCache, layer: int, K: torch.Tensor, V: torch.Tensor, cu_tokens: torch.Tensor,
               slots: torch.Tensor | None = None, lo: int = -3, hi: int = 7, stream=None) -> None:
     """Quantise new rows K, V [tokens, heads, head_dim] into the pages of their slots: item i's rows
@@ -839,8 +863,7 @@ def kv_read(cache: KVCache, layer: int, tokens: int, cu_tokens: torch.Tensor,
             slots: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16, stream=None):
     """The cached values of the items' last rows: (K, V), each [tokens, heads, head_dim]."""
     shape = (tokens, cache.heads, cache.head_dim)
-    K = torch.empty(shape, dtype=dtype, device=cache.device)
-    V = torch.empty(shape, dtype=dtype, device=cache.device)
+    K, V = (_kv_empty(cache, shape, dtype, stream) for _ in range(2))
     nvfp4_kv_read(cache, layer, K, V, tokens, cu_tokens, slots, cu_tokens.numel() - 1, stream)
     return K, V
 
@@ -851,50 +874,50 @@ def kv_attention(cache: KVCache, layer: int, Q: torch.Tensor, cu_tokens: torch.T
                  window: int = 0, stream=None):
     """Attention of Q [tokens, q_heads, head_dim] over the cached keys and values; returns
     (out like Q, lse float32 [tokens, q_heads]). max_q and max_kv bound the items' rows and lengths
-    (None: all rows, the table's capacity; tight bounds split the work better)."""
+    (None: all rows, the table's capacity). Tight bounds give faster kernels: a decode step passes
+    max_q=1."""
     T, q_heads, D = Q.shape
     seqs = cu_tokens.numel() - 1
     max_q = T if max_q is None else max_q
     max_kv = cache.table.shape[1] * cache.page_size if max_kv is None else max_kv
-    out = torch.empty((T, q_heads, D), dtype=Q.dtype, device=Q.device)
-    lse = torch.empty((T, q_heads), dtype=torch.float32, device=Q.device)
+    out = _kv_empty(cache, (T, q_heads, D), Q.dtype, stream)
+    lse = _kv_empty(cache, (T, q_heads), torch.float32, stream)
     need = nvfp4_kv_attention_workspace_size(cache, Q.dtype, T, q_heads, seqs, max_q, max_kv)
-    ws = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+    ws = _kv_empty(cache, need, torch.uint8, stream) if need else None
     nvfp4_kv_attention(cache, layer, Q, cu_tokens, slots, seqs, max_q, max_kv,
                        D ** -0.5 if scale is None else scale, causal, window, out, lse, ws, stream)
     return out, lse
 
 
-def _pages_space(cache: KVCache, n: int):
-    return torch.empty(max(16, nvfp4_kv_pages_workspace_size(cache, n)), dtype=torch.uint8,
-                       device=cache.device)
+def _pages_space(cache: KVCache, n: int, stream):
+    return _kv_empty(cache, max(16, nvfp4_kv_pages_workspace_size(cache, n)), torch.uint8, stream)
 
 
 def kv_reserve(cache: KVCache, slots: torch.Tensor, counts: torch.Tensor, stream=None) -> torch.Tensor:
     """Room for counts[i] more tokens in slots[i]; returns the device status (KV_DONE, ...) [1]."""
-    status = torch.empty(1, dtype=torch.int32, device=cache.device)
+    status = _kv_empty(cache, 1, torch.int32, stream)
     n = slots.numel()
-    nvfp4_kv_reserve(cache, slots, counts, n, status, _pages_space(cache, n), stream)
+    nvfp4_kv_reserve(cache, slots, counts, n, status, _pages_space(cache, n, stream), stream)
     return status
 
 
 def kv_fork(cache: KVCache, parents: torch.Tensor, children: torch.Tensor, stream=None) -> torch.Tensor:
     """Empty slots children[i] become copies of parents[i]; returns the device status [1]."""
-    status = torch.empty(1, dtype=torch.int32, device=cache.device)
+    status = _kv_empty(cache, 1, torch.int32, stream)
     n = parents.numel()
-    nvfp4_kv_fork(cache, parents, children, n, status, _pages_space(cache, n), stream)
+    nvfp4_kv_fork(cache, parents, children, n, status, _pages_space(cache, n, stream), stream)
     return status
 
 
 def kv_free(cache: KVCache, slots: torch.Tensor, stream=None) -> torch.Tensor:
     """Empties slots; returns the device status [1]."""
-    status = torch.empty(1, dtype=torch.int32, device=cache.device)
+    status = _kv_empty(cache, 1, torch.int32, stream)
     nvfp4_kv_free(cache, slots, slots.numel(), status, stream)
     return status
 
 
 def kv_compact(cache: KVCache, stream=None) -> torch.Tensor:
     """Moves the used pages to the lowest numbers; returns how many there are, on the device [1]."""
-    used = torch.empty(1, dtype=torch.int32, device=cache.device)
-    nvfp4_kv_compact(cache, used, _pages_space(cache, 0), stream)
+    used = _kv_empty(cache, 1, torch.int32, stream)
+    nvfp4_kv_compact(cache, used, _pages_space(cache, 0, stream), stream)
     return used

@@ -462,7 +462,7 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  *
  * A slot (a sequence) is a row of `table`: position p of slot s lies in page table[s][p / page_size]
  * at row p % page_size. lens[s] is the slot's length in tokens. A slot holds exactly
- * ceil(lens / page_size) pages; the table's other entries are not read. refs[p] is the number of
+ * ceil(lens / page_size) pages; what the table's other entries hold does not matter. refs[p] is the number of
  * slots that hold page p (0: free). Full pages may be shared by several slots; a partly filled last
  * page belongs to one slot alone. A new cache has lens and refs zeroed and table filled with -1;
  * nvfp4_kv_reserve, _fork, _free and _compact keep these rules.
@@ -562,8 +562,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, int64_t layer, void* K, 
  *          aligned, no initialisation needed (may be NULL when that is 0).
  * Rows of O and lse behind cu_tokens[seqs] are left as they are.
  * Requires heads <= 65,535, q_heads a multiple of heads, tokens * q_heads < 2^31, seqs <= 65,535,
- * max_q * (q_heads / heads) < 2^24, seqs * heads * ceil(max_q * (q_heads / heads) / 16) < 2^31 -
- * 1,024 * heads (max_q here at most tokens). */
+ * max_q * (q_heads / heads) < 2^24, and fewer than 2^24 workgroups: with T = 128 query rows per
+ * workgroup (32 for up to 32 rows an item, 16 for up to 16), heads * (seqs + tokens * (q_heads /
+ * heads) / T + 1,024) for up to 1,024 items, heads * seqs * ceil(max_q * (q_heads / heads) / T) for more. */
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int dtype, int64_t tokens,
                                          int64_t q_heads, int64_t seqs, int64_t max_q,
                                          int64_t max_kv);

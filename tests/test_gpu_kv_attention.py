@@ -57,10 +57,34 @@ def test_windows(nv, window, new):
     _run(nv, [300, 5, 90], new, 1, 3, 64, 32, torch.float32, window=window, seed=window)
 
 
-def test_a_long_slot_beside_short_ones(nv):
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_long_slot_beside_short_ones(nv, dim, dtype):
     lens = [7000, 1, 300, 2049]
     for new in ([1, 1, 1, 1], [5, 1, 3, 2], [70, 1, 64, 33]):
-        _run(nv, lens, new, 2, 4, 128, 64, torch.bfloat16, seed=len(new) + new[0])
+        _run(nv, lens, new, 2, 4, dim, 64, dtype, seed=len(new) + new[0], max_q=max(new))
+
+
+@pytest.mark.parametrize("seqs", [65, 200, 1030])
+def test_many_items(nv, seqs):
+    """More items than a wave has lanes, and more than are scanned: short ones, empty ones, a long one."""
+    lens = [0 if i % 11 == 5 else 1 + (i * 37) % 50 for i in range(seqs)]
+    lens[seqs - 3] = 2600 if seqs < 1000 else 300
+    lens[70 % seqs] = 1500 if seqs < 1000 else 90
+    _run(nv, lens, [1] * seqs, 1, 4, 64, 16, torch.bfloat16, seed=seqs, max_q=1)
+    new = [min(i % 4, t) for i, t in enumerate(lens)]
+    _run(nv, lens, new, 1, 6, 64, 16, torch.float32, seed=seqs, max_q=3)       # two tiles of 16 rows
+    if seqs < 1000:
+        new[seqs - 3], new[2] = 150, min(30, lens[2])
+        _run(nv, lens, new, 1, 2, 64, 16, torch.bfloat16, seed=seqs, max_q=150)
+        _run(nv, lens, new, 1, 2, 64, 16, torch.bfloat16, seed=seqs)            # bounds far too wide
+
+
+def test_windows_beyond_every_length(nv):
+    """Windows as large as int32 and int64, rows before the first position among those that see some."""
+    for window in ((1 << 31) - 1, (1 << 31) - 70000, 1 << 40):
+        for new in ([9, 1], [60, 40]):
+            _run(nv, [5, 40], new, 1, 4, 64, 16, torch.bfloat16, window=window, seed=3)
 
 
 def test_rows_that_see_nothing(nv):

@@ -30,7 +30,7 @@ def _moved(before, copies, record):
 
 @pytest.mark.parametrize("seed,num_pages,page,slots,width,stride", [
     (1, 40, 16, 12, 9, None), (2, 300, 32, 40, 16, 2304 * 2 + 16), (3, 9000, 16, 700, 40, None),
-    (4, 17, 16, 5, 17, None)])
+    (4, 17, 16, 5, 17, None), (5, 20000, 16, 900, 40, None)])
 def test_random_history(nv, seed, num_pages, page, slots, width, stride):
     r = random.Random(seed)
     c, pool = _new(nv, num_pages, page, slots, width, stride=stride)
