@@ -740,8 +740,7 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
             const int64_t target = (prefill ? 512 : slots) / heads, fit = slots / heads;
             p.target = (int32_t)(target < 1 ? 1 : target < kMaxSplits ? target : kMaxSplits);
             p.scan = 1;
-            // tiles of a causal prompt differ in length: there more tasks than slots even out
-            p.fit = (int32_t)(p.tiles == 1 ? fit : 0);
+            p.fit = (int32_t)(fit < 1 ? 1 : fit);
         }
     }
     int64_t tasks = p.scan ? most : seqs * p.tiles;

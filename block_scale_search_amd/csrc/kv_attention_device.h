@@ -180,7 +180,7 @@ struct KvPlan {
     int32_t target;          // tasks a head aimed at; 0: no splitting
     int32_t scan;            // tasks are numbered without gaps; else task = item * tiles + tile
     int32_t tasks;           // tasks a head at most
-    int32_t fit;             // tasks a head that run at once, where one round is wanted (else 0)
+    int32_t fit;             // tasks a head that run at once
     int32_t least;           // units of a chunk at least
     int32_t by_item;         // join: workgroups by (item, row of max_q) instead of by token row
     uint64_t page_magic;     // division of a 16-token unit by the units of a page
@@ -292,12 +292,33 @@ __device__ __forceinline__ bool find_task(const KvAttention& a, const KvPlan& p,
         // `target` chunks and all have at most `target` more than their tiles
         const float share = last_lane(wave_prefix(sum)) / (float)max(p.target, 1);
         int chunk = p.target > 0 ? max((int)min(share * 1.001f, 1e9f) + 1, p.least) : 0x7FFFFFFF;
-        // every item's chunks are rounded up: larger ones until all tasks run at once, if they can
-        if (p.fit > 0 && a.b.seqs <= 64 && last_lane(wave_prefix(tiles)) < p.fit) {
-            for (int i = 0; i < 16; ++i) {
-                const int all = last_lane(wave_prefix(tiles * chunks_of(units, chunk)));
-                if (all <= p.fit) break;
-                chunk += max(1, chunk >> 3);
+        if (p.target > 0 && a.b.seqs <= 64) {
+            if (p.tiles > 1) {
+                // prompts: the longest item in k chunks, k such that the rounds of workgroups times a chunk's
+                // length (and a unit's worth of start) is least (8 items of up to 1000 rows over up to 8000
+                // positions, 4 heads of 4, 256 wide: 261 us; with `target` tasks, whatever their rounds, 318)
+                int longest = units;
+#pragma unroll
+                for (int o = 32; o >= 1; o >>= 1) longest = max(longest, __shfl_xor(longest, o, 64));
+                float best = __builtin_inff();
+                for (int k = 1; k <= 16; ++k) {
+                    const int size = max((longest + k - 1) / k, p.least);
+                    const int all = last_lane(wave_prefix(tiles * chunks_of(units, size)));
+                    if (all > p.tasks) break;
+                    const float cost = (float)((all + p.fit - 1) / p.fit) * (float)(size + 1);
+                    if (cost < best) {
+                        best = cost;
+                        chunk = size;
+                    }
+                    if (size == p.least) break;
+                }
+            } else if (last_lane(wave_prefix(tiles)) < p.fit) {
+                // every item's chunks are rounded up: larger ones until all tasks run at once, if they can
+                for (int i = 0; i < 16; ++i) {
+                    const int all = last_lane(wave_prefix(tiles * chunks_of(units, chunk)));
+                    if (all <= p.fit) break;
+                    chunk += max(1, chunk >> 3);
+                }
             }
         }
         int before = 0;
