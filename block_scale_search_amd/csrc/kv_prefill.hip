@@ -10,8 +10,16 @@
 // the logits of row n at positions 8 i + 4 h .. + 3, and those registers are P^T's operand as they
 // are, once V's positions are stored in that order (V's row holds, for each 16 positions, the blocks
 // of four 0, 2 for h = 0 and 1, 3 for h = 1).
-// Both LDS tiles permute the 16-byte pieces of a row by its number, so that reads and writes use
-// all banks.
+// Both LDS tiles permute the 16-byte pieces of a row so that 16 lanes that read a piece, and 8 that write
+// pieces of K, use all banks (4 heads of 4, 256 wide, two prompts of 4096 rows over 8192 positions: 1027 us,
+// with a permutation that only the reads need 1088).
+//
+// Rates (one MI355X): two prompts of 8192 rows, 8 heads of 4, 128 wide, bf16: 1.14 to 1.20 ms with the
+// clock, 920 to 965 TFLOP/s of the pairs that causal rows see; the matrix units are busy 46% of the cycles, vector arithmetic 62%, one or the
+// other 83%. 64 wide the exponentials weigh twice as much against the products (two prompts of 4096
+// rows over 8192 positions, 4 heads of 4: 313 us; 128 wide 472 us, 256 wide 1027 us). 256 wide a wave has a
+// SIMD for itself (registers and LDS), so its waits are not covered; making a tile's logits while the
+// previous tile's become weights gave nothing there (1059 us) nor 128 wide.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"
@@ -39,8 +47,8 @@ struct Lds {
     // K: piece c (8 values) of token t
     static __device__ __forceinline__ int k(int t, int c) {
         constexpr int P = D / 8;
-        const int f = D == 64 ? (t >> 1) & 7 : t & 15;
-        return (t * P + (c ^ f)) * 16;
+        const int f = D == 64 ? ((t >> 1) & 7) ^ (t & 1) : t & 15;
+        return (t * P + (c ^ f ^ (c >> 3 << 1))) * 16;
     }
     // V: piece c (8 positions) of row r
     static __device__ __forceinline__ int v(int r, int c) {
@@ -49,7 +57,10 @@ struct Lds {
 };
 
 // Lane offsets of a unit's codes and scales in a record, without its first row: token lane / 4 and a
-// quarter of its values for K, values of 4 tokens (block lane / 16, n = lane % 16) for V.
+// quarter of its values for K; for V, values of column lane % 16 of 4 tokens, block value_block(lane): the
+// blocks 0 and 2, whose 8 bytes lie side by side in LDS, in the lower half of the wave.
+__device__ __forceinline__ int value_block(int lane) { return (lane >> 5) | ((lane >> 3) & 2); }
+
 struct UnitOffsets {
     uint32_t k, v, ks, vs;
 };
@@ -60,9 +71,10 @@ __device__ __forceinline__ UnitOffsets unit_offsets(const KvView& kv, int head, 
     const uint32_t codes = (uint32_t)head * kv.page * (D / 2), scales = (uint32_t)head * kv.page * (D / 16);
     UnitOffsets o;
     o.k = codes + lane * (D / 8);
-    o.v = o.k + region;
+    const int block = value_block(lane), n = lane & 15;
+    o.v = codes + region + (block * 16 + n) * (D / 8);
     o.ks = 2 * region + scales + lane * (D / 64);
-    o.vs = 2 * region + (region >> 3) + scales + ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4;
+    o.vs = 2 * region + (region >> 3) + scales + (block * (D / 16) + n * D / 256) * 4;
     return o;
 }
 
@@ -114,8 +126,8 @@ struct UnitStore {
         t = 16 * wave + (lane >> 2);
         first = (lane & 3) * (D / 32);
         n = lane & 15;
-        c = 2 * wave + ((lane >> 4) & 1);
-        high = (lane >> 5) * 8;
+        c = 2 * wave + (value_block(lane) & 1);
+        high = (value_block(lane) >> 1) * 8;
     }
     template <int I>
     __device__ __forceinline__ void piece() {
