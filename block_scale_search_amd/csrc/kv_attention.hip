@@ -1,17 +1,25 @@
 // Attention over the paged NVFP4 key/value cache for gfx950.
 //
 // Few rows per (item, key/value head) - decode steps and drafts: k_kv_decode. A wave owns tiles of 32
-// positions and 16 RT query rows, with everything in registers. S^T = K Q^T puts a query row in a
-// lane column: the f16 MFMA 16x16x32 gives lane (n, g) = (lane % 16, lane / 16) the logits of row n
-// at positions 4g .. 4g + 3 of each half tile. O^T = V^T P^T needs, in that same lane, the weights of row n
-// at 8 positions: any 8, as long as V's operand uses the same ones, so the logits' registers are the
-// weights' registers and no lane exchanges anything. V's operand then holds, for lane (n, g), the
-// positions 4g .. 4g + 3 of both half tiles and the values d = n D/16 + j of tile j: the record
-// layout keeps exactly those codes together, 4 tokens x D/16 values in one load.
+// positions and 16 RT query rows. S^T = K Q^T puts a query row in a lane column: the f16 MFMA 16x16x32
+// gives lane (n, g) = (lane % 16, lane / 16) the logits of row n at positions 4g .. 4g + 3 of each half
+// tile. O^T = V^T P^T needs, in that same lane, the weights of row n at 8 positions: any 8, as long as
+// V's operand uses the same ones, so the logits' registers are the weights' registers and no lane
+// exchanges anything. V's operand then holds, for lane (n, g), the positions 4g .. 4g + 3 of both half
+// tiles and the values d = n D/16 + j of tile j: the record layout keeps exactly those codes together,
+// 4 tokens x D/16 values in one load.
 // A row's running maximum is only raised when a logit exceeds it by more than 2^7 (weights are
 // scaled by 2^8 and stay below 2^15), so most tiles need no cross-lane step and no rescaling.
 // The waves of a workgroup take tiles in turn and are joined in LDS; the chunks of a long
 // sequence are joined by k_kv_join.
+//
+// What bounds it is HBM, and before that the loads' order: read from the pages in the operands' order, a tile
+// touches each 128-byte line several times, and a touch of a line that is still on its way waits for it. So a
+// wave copies whole tiles into its own ring in LDS, each line once and one tile ahead, and reads operands
+// there. 64 rows of 4 heads over up to 8192 positions, 8 key/value heads, 128 wide (247.5 MB): 54 us
+// (4.6 TB/s; straight from the pages 72) and the join 5; 4 rows of 8 over up to 131072 (238 MB): 48
+// (5.0 TB/s) and 6. A large copy runs at 5.0 TB/s. Short caches are bound by the chain of launch, task,
+// length, page and tile: one row over 1023 positions 12 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -28,10 +36,11 @@ constexpr int kDepth = 2;            // tiles of a wave in LDS (3: half the wave
 constexpr int kMaxSplits = 1024;     // chunks of a row
 constexpr int64_t kMaxGrid = (int64_t)1 << 24;   // workgroups: 2^32 threads a launch
 // Rows up to which k_kv_decode takes an item (in tiles of 16 or 32). Above, kv_prefill.hip shares the
-// conversion of a tile: 46 items of 112 rows over 10596 positions 249 us, here 273.
+// conversion of a tile: 46 items of 112 rows over up to 10596 positions, 2 heads, 54 us (here 74), of 40
+// rows 42 (here 42).
 constexpr int kFewRows = 32;
-// The join gives a row a workgroup below this many rows, a wave above: 256 rows of 30 chunks 58.1 us in all
-// (a wave each 61.8), 1920 rows of 3 chunks 18 us (a workgroup each 22).
+// The join gives a row a workgroup below this many rows, a wave above: 256 rows of 33 chunks 58.5 us in all
+// (a wave each 62.8), 1920 rows of few chunks 17 us (a workgroup each 21).
 constexpr int kWideJoin = 1024;
 
 // A tile of 32 positions in LDS, as it is copied from the pages: the codes of [K half 0][K half 1]
@@ -511,7 +520,7 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
 #pragma unroll
                 for (int k = 0; k < kWaves; ++k) {
                     const float2 sk = stat[k][16 * rt + r];
-                    if (sk.x != -__builtin_inff()) rl += sk.y * __builtin_amdgcn_exp2f(sk.x - rm);
+                    if (sk.y != 0.0f) rl += sk.y * __builtin_amdgcn_exp2f(sk.x - rm);
                     const float4 x = *reinterpret_cast<const float4*>(&joined[k][r][c]);
                     v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
                 }
@@ -519,7 +528,7 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
                 const RowAt of = row_at(first, head, group, row0 + 16 * rt + r);
                 if (whole) {
                     const int64_t row = of.token * a.q_heads + of.head;
-                    const float z = rl > 0.0f ? S_v / rl : 0.0f;
+                    const float z = rl == 0.0f ? 0.0f : S_v / rl;
                     uint8_t* dst = static_cast<uint8_t*>(a.out) + of.token * a.out_stride_t +
                                    of.head * a.out_stride_h;
                     if constexpr (BF16)
@@ -601,7 +610,7 @@ __device__ __forceinline__ float4 fma4(float4 a, float f, float4 b) {
 template <bool BF16>
 __device__ __forceinline__ void store_row(const KvAttention& a, const JoinRow& r, int c, float4 v, float m,
                                           float l) {
-    const float z = l > 0.0f ? a.kv.S_v[r.head] / l : 0.0f;
+    const float z = l == 0.0f ? 0.0f : a.kv.S_v[r.head] / l;
     if constexpr (BF16)
         reinterpret_cast<uint2*>(r.dst)[c] =
             make_uint2(bf16_pair(v.x * z, v.y * z), bf16_pair(v.z * z, v.w * z));
@@ -712,10 +721,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // How a batch is split: row tiles of 16, 32 or (prompts) 128 rows, and where these alone do not fill the chip,
 // chunks of positions. span: the most positions a row tile sees. Splitting costs the join, about 5 us:
 // a decode batch is split where its tiles leave workgroup slots empty and a tile has more than 10 units
-// of work (64 rows over up to 8192 positions 63 us, not split 84; 4 over up to 131072 58, not split
-// 853; but 16 x 5 rows behind a window of 1024 18, not split 14). A prompt's tiles are 128 rows whose
+// of work (64 rows over up to 8192 positions 63 us, not split 85; 4 over up to 131072 58, not split
+// 855; but 16 x 5 rows behind a window of 1024 19, not split 14). A prompt's tiles are 128 rows whose
 // partial outputs outweigh a few hundred positions: it is split below 256 tiles and from 6 units on, into
-// at least 2 units each (4 items of 200 rows over 2088 positions 41 us, not split 54).
+// at least 2 units each (4 items of 200 rows over up to 2088 positions 26 us, not split 55).
 KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,
                int64_t span) {
     const int64_t group = q_heads / heads, rows = max_q * group;

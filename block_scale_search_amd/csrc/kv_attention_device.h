@@ -76,11 +76,11 @@ __device__ __forceinline__ int row_exponent(float top) {
     return min(15 - __builtin_amdgcn_frexp_expf(top), 126);
 }
 
-// One rounding to bf16, to nearest even, of finite values.
+// One rounding to bf16, to nearest even; NaN of any bits stays NaN.
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     const auto r = [](float v) {
         const uint32_t u = __float_as_uint(v);
-        return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+        return v == v ? (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16 : 0x7FC0u;
     };
     return r(a) | (r(b) << 16);
 }
@@ -159,18 +159,19 @@ __device__ __forceinline__ RowAt row_at(int64_t first, int head, int group, int 
     return RowAt{first + j, head * group + row - j * group};
 }
 
-// lse of a row from its maximum (log2, the weights' scale of 2^kUp apart) and sum.
+// lse of a row from its maximum (log2, the weights' scale of 2^kUp apart) and sum; a sum of zero is a row
+// that sees nothing, a NaN (of a query) stays one.
 __device__ __forceinline__ float row_lse(float m, float l) {
-    return l > 0.0f ? (m - kUp + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
+    return l == 0.0f ? -__builtin_inff() : (m - kUp + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Work split. Rows of an item and head: (token j, query head of the group), row = j * group + head,
 // in tiles; the positions a tile sees in chunks. Lengths are known on the device only, and in a batch
 // they differ widely, so each workgroup finds its task itself: a wave sums the positions of all
 // tiles, which gives the chunk size that makes about `target` tasks a head (as many as run at once),
-// and then finds its own in the prefix sum of the items' tasks. (A grid made for the longest item left most workgroups
-// without work and the others unevenly spread: 4 sequences of up to 131072 positions took 81 us
-// that way and 57 us so.)
+// and then finds its own in the prefix sum of the items' tasks. (A grid made for the longest item left most
+// workgroups without work and the others unevenly spread: 4 sequences of up to 131072 positions took 81 us
+// that way and 58 us so.)
 constexpr int kUnit = 128;       // positions by which chunks are cut
 constexpr int kMaxScan = 1024;   // items up to which a task is found by scanning them
 

@@ -15,8 +15,8 @@
 // with a permutation that only the reads need 1088).
 //
 // Rates (one MI355X): two prompts of 8192 rows, 8 heads of 4, 128 wide, bf16: 1.14 to 1.20 ms with the
-// clock, 920 to 965 TFLOP/s of the pairs that causal rows see; the matrix units are busy 46% of the cycles, vector arithmetic 62%, one or the
-// other 83%. 64 wide the exponentials weigh twice as much against the products (two prompts of 4096
+// clock, 920 to 965 TFLOP/s of the pairs that causal rows see; the matrix units are busy 46% of the cycles,
+// vector arithmetic 62%, one or the other 83%. 64 wide the exponentials weigh twice as much against the products (two prompts of 4096
 // rows over 8192 positions, 4 heads of 4: 313 us; 128 wide 472 us, 256 wide 1027 us). 256 wide a wave has a
 // SIMD for itself (registers and LDS), so its waits are not covered; making a tile's logits while the
 // previous tile's become weights gave nothing there (1059 us) nor 128 wide.
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
     if (!live) return;
     // o[j][i]: V's row 32 j + 8 (i / 4) + 4 h + i % 4 = 16 e + c, the value d = c D/16 + e: for each of the
     // lane's eight c, D/16 values in a row
-    const float z = whole ? (l > 0.0f ? kv.S_v[head] / l : 0.0f) : 1.0f;
+    const float z = whole ? (l == 0.0f ? 0.0f : kv.S_v[head] / l) : 1.0f;
     uint8_t* dst = static_cast<uint8_t*>(a.out) + of.token * a.out_stride_t + of.head * a.out_stride_h;
     float* part = whole ? nullptr : part_out(a, plan, task, head) + (row_first + n) * D;
     if (h == 0) {

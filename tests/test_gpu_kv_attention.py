@@ -154,6 +154,23 @@ def test_queries_of_every_size(nv):
     check_attention(out, lse, attention(c, 0, Q, [0, 4], [0], 1e-30, True, 0))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,new", [([90, 40], [1, 1]), ([90, 40], [6, 3]), ([90, 40], [60, 40]),
+                                      ([5000, 40], [1, 1]), ([5000, 2000], [5, 2]), ([5000, 2000], [300, 80])])
+def test_nan_queries_stay_in_their_rows(nv, lens, new, dtype):
+    """A row with a NaN, of any bits, is NaN throughout and its lse too; every other row keeps its bytes."""
+    c, Q, cu, out, lse = _run(nv, lens, new, 2, 4, 128, 32, dtype, max_q=max(new))
+    bad = torch.zeros(Q.shape[:2], dtype=torch.bool)
+    for k, (t, h) in enumerate([(0, 1), (cu[1] - 1, 6), (cu[-1] - 1, 3), (cu[-1] // 2, 0)]):
+        bits = Q[t, h].view(torch.int16 if dtype == torch.bfloat16 else torch.int32)
+        bits[(37 * k) % 128] = [0x7FFF, -1, 0x7FC0, 0x7F81][k] if dtype == torch.bfloat16 else \
+            [0x7FFFFFFF, -1, 0x7FC00000, 0x7F800001][k]
+        bad[t, h] = True
+    got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    assert torch.isnan(got[bad]).all() and torch.isnan(glse[bad]).all()
+    assert torch.equal(got[~bad], out[~bad]) and torch.equal(glse[~bad], lse[~bad])
+
+
 def test_sharp_and_flat_rows(nv):
     """Logits of hundreds (one position takes all), and of nothing (every position the same)."""
     for scale in (30.0, 1e-20):
