@@ -581,8 +581,10 @@ __device__ __forceinline__ bool find_row(const KvAttention& a, const KvPlan& pla
     }
     const int2 info = item_info(a)[item];
     const int64_t first = a.b.cu[item];
-    const int n_new = (int)min((int64_t)a.b.cu[item + 1], total) - (int)first;
-    if (first < 0 || j < 0 || j >= min(n_new, a.max_q)) return false;
+    const int64_t last = min((int64_t)a.b.cu[item + 1], total);
+    if (first < 0 || last <= first) return false;
+    const int n_new = (int)(last - first);
+    if (j < 0 || j >= min(n_new, a.max_q)) return false;
     const int64_t token = first + j;
     r.row = token * a.q_heads + hq;
     r.dst = static_cast<uint8_t*>(a.out) + token * a.out_stride_t + hq * a.out_stride_h;
@@ -592,7 +594,7 @@ __device__ __forceinline__ bool find_row(const KvAttention& a, const KvPlan& pla
     // chunk s of this row's tile: task info.x + s * tiles + (tiles - 1 - tile)
     const int task0 = info.x + tiles - 1 - tile;
     r.chunks = min(min(info.y, kMaxSplits), (plan.tasks - task0 + tiles - 1) / tiles);
-    if (r.chunks <= 1) return false;
+    if (task0 < 0 || r.chunks <= 1) return false;        // (offsets that overlap: no task may have said)
     r.stat_step = (int64_t)tiles * kv.heads * plan.tile_rows;
     r.stat = part_stat(a, plan, task0, r.head) + inside;
     r.part = part_out(a, plan, task0, r.head) + inside * kv.dim;

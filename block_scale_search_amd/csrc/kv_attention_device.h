@@ -224,11 +224,12 @@ __device__ __forceinline__ KvWork work_of(const KvAttention& a, int i, int group
     const int32_t total = (int32_t)min((int64_t)a.b.cu[a.b.seqs], a.b.tokens);
     const int32_t next = a.b.cu[i + 1];
     w.first = a.b.cu[i];
-    w.all_new = next - w.first;
+    w.all_new = (int32_t)((uint32_t)next - (uint32_t)w.first);
     const KvItem it = kv_item(a.kv, a.b, i);
     w.slot = it.slot;
     w.len = it.len;
-    w.rows = w.first < 0 ? 0 : max(0, min(min(next, total) - w.first, a.max_q)) * group;
+    const int32_t last = min(next, total);
+    w.rows = w.first < 0 || last <= w.first ? 0 : min(last - w.first, a.max_q) * group;
     return w;
 }
 

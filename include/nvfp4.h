@@ -489,7 +489,8 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  * and every layer's append, read and attention then use the same lengths. The device contents are
  * checked where a bad one could reach memory outside the cache: an item whose slot is outside
  * 0 .. max_slots - 1 has length 0, lengths are clamped to 0 .. max_pages * page_size, and a position
- * that is negative or whose table entry is outside 0 .. num_pages - 1 is not in the cache.
+ * that is negative or whose table entry is outside 0 .. num_pages - 1 is not in the cache. Offsets
+ * that are no such partition give unspecified values in the token rows, nothing outside them.
  * ------------------------------------------------------------------------------------------- */
 typedef struct nvfp4_kv_cache {
     uint8_t* pages;          /* device, [layers][num_pages] records */

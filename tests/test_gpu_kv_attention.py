@@ -204,6 +204,27 @@ def test_strides_streams_and_rows_behind_the_last(nv):
         assert bool((O[27:] == 7).all()) and bool((lse[27:] == 7).all())
 
 
+@pytest.mark.parametrize("offsets", [[0, -(1 << 31), 20, 40], [3, 1, 60, 7], [0, 40, 0, 40],
+                                     [-5, 9, 1 << 30, 40], [0, 10, 20, (1 << 31) - 1],
+                                     [0, 10, 20, -1], [40, 40, 40, 40]])
+def test_offsets_that_are_no_partition(nv, offsets):
+    """Nothing outside the batch's rows and the cache is written, whatever the offsets hold."""
+    c = make_cache(nv, [3000, 90, 40], 2, 128, 16)
+    fill_cache(nv, c, [3000, 90, 40])
+    T, cu = 40, i32(offsets)
+    for dtype in (torch.bfloat16, torch.float32):
+        Q = _q(T, 8, 128, dtype, 1)
+        for max_q in (1, 8, T):
+            O = torch.full((T + 16, 8, 128), 7.0, dtype=dtype, device=DEV)
+            lse = torch.full((T + 16, 8), 7.0, device=DEV)
+            ws = torch.full((max(16, nv.nvfp4_kv_attention_workspace_size(c, dtype, T, 8, 3, max_q, 3000)),),
+                            0xFF, dtype=torch.uint8, device=DEV)
+            nv.nvfp4_kv_attention(c, 0, Q, cu, None, 3, max_q, 3000, 0.1, True, 0, O[8:-8], lse[8:-8], ws)
+            torch.cuda.synchronize()
+            for t in (O, lse):
+                assert bool((t[:8] == 7.0).all()) and bool((t[-8:] == 7.0).all())
+
+
 def test_bounds_below_the_need(nv):
     """Rows at or beyond max_q are not written, positions at or beyond max_kv are left out."""
     lens, new = [90, 33], [20, 7]
