@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kDepth = 2;            // tiles of a wave in LDS (3: half the waves, 4 x 131072 positions 63 us, not 58)
+constexpr int kUnits = 256;          // compute units
 constexpr int kMaxSplits = 1024;     // chunks of a row
 constexpr int64_t kMaxGrid = (int64_t)1 << 24;   // workgroups: 2^32 threads a launch
 // Rows up to which k_kv_decode takes an item (in tiles of 16 or 32). Above, kv_prefill.hip shares the
@@ -202,6 +202,17 @@ template <int N>
 __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%c0)" ::"n"(N) : "memory");
 }
+// Waits until at most `behind` tiles (0 .. N) of L copies each are in flight.
+template <int L, int N>
+__device__ __forceinline__ void wait_behind(int behind) {
+    if constexpr (N == 0) {
+        wait_copies<0>();
+    } else if (behind == N) {
+        wait_copies<N * L>();
+    } else {
+        wait_behind<L, N - 1>(behind);
+    }
+}
 
 // V operand of output tile J: column J of the lane's D/16, tokens 4g .. 4g + 3 of both half tiles.
 template <int D, int J>
@@ -284,8 +295,22 @@ __device__ __forceinline__ void convert_query(QRow<D, BF16>& q, const RawQuery<D
 template <int D, int RT>
 constexpr int kOccupancy = D * RT <= 128 ? 4 : D * RT <= 256 ? 2 : 1;
 
-template <int D, bool BF16, int RT>
-__global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvAttention a, KvPlan plan) {
+// Waves of a workgroup and tiles of a wave in LDS. Four waves with two tiles, so that a compute unit holds as
+// many waves as its registers (three tiles: half the waves, 4 x 131072 positions 63 us, not 58). A
+// workgroup that has a compute unit to itself (`ALONE`) takes its whole LDS: eight waves and what fits
+// (one row over 1023 positions 12.2 us, with four and two 13.0; up to 512 positions and 256 wide they are
+// no slower).
+template <int D, bool ALONE>
+struct Shape {
+    static constexpr int kWaves = ALONE ? 8 : 4;
+    static constexpr int kDepth = ALONE ? 4096 / D / kWaves : 2;
+};
+
+template <int D, bool BF16, int RT, bool ALONE>
+__global__ __launch_bounds__((64 * Shape<D, ALONE>::kWaves), (ALONE ? 2 : kOccupancy<D, RT>))
+void k_kv_decode(KvAttention a, KvPlan plan) {
+    constexpr int kWaves = Shape<D, ALONE>::kWaves, kThreads = 64 * kWaves;
+    constexpr int kDepth = Shape<D, ALONE>::kDepth;
     constexpr int R = 16 * RT, NJ = D / 16, NS = D / 32;
     constexpr int JC = NJ < 8 ? NJ : 8;                  // output tiles joined at a time
     using T = TileLds<D>;
@@ -467,12 +492,8 @@ __global__ __launch_bounds__(kThreads, (kOccupancy<D, RT>)) void k_kv_decode(KvA
     for (int i = 0; i < tiles; ++i) {
         Tile x;
         const int behind = min(kDepth - 1, tiles - 1 - i);   // tiles in flight after this one
-        if (behind == kDepth - 1) {
-            copy(i + kDepth - 1);                        // its place was read an iteration ago
-            wait_copies<(kDepth - 1) * T::kLoads>();
-        } else {
-            wait_copies<0>();
-        }
+        if (i + kDepth - 1 < tiles) copy(i + kDepth - 1);    // its place was read an iteration ago
+        wait_behind<T::kLoads, kDepth - 1>(behind);
         x.ok[0] = (named >> (2 * behind + 1)) & 1u;
         x.ok[1] = (named >> (2 * behind)) & 1u;
         read_tile<D>(x.h, ring_at + i % kDepth * T::kBytes, at);
@@ -722,9 +743,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a batch is split: row tiles of 16, 32 or (prompts) 128 rows, and where these alone do not fill the chip,
 // chunks of positions. span: the most positions a row tile sees. Splitting costs the join, about 5 us:
-// a decode batch is split where its tiles leave workgroup slots empty and a tile has more than 10 units
-// of work (64 rows over up to 8192 positions 63 us, not split 85; 4 over up to 131072 58, not split
-// 855; but 16 x 5 rows behind a window of 1024 19, not split 14). A prompt's tiles are 128 rows whose
+// a decode batch is split where its tiles leave workgroup slots empty and a tile may have more than 10
+// units of work, or more the more tiles there are: those load the chip without it, unless lengths differ
+// (8 heads of 4: 16 rows over 1400 positions 19 us, not split 15; 64 over 1400 33 and 26, over up to 8192,
+// ragged, 63 and 85; 4 over up to 131072 56 and 855). A prompt's tiles are 128 rows whose
 // partial outputs outweigh a few hundred positions: it is split below 256 tiles and from 6 units on, into
 // at least 2 units each (4 items of 200 rows over up to 2088 positions 26 us, not split 55).
 KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,
@@ -736,7 +758,7 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
     p.tiles = p.tiles > 0 ? p.tiles : 1;
     const bool prefill = p.tile_rows == kPrefillRows;
     // workgroups that 256 compute units hold at once (registers and LDS)
-    const int64_t slots = 256 * (prefill ? (dim <= 128 ? 2 : 1)
+    const int64_t slots = kUnits * (prefill ? (dim <= 128 ? 2 : 1)
                                  : dim * p.tile_rows <= 128 * 16 ? 4 : dim * p.tile_rows <= 256 * 16 ? 2 : 1);
     p.least = prefill ? 2 : 1;
     // tiles of all items, a head: numbered by item and tile, or without gaps where bounds that are too wide
@@ -746,9 +768,12 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
     if (seqs <= kMaxScan) {
         p.scan = by_rows < most / 2;
         most = most < by_rows ? most : by_rows;
-        if (prefill ? most * heads < 256 && span > 6 * kUnit
-                    : most * heads < slots && span > (dim <= 128 ? 10 : 5) * kUnit) {
-            const int64_t target = (prefill ? 512 : slots) / heads, fit = slots / heads;
+        const int64_t all = most * heads;
+        if (prefill ? all < kUnits && span > 6 * kUnit
+                    : all < slots && span > (10 + all / 24) * (dim <= 128 ? kUnit : kUnit / 2)) {
+            // few rows: as many tasks as run at once; two to a compute unit where one would do for the tiles
+            const int64_t now = !prefill && all <= kUnits && slots > 2 * kUnits ? 2 * kUnits : slots;
+            const int64_t target = (prefill ? 512 : now) / heads, fit = now / heads;
             p.target = (int32_t)(target < 1 ? 1 : target < kMaxSplits ? target : kMaxSplits);
             p.scan = 1;
             p.fit = (int32_t)(fit < 1 ? 1 : fit);
@@ -762,6 +787,7 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
         p.by_item = seqs * max_q <= 2 * tokens;
     }
     p.tasks = tasks < kMaxGrid / heads ? (int32_t)tasks : -1;
+    p.alone = !prefill && dim <= 128 && tasks * heads <= kUnits && span > 4 * kUnit;
     return p;
 }
 
@@ -771,13 +797,26 @@ size_t space_of(const KvPlan& p, int64_t heads, int64_t dim, int64_t seqs) {
            (size_t)p.tasks * (size_t)heads * (size_t)p.tile_rows * (size_t)(8 + 4 * dim);
 }
 
+template <int D, bool BF16, int RT>
+void launch_decode(const KvAttention& a, const KvPlan& p, dim3 grid, hipStream_t stream) {
+    if constexpr (D <= 128) {
+        if (p.alone) {
+            hipLaunchKernelGGL((k_kv_decode<D, BF16, RT, true>), grid, dim3(64 * Shape<D, true>::kWaves), 0,
+                               stream, a, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_kv_decode<D, BF16, RT, false>), grid, dim3(64 * Shape<D, false>::kWaves), 0,
+                       stream, a, p);
+}
+
 template <int D, bool BF16>
 hipError_t launch(const KvAttention& a, const KvPlan& p, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.kv.heads * p.tasks));
     if (p.tile_rows == 16)
-        hipLaunchKernelGGL((k_kv_decode<D, BF16, 1>), grid, dim3(kThreads), 0, stream, a, p);
+        launch_decode<D, BF16, 1>(a, p, grid, stream);
     else if (p.tile_rows == 32)
-        hipLaunchKernelGGL((k_kv_decode<D, BF16, 2>), grid, dim3(kThreads), 0, stream, a, p);
+        launch_decode<D, BF16, 2>(a, p, grid, stream);
     else
         launch_kv_prefill(a, p, stream);
     if (p.target > 0) {

@@ -183,6 +183,7 @@ struct KvPlan {
     int32_t tasks;           // tasks a head at most
     int32_t fit;             // tasks a head that run at once
     int32_t least;           // units of a chunk at least
+    int32_t alone;           // few rows: at most a workgroup for each compute unit, and much for each to do
     int32_t by_item;         // join: workgroups by (item, row of max_q) instead of by token row
     uint64_t page_magic;     // division of a 16-token unit by the units of a page
     uint32_t page_shift;
