@@ -17,9 +17,10 @@
 // touches each 128-byte line several times, and a touch of a line that is still on its way waits for it. So a
 // wave copies whole tiles into its own ring in LDS, each line once and one tile ahead, and reads operands
 // there. 64 rows of 4 heads over up to 8192 positions, 8 key/value heads, 128 wide (247.5 MB): 54 us
-// (4.6 TB/s; straight from the pages 72) and the join 5; 4 rows of 8 over up to 131072 (238 MB): 48
-// (5.0 TB/s) and 6. A large copy runs at 5.0 TB/s. Short caches are bound by the chain of launch, task,
-// length, page and tile: one row over 1023 positions 12 us.
+// (4.6 TB/s; straight from the pages 72) and the join 5; 4 rows of 8 over up to 131072 (238 MB): 45
+// (5.3 TB/s) and 5. A large copy runs at 5.0 TB/s. Few short sequences are bound by what one compute unit
+// can have on its way (about 28 GB/s) and by the chain of launch, task, length, page and tile: one row over
+// 1023 positions 12 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -39,8 +40,8 @@ constexpr int64_t kMaxGrid = (int64_t)1 << 24;   // workgroups: 2^32 threads a l
 // conversion of a tile: 46 items of 112 rows over up to 10596 positions, 2 heads, 54 us (here 74), of 40
 // rows 42 (here 42).
 constexpr int kFewRows = 32;
-// The join gives a row a workgroup below this many rows, a wave above: 256 rows of 33 chunks 58.5 us in all
-// (a wave each 62.8), 1920 rows of few chunks 17 us (a workgroup each 21).
+// The join gives a row a workgroup below this many rows, a wave above: 256 rows of 17 chunks 55.9 us in all
+// (a wave each 56.7), 1920 rows of few chunks 17.5 (a workgroup each 21).
 constexpr int kWideJoin = 1024;
 
 // A tile of 32 positions in LDS, as it is copied from the pages: the codes of [K half 0][K half 1]
@@ -295,8 +296,8 @@ __device__ __forceinline__ void convert_query(QRow<D, BF16>& q, const RawQuery<D
 template <int D, int RT>
 constexpr int kOccupancy = D * RT <= 128 ? 4 : D * RT <= 256 ? 2 : 1;
 
-// Waves of a workgroup and tiles of a wave in LDS. Four waves with two tiles, so that a compute unit holds as
-// many waves as its registers (three tiles: half the waves, 4 x 131072 positions 63 us, not 58). A
+// Waves of a workgroup and tiles of a wave in LDS. Four waves with two tiles, so that a compute unit holds
+// as many waves as its registers (three tiles: 64 rows over up to 8192 positions 70 us, not 63). A
 // workgroup that has a compute unit to itself (`ALONE`) takes its whole LDS: eight waves and what fits
 // (one row over 1023 positions 12.2 us, with four and two 13.0; up to 512 positions and 256 wide they are
 // no slower).
@@ -745,8 +746,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // chunks of positions. span: the most positions a row tile sees. Splitting costs the join, about 5 us:
 // a decode batch is split where its tiles leave workgroup slots empty and a tile may have more than 10
 // units of work, or more the more tiles there are: those load the chip without it, unless lengths differ
-// (8 heads of 4: 16 rows over 1400 positions 19 us, not split 15; 64 over 1400 33 and 26, over up to 8192,
-// ragged, 63 and 85; 4 over up to 131072 56 and 855). A prompt's tiles are 128 rows whose
+// (8 heads of 4: 16 rows over 1400 positions 19 us, not split 16; 64 over 1400 33 and 25, over up to 8192,
+// ragged, 63 and 83; 8 heads of 8: 4 over up to 131072 56 and 642). A prompt's tiles are 128 rows whose
 // partial outputs outweigh a few hundred positions: it is split below 256 tiles and from 6 units on, into
 // at least 2 units each (4 items of 200 rows over up to 2088 positions 26 us, not split 55).
 KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,

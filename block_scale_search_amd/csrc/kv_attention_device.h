@@ -171,7 +171,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // tiles, which gives the chunk size that makes about `target` tasks a head (as many as run at once),
 // and then finds its own in the prefix sum of the items' tasks. (A grid made for the longest item left most
 // workgroups without work and the others unevenly spread: 4 sequences of up to 131072 positions took 81 us
-// that way and 58 us so.)
+// that way and 57 us so.)
 constexpr int kUnit = 128;       // positions by which chunks are cut
 constexpr int kMaxScan = 1024;   // items up to which a task is found by scanning them
 
