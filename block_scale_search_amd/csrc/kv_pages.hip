@@ -1,7 +1,7 @@
 // Page bookkeeping of the paged key/value cache for gfx950: reserve, fork, free and compact change the
 // page table, the lengths and the reference counts on the device.
 //
-// The bookkeeping of reserve, fork and free is one workgroup: it checks every item before it changes
+// The bookkeeping of reserve and fork is one workgroup: it checks every item before it changes
 // anything (slots listed twice are found in a bit map in LDS), ranks the pages the items need with a
 // prefix sum, collects that many free pages in ascending order, and hands them out. What bounds it is
 // the chain of dependent loads (slot, length, table entry), so every step is made for all items at
@@ -11,9 +11,9 @@
 // the rate of a copy. Reference counts change by integer atomics, whose result does not depend on
 // their order.
 //
-// 16 slots of up to 500 positions (pages of 16): free 3.5 us, fork 5.4 and its copies 3.4, reserve 4.8.
-// 256 slots of up to 4000 (pages of 64, 4 layers, 8 heads, 128 wide): 8.6, 7.6 and 8.2 (37 MB, 4.5 TB/s), 7.8.
-// Compact of 192 slots of up to 3000: 8.1 us to rank, 140.5 to move 785 MB (5.6 TB/s read and written).
+// 16 slots of up to 500 positions (pages of 16): free 2.5 us, fork 4.9 and its copies 3.6, reserve 4.4.
+// 256 slots of up to 4000 (pages of 64, 4 layers, 8 heads, 128 wide): 3.9, 5.5 and 8.4 (37 MB, 4.4 TB/s), 5.7.
+// Compact of 192 slots of up to 3000: 6.5 us to rank, 140 to move 785 MB (5.6 TB/s read and written).
 #include <hip/hip_runtime.h>
 
 #include "../../include/nvfp4.h"
@@ -25,8 +25,9 @@ namespace {
 constexpr int kBook = 1024;          // threads of the bookkeeping workgroup
 constexpr int kWaves = kBook / 64;
 constexpr int kSlotWords = 65536 / 32;
-constexpr int kFirst = 8;            // reference counts a thread loads ahead
-constexpr int kBatch = 8;            // table rows a wave has in flight
+constexpr int kFirst = 4;            // reference counts a thread loads ahead
+constexpr int kFreeRows = 16;        // slots a workgroup of free empties, one a wave, where there are few
+constexpr int kFreeMost = 64;        // its workgroups (65,536 slots: kBook each)
 constexpr int kOne = 16 * kBook;     // pages that one workgroup ranks for compact
 constexpr int kChunk = 1024;         // pages per workgroup of compact's counting
 constexpr int kCopyThreads = 256;
@@ -93,30 +94,41 @@ __device__ __forceinline__ bool mark_slots(const KvPool& p, const int32_t* slots
     return bad;
 }
 
-// The thread's kFirst pages from page p0 on: which are free, as bits.
+// Reference counts of the pages q .. q + 3 (`none` at or beyond end) in one load: counts one by one would
+// touch a line again and again, and a touch of a line that is still on its way waits for it (256 slots:
+// fork 5.5 us, reserve 5.7; with eight counts a thread one by one 7.6 and 7.8).
+typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ i32x4 counts_of(const KvPool& p, int q, int end, int none) {
+    if (q + 4 <= end) return *reinterpret_cast<const i32x4*>(p.refs + q);
+    i32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = q + i < end ? p.refs[q + i] : none;
+    return r;
+}
+
+// Which of the thread's kFirst pages from page p0 on are free, as bits; of kFirst kBook pages in all.
 __device__ __forceinline__ uint32_t free_bits(const KvPool& p, int p0) {
-    const int q = p0 + kFirst * (int)threadIdx.x;
+    const i32x4 r = counts_of(p, p0 + kFirst * (int)threadIdx.x, p.num_pages, 1);
     uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < kFirst; ++i) {
-        const int r = q + i < p.num_pages ? p.refs[q + i] : 1;
-        bits |= r <= 0 ? 1u << i : 0u;
-    }
+    for (int i = 0; i < kFirst; ++i) bits |= r[i] <= 0 ? 1u << i : 0u;
     return bits;
 }
 
 // The lowest `need` free pages in ascending order into list[]; returns how many were found (at most
-// need). bits: free_bits(p, 0), loaded ahead.
+// need). bits: free_bits(p, 0), loaded ahead, as every round's are by the one before.
 __device__ __forceinline__ int take_free(const KvPool& p, int need, uint32_t bits, int32_t* list,
                                          int* sums) {
     int found = 0;
-    for (int p0 = 0; p0 < p.num_pages && found < need; p0 += kFirst * kBook) {
-        if (p0 > 0) bits = free_bits(p, p0);
+    for (int64_t p0 = 0; p0 < p.num_pages && found < need; p0 += kFirst * kBook) {
+        const bool more = p0 + kFirst * kBook < p.num_pages;
+        const uint32_t next = more ? free_bits(p, (int)p0 + kFirst * kBook) : 0u;
         int total;
         int k = found + block_exclusive<kWaves>(__popc(bits), sums, total);
         for (uint32_t left = bits; left != 0 && k < need; left &= left - 1)
-            list[k++] = p0 + kFirst * (int)threadIdx.x + __builtin_ctz(left);
+            list[k++] = (int)p0 + kFirst * (int)threadIdx.x + __builtin_ctz(left);
         found += total;
+        bits = next;
     }
     return min(found, need);
 }
@@ -267,6 +279,9 @@ __global__ __launch_bounds__(kBook) void k_kv_fork(KvPool p, const int32_t* __re
     if (threadIdx.x == 0) *status = reason;
 }
 
+// Every workgroup checks all slots and empties its share of them: the changes of reference counts are
+// scattered atomics, which one compute unit issues an address at a time (256 slots of up to 63 pages 9.0 us
+// in one workgroup, 3.9 in sixteen).
 __global__ __launch_bounds__(kBook) void k_kv_free(KvPool p, const int32_t* __restrict__ slots,
                                                    int n, int32_t* status) {
     __shared__ uint32_t map[kSlotWords];
@@ -274,42 +289,27 @@ __global__ __launch_bounds__(kBook) void k_kv_free(KvPool p, const int32_t* __re
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     clear_map(p, map);
     if (__syncthreads_or(mark_slots(p, slots, n, map))) {
-        if (threadIdx.x == 0) *status = NVFP4_KV_BAD_SLOT;
+        if (blockIdx.x == 0 && threadIdx.x == 0) *status = NVFP4_KV_BAD_SLOT;
         return;
     }
-    for (int i0 = 0; i0 < n; i0 += kBook) {
-        const int m = min(kBook, n - i0);
-        __syncthreads();
-        if ((int)threadIdx.x < m) {
-            const int s = slots[i0 + threadIdx.x];
-            slot[threadIdx.x] = s;
-            held[threadIdx.x] = pages_of(length_of(p, s), p.page);
-            p.lens[s] = 0;
-        }
-        __syncthreads();
-        // kBatch rows of a wave at a time, 64 entries of each: all loads, then all changes
-        for (int j0 = wave * kBatch; j0 < m; j0 += kWaves * kBatch) {
-            int most = 0;
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) most = max(most, j0 + j < m ? held[j0 + j] : 0);
-            for (int k = lane; k - lane < most; k += 64) {
-                int page[kBatch];
-                int32_t* at[kBatch];
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const bool in = j0 + j < m && k < held[j0 + j];
-                    at[j] = in ? p.table + (int64_t)slot[j0 + j] * p.max_pages + k : nullptr;
-                    page[j] = in ? *at[j] : -1;
-                }
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    if (at[j]) *at[j] = -1;
-                    if ((uint32_t)page[j] < (uint32_t)p.num_pages) atomicSub(&p.refs[page[j]], 1);
-                }
-            }
+    const int share = (n + (int)gridDim.x - 1) / (int)gridDim.x;        // at most kBook
+    const int i0 = (int)blockIdx.x * share, m = min(share, n - i0);
+    if ((int)threadIdx.x < m) {
+        const int s = slots[i0 + threadIdx.x];
+        slot[threadIdx.x] = s;
+        held[threadIdx.x] = pages_of(length_of(p, s), p.page);
+        p.lens[s] = 0;
+    }
+    __syncthreads();
+    for (int j = wave; j < m; j += kWaves) {             // a row of a wave at a time
+        int32_t* row = p.table + (int64_t)slot[j] * p.max_pages;
+        for (int k = lane; k < held[j]; k += 64) {
+            const int page = row[k];
+            row[k] = -1;
+            if ((uint32_t)page < (uint32_t)p.num_pages) atomicSub(&p.refs[page], 1);
         }
     }
-    if (threadIdx.x == 0) *status = NVFP4_KV_DONE;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = NVFP4_KV_DONE;
 }
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -374,7 +374,11 @@ template <int N>
 __device__ __forceinline__ uint32_t used_bits(const KvPool& p, int q, int end) {
     uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) bits |= q + i < end && p.refs[q + i] > 0 ? 1u << i : 0u;
+    for (int i = 0; i < N; i += 4) {
+        const i32x4 r = counts_of(p, q + i, end, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bits |= r[j] > 0 ? 1u << (i + j) : 0u;
+    }
     return bits;
 }
 
@@ -513,14 +517,17 @@ hipError_t launch_kv_fork(const KvPool& p, const int32_t* parents, const int32_t
                        first, list, src, dst);
     const int64_t parts = parts_of(p);
     if (n > 0)
-        hipLaunchKernelGGL(k_kv_copy, dim3((uint32_t)n, (uint32_t)(parts < 64 ? parts : 64),
-                                           (uint32_t)p.layers), dim3(kCopyThreads), 0, stream, p, parents, children, src, dst, (int)parts);
+        hipLaunchKernelGGL(k_kv_copy, dim3((uint32_t)n, (uint32_t)(parts < 64 ? parts : 64), (uint32_t)p.layers),
+                           dim3(kCopyThreads), 0, stream, p, parents, children, src, dst,
+                           (int)parts);
     return hipGetLastError();
 }
 
 hipError_t launch_kv_free(const KvPool& p, const int32_t* slots, int32_t n, int32_t* status,
                           hipStream_t stream) {
-    hipLaunchKernelGGL(k_kv_free, dim3(1), dim3(kBook), 0, stream, p, slots, n, status);
+    const int wanted = (n + kFreeRows - 1) / kFreeRows;
+    const int groups = wanted < 1 ? 1 : wanted < kFreeMost ? wanted : kFreeMost;
+    hipLaunchKernelGGL(k_kv_free, dim3(groups), dim3(kBook), 0, stream, p, slots, n, status);
     return hipGetLastError();
 }
 

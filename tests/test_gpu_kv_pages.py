@@ -69,6 +69,25 @@ def test_random_history(nv, seed, num_pages, page, slots, width, stride):
     assert ("reserve", 0) in seen and ("fork", 0) in seen and ("free", 0) in seen
 
 
+@pytest.mark.parametrize("slots", [1, 17, 1025, 20000])
+def test_many_slots_at_once(nv, slots):
+    """Calls whose slots are shared out to several workgroups, one of them listed in two of their shares."""
+    r = random.Random(slots)
+    c, pool = _new(nv, 2 * slots + 3, 16, slots, 3, layers=1)
+    every = r.sample(range(slots), slots)
+    for counts in ([r.randint(0, 20) for _ in every], [1] * slots):
+        assert nv.kv_reserve(c, i32(every), i32(counts)).item() == pool.reserve(every, counts)
+        pool.check(c, f"reserve {slots}")
+    twice = every + every[:1]
+    assert nv.kv_free(c, i32(twice)).item() == pool.free(twice) == 1
+    pool.check(c, f"refused {slots}")
+    some = every[:slots - slots // 7]
+    assert nv.kv_free(c, i32(some)).item() == pool.free(some) == 0
+    pool.check(c, f"free {slots}")
+    assert nv.kv_reserve(c, i32(some), i32([9] * len(some))).item() == pool.reserve(some, [9] * len(some)) == 0
+    pool.check(c, f"again {slots}")
+
+
 def test_refused_items_change_nothing(nv):
     c, pool = _new(nv, 20, 16, 6, 8)
     assert nv.kv_reserve(c, i32([0, 1, 2]), i32([40, 16, 1])).item() == pool.reserve([0, 1, 2], [40, 16, 1])
