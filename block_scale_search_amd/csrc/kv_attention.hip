@@ -742,8 +742,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttention a, KvPlan plan
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// How a batch is split: row tiles of 16, 32 or (prompts) 128 rows, and where these alone do not fill the chip,
-// chunks of positions. span: the most positions a row tile sees. Splitting costs the join, about 5 us:
+// How a batch is split: row tiles of 16, 32 or (prompts) 128 rows, and where these alone do not fill the
+// chip, chunks of positions. span: the most positions a row tile sees. Splitting costs the join, about 5 us:
 // a decode batch is split where its tiles leave workgroup slots empty and a tile may have more than 10
 // units of work, or more the more tiles there are: those load the chip without it, unless lengths differ
 // (8 heads of 4: 16 rows over 1400 positions 19 us, not split 16; 64 over 1400 33 and 25, over up to 8192,
