@@ -453,11 +453,7 @@ void k_kv_decode(KvAttention a, KvPlan plan) {
                               fmaxf(fmaxf(s[rt][1][0], s[rt][1][1]), fmaxf(s[rt][1][2], s[rt][1][3])));
             top *= q[rt].f;
             if (__any(top > m[rt] + kSlack)) {
-                const float mn = fmaxf(m[rt], max_groups(top));
-                const bool none = mn == -__builtin_inff();
-                const float al = none ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
-                m[rt] = mn;
-                sub[rt] = none ? 0.0f : kUp - mn;
+                const float al = raise_row(m[rt], sub[rt], max_groups(top));
                 l[rt] *= al;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) o[rt][j] *= al;

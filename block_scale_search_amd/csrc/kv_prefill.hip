@@ -331,11 +331,7 @@ __global__ __launch_bounds__(kThreads, kOccupancy<D>) void k_kv_prefill(KvAttent
             for (int k = 1; k < 32; ++k) top = fmaxf(top, s[k >> 4][k & 15]);
             top *= q.f;
             if (__any(top > m + kSlack)) {
-                const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
-                const bool none = mn == -__builtin_inff();
-                const float al = none ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
-                sub = none ? 0.0f : kUp - mn;
+                const float al = raise_row(m, sub, fmaxf(top, __shfl_xor(top, 32, 64)));
                 l *= al;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) o[j] *= al;

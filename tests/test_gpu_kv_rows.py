@@ -1,0 +1,53 @@
+"""Rows of the key/value cache's attention that hold what no other row may see: late maxima, infinities,
+scales that are no number."""
+import math
+
+import pytest
+import torch
+
+from kv_helpers import DEV, attention, check_attention, i32, make_cache
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [([700], [1]), ([700], [6]), ([700], [40]), ([6000], [1]), ([6000], [5]), ([6000, 900], [200, 30])]
+
+
+def _climbing(nv, lens, heads, dim, seed=0):
+    """A cache whose keys' first 16 values are 0 in the first half of a slot and 30 behind it, the others small."""
+    c = make_cache(nv, lens, heads, dim, 16, seed=seed)
+    g = torch.Generator(device=DEV).manual_seed(seed + 1)
+    k = 0.5 * torch.randn((sum(lens), heads, dim), generator=g, device=DEV)
+    v = torch.randn((sum(lens), heads, dim), generator=g, device=DEV)
+    k[:, :, :16] = 0
+    at = 0
+    for n in lens:
+        k[at + n // 2:at + n, :, :16] = 30
+        at += n
+    nv.kv_append(c, 0, k, v, i32([0] + torch.tensor(lens).cumsum(0).tolist()))
+    return c
+
+
+def _queries(new, heads, dim, dtype, seed=2):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = 2 * torch.randn((sum(new), heads, dim), generator=g, device=DEV)
+    q[:, :, :16] = 0
+    return q.to(dtype), [0] + torch.tensor(new).cumsum(0).tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,new", SHAPES)
+def test_a_late_maximum_stays_in_its_row(nv, lens, new, dim, dtype):
+    """A row whose logits rise by 2^50 and more halfway, and the same row as a NaN: every other row of its
+    wave has the same bytes both times."""
+    c = _climbing(nv, lens, 2, dim)
+    Q, cu = _queries(new, 8, dim, dtype)
+    bad = torch.zeros(Q.shape[:2], dtype=torch.bool)
+    bad[cu[-1] - 1, 1] = bad[cu[-1] // 2, 6] = True
+    Q[bad] = 1.0
+    out, lse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    check_attention(out, lse, attention(c, 0, Q, cu, range(len(new)), dim ** -0.5, True, 0))
+    Q[bad] = math.nan
+    got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    assert torch.isnan(got[bad]).all() and torch.isnan(glse[bad]).all()
+    assert torch.equal(got[~bad], out[~bad]) and torch.equal(glse[~bad], lse[~bad])
