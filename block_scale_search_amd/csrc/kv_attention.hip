@@ -277,12 +277,14 @@ __device__ __forceinline__ void convert_query(QRow<D, BF16>& q, const RawQuery<D
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
-    const int k = row_exponent(max_groups(top));
+    top = max_groups(top);
+    const int k = row_exponent(top);
+    const float up = row_factor(k, top);
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float v = __builtin_ldexpf(x[8 * s + j], k);
+            const float v = x[8 * s + j] * up;
             const _Float16 h = (_Float16)v;
             q.hi[s][j] = h;
             if constexpr (!BF16) q.lo[s][j] = (_Float16)(v - (float)h);

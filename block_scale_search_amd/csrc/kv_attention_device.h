@@ -76,6 +76,12 @@ __device__ __forceinline__ int row_exponent(float top) {
     return min(15 - __builtin_amdgcn_frexp_expf(top), 126);
 }
 
+// What the row's values are multiplied by: 2^k, or NaN for a row with an infinity. Its logits are infinite or
+// NaN, their softmax is NaN whatever they are, and logits of -infinity would look like positions that are masked.
+__device__ __forceinline__ float row_factor(int k, float top) {
+    return top == __builtin_inff() ? __builtin_nanf("") : __builtin_ldexpf(1.0f, k);
+}
+
 // One rounding to bf16, to nearest even; NaN of any bits stays NaN.
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     const auto r = [](float v) {

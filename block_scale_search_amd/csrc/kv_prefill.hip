@@ -181,12 +181,14 @@ __device__ __forceinline__ void load_query(Query<D, BF16>& q, const uint8_t* p, 
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[s][k]));
     }
-    const int e = row_exponent(fmaxf(top, __shfl_xor(top, 32, 64)));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const int e = row_exponent(top);
+    const float up = row_factor(e, top);
 #pragma unroll
     for (int s = 0; s < N; ++s)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float v = __builtin_ldexpf(x[s][k], e);
+            const float v = x[s][k] * up;
             const _Float16 r = (_Float16)v;
             q.hi[s][k] = r;
             if constexpr (!BF16) q.lo[s][k] = (_Float16)(v - (float)r);

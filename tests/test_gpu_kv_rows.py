@@ -51,3 +51,28 @@ def test_a_late_maximum_stays_in_its_row(nv, lens, new, dim, dtype):
     got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
     assert torch.isnan(got[bad]).all() and torch.isnan(glse[bad]).all()
     assert torch.equal(got[~bad], out[~bad]) and torch.equal(glse[~bad], lse[~bad])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,new", SHAPES)
+def test_infinite_queries_are_nan(nv, lens, new, dim, dtype):
+    """A query row with an infinity that makes every logit -infinity (or +infinity) is NaN, as the softmax of
+    such logits is; a row that sees nothing keeps its zeros; every other row keeps its bytes."""
+    c = make_cache(nv, lens, 2, dim, 16)
+    k = torch.randn((sum(lens), 2, dim), generator=torch.Generator(device=DEV).manual_seed(4), device=DEV)
+    k[:, :, 3] = 4.0                                     # a code above 0 at every position
+    nv.kv_append(c, 0, k, k, i32([0] + torch.tensor(lens).cumsum(0).tolist()))
+    Q, cu = _queries(new, 8, dim, dtype)
+    out, lse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    bad = torch.zeros(Q.shape[:2], dtype=torch.bool)
+    for i, (t, h, x) in enumerate([(0, 1, -math.inf), (cu[-1] - 1, 6, math.inf), (cu[-1] // 2, 3, -math.inf)]):
+        Q[t, h] *= 0.01                                  # beside it values that f16 holds after any scaling
+        Q[t, h, 3 if i < 2 else 5] = x
+        bad[t, h] = True
+    got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    assert torch.isnan(got[bad]).all() and torch.isnan(glse[bad]).all()
+    assert torch.equal(got[~bad], out[~bad]) and torch.equal(glse[~bad], lse[~bad])
+    c.lens.zero_()
+    got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    assert bool((got == 0).all()) and bool((glse == -math.inf).all())
