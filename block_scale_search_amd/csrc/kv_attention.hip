@@ -279,7 +279,7 @@ __device__ __forceinline__ void convert_query(QRow<D, BF16>& q, const RawQuery<D
     for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
     top = max_groups(top);
     const int k = row_exponent(top);
-    const float up = row_factor(k, top);
+    const float up = row_factor(k, top, S);
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
 #pragma unroll

@@ -76,10 +76,12 @@ __device__ __forceinline__ int row_exponent(float top) {
     return min(15 - __builtin_amdgcn_frexp_expf(top), 126);
 }
 
-// What the row's values are multiplied by: 2^k, or NaN for a row with an infinity. Its logits are infinite or
-// NaN, their softmax is NaN whatever they are, and logits of -infinity would look like positions that are masked.
-__device__ __forceinline__ float row_factor(int k, float top) {
-    return top == __builtin_inff() ? __builtin_nanf("") : __builtin_ldexpf(1.0f, k);
+// What the row's values are multiplied by: 2^k, or NaN for a row with an infinity and where S_k is NaN or
+// infinite. Such logits are infinite or NaN, their softmax is NaN whatever they are, and logits of -infinity
+// would look like positions that are masked.
+__device__ __forceinline__ float row_factor(int k, float top, float S) {
+    return top < __builtin_inff() && S < __builtin_inff() ? __builtin_ldexpf(1.0f, k)
+                                                          : __builtin_nanf("");
 }
 
 // One rounding to bf16, to nearest even; NaN of any bits stays NaN.

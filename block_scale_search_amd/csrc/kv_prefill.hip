@@ -183,7 +183,7 @@ __device__ __forceinline__ void load_query(Query<D, BF16>& q, const uint8_t* p, 
     }
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const int e = row_exponent(top);
-    const float up = row_factor(e, top);
+    const float up = row_factor(e, top, S);
 #pragma unroll
     for (int s = 0; s < N; ++s)
 #pragma unroll

@@ -544,8 +544,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, int64_t layer, void* K, 
  *   out[t]      = sum_p exp(logit[t, p]) v[p] / sum_p exp(logit[t, p])   over the visible p
  *   lse[t]      = ln sum_p exp(logit[t, p])
  * A row that sees no position gets zeros and lse = -infinity, any other query row with a NaN or an
- * infinity gets NaN, its lse too. No row's bits depend on another row's values. Query head j reads
- * key/value head j / (q_heads / heads). Not causal: every row sees the whole slot (e.g. an encoder's states).
+ * infinity gets NaN, its lse too, as does every row of a head whose S_k is NaN or infinite. No row's bits
+ * depend on another row's values. Query head j reads key/value head j / (q_heads / heads). Not causal:
+ * every row sees the whole slot (e.g. an encoder's states).
  *
  * The products run on f16 MFMA with binary32 sums: level * E4M3 has at most 6 significant bits and is
  * exact in f16; a bf16 query row is exact after a power-of-two scaling of the row; an f32 query

@@ -76,3 +76,22 @@ def test_infinite_queries_are_nan(nv, lens, new, dim, dtype):
     c.lens.zero_()
     got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
     assert bool((got == 0).all()) and bool((glse == -math.inf).all())
+
+
+@pytest.mark.parametrize("bad_scale", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,new", SHAPES)
+def test_a_scale_that_is_no_number(nv, lens, new, dim, dtype, bad_scale):
+    """S_k of one head NaN or infinite: its query heads are NaN, the other head's keep their bytes, and rows
+    that see nothing their zeros."""
+    c = _climbing(nv, lens, 2, dim, 5)
+    Q, cu = _queries(new, 8, dim, dtype)
+    out, lse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    c.S_k[0, 1] = bad_scale
+    got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    assert torch.isnan(got[:, 4:]).all() and torch.isnan(glse[:, 4:]).all()
+    assert torch.equal(got[:, :4], out[:, :4]) and torch.equal(glse[:, :4], lse[:, :4])
+    c.lens.zero_()
+    got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
+    assert bool((got == 0).all()) and bool((glse == -math.inf).all())
