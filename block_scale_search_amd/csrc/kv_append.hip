@@ -187,15 +187,6 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(KvView kv, KvTokens K, K
         (uint8_t)code;
 }
 
-// Two bf16 (rounded to nearest even) of finite a, b, a in the low half.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-    const auto r = [](float v) {
-        const uint32_t u = __float_as_uint(v);
-        return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-    };
-    return r(a) | (r(b) << 16);
-}
-
 template <bool BF16, int GPH>
 __global__ __launch_bounds__(kThreads) void k_kv_read(KvView kv, uint8_t* __restrict__ K,
                                                       uint8_t* __restrict__ V, KvBatch b) {

@@ -84,15 +84,6 @@ __device__ __forceinline__ float row_factor(int k, float top, float S) {
                                                           : __builtin_nanf("");
 }
 
-// One rounding to bf16, to nearest even; NaN of any bits stays NaN.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-    const auto r = [](float v) {
-        const uint32_t u = __float_as_uint(v);
-        return v == v ? (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16 : 0x7FC0u;
-    };
-    return r(a) | (r(b) << 16);
-}
-
 constexpr float kUp = 8.0f;          // log2 of the weights' scale
 constexpr float kSlack = 7.0f;       // how far a logit may exceed the maximum in use, log2
 

@@ -125,6 +125,15 @@ __device__ __forceinline__ int kv_find_item(const int32_t* __restrict__ cu, int 
     return lo;
 }
 
+// Two values rounded to bf16, to nearest even, a in the low half; NaN of any bits stays NaN.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    const auto r = [](float v) {
+        const uint32_t u = __float_as_uint(v);
+        return v == v ? (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16 : 0x7FC0u;
+    };
+    return r(a) | (r(b) << 16);
+}
+
 #endif  // __HIPCC__
 
 }  // namespace nvfp4

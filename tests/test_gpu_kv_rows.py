@@ -1,4 +1,4 @@
-"""Rows of the key/value cache's attention that hold what no other row may see: late maxima, infinities,
+"""Rows of the key/value cache that hold what no other row may see: late maxima, infinities,
 scales that are no number."""
 import math
 
@@ -95,3 +95,35 @@ def test_a_scale_that_is_no_number(nv, lens, new, dim, dtype, bad_scale):
     c.lens.zero_()
     got, glse = nv.kv_attention(c, 0, Q, i32(cu), max_q=max(new))
     assert bool((got == 0).all()) and bool((glse == -math.inf).all())
+
+
+READ = pytest.mark.parametrize("dtype,dim,bits", [(t, d, b) for t in (torch.bfloat16, torch.float32) for d in (64, 128, 256)
+                               for b in (0x7FFFFFFF, -1, 0x7FC00000, 0x7F800001, 0x7F800000)])
+
+
+def _read_before_and_after(nv, dtype, dim, bits):
+    """What two slots read as, one with a page that the table does not name and one with more rows asked for than it
+    is long, before and after the second head's S_k and S_v become the binary32 of `bits`; and which rows are
+    cached."""
+    c = make_cache(nv, [40, 8], 2, dim, 16)
+    c.table[0, 1] = -1
+    x = torch.randn((60, 2, dim), generator=torch.Generator(device=DEV).manual_seed(6), device=DEV)
+    cu = i32([0, 40, 60])
+    nv.kv_append(c, 0, x, x, cu)
+    want = nv.kv_read(c, 0, 60, cu, dtype=dtype)
+    there = torch.ones(60, dtype=torch.bool, device=DEV)
+    there[16:32] = there[40:52] = False
+    for S in (c.S_k, c.S_v):
+        S[0].view(torch.int32)[1] = bits
+    return want, nv.kv_read(c, 0, 60, cu, dtype=dtype), there
+
+
+@READ
+def test_read_with_a_scale_that_is_no_number(nv, dtype, dim, bits):
+    """Values of a head whose S is a NaN of any bits are NaN, of an infinite one NaN or infinite; the other
+    head's values stay."""
+    want, got, there = _read_before_and_after(nv, dtype, dim, bits)
+    for x, ref in zip(got, want):
+        assert torch.equal(x[:, 0], ref[:, 0])
+        assert not torch.isfinite(x[there, 1]).any()
+        assert bits == 0x7F800000 or torch.isnan(x[there, 1]).all()
