@@ -206,7 +206,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvView kv, uint8_t* __rest
                           scale_offset<GPH>(kv, is_v, head, p.row, p.g)];
         e = e4m3_value(s & 127);
     }
-    const float S = (is_v ? kv.S_v : kv.S_k)[head];
+    // zeros where nothing is cached, whatever S is
+    const float S = p.page >= 0 ? (is_v ? kv.S_v : kv.S_k)[head] : 0.0f;
     float v[16];
     e2m1_levels2<0>(c.x, v[0], v[1]);
     e2m1_levels2<1>(c.x, v[2], v[3]);

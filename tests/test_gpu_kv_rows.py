@@ -127,3 +127,11 @@ def test_read_with_a_scale_that_is_no_number(nv, dtype, dim, bits):
         assert torch.equal(x[:, 0], ref[:, 0])
         assert not torch.isfinite(x[there, 1]).any()
         assert bits == 0x7F800000 or torch.isnan(x[there, 1]).all()
+
+
+@READ
+def test_read_of_nothing_is_zero_at_any_scale(nv, dtype, dim, bits):
+    """Positions that are not in the cache read as zeros where S is NaN or infinite, too."""
+    want, got, there = _read_before_and_after(nv, dtype, dim, bits)
+    for x in want + got:
+        assert bool((x[~there] == 0).all())
