@@ -455,7 +455,7 @@ void k_kv_decode(KvAttention a, KvPlan plan) {
                               fmaxf(fmaxf(s[rt][1][0], s[rt][1][1]), fmaxf(s[rt][1][2], s[rt][1][3])));
             top *= q[rt].f;
             if (__any(top > m[rt] + kSlack)) {
-                const float al = raise_row(m[rt], sub[rt], max_groups(top));
+                const float al = raise_row(m[rt], sub[rt], max_groups(top), kSlack);
                 l[rt] *= al;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) o[rt][j] *= al;

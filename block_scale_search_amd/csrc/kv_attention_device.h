@@ -87,12 +87,11 @@ __device__ __forceinline__ float row_factor(int k, float top, float S) {
 constexpr float kUp = 8.0f;          // log2 of the weights' scale
 constexpr float kSlack = 7.0f;       // how far a logit may exceed the maximum in use, log2
 
-// Raises a row's maximum in use m (and sub, what its logits are shifted by) to `top`, the row's largest
-// logit of a tile, if that passes the slack; returns the factor of its sums so far. The wave comes here when one of
-// its rows has to; a row that does not have to keeps its m, so that its bits are the same whatever the
-// wave's other rows hold.
-__device__ __forceinline__ float raise_row(float& m, float& sub, float top) {
-    const bool up = top > m + kSlack;
+// Raises a row's maximum in use m (and sub, what its logits are shifted by) to `top`, the row's largest logit, if
+// that passes the slack; returns the factor of the row's sums so far. The wave comes here when one of its rows
+// has to; another keeps its m, so that its bits are the same whatever the wave's other rows hold.
+__device__ __forceinline__ float raise_row(float& m, float& sub, float top, float slack) {
+    const bool up = top > m + slack;
     const float al = up ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
     m = up ? top : m;
     sub = up ? kUp - top : sub;
