@@ -192,6 +192,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvView kv, uint8_t* __rest
                                                       uint8_t* __restrict__ V, KvBatch b) {
     const int head = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
+    const float S_head = (is_v ? kv.S_v : kv.S_k)[head];  // beside the look-up, not behind it
     const Place p = place_of<GPH>(kv, b);
     if (!p.valid) return;
     uint2 c = make_uint2(0u, 0u);
@@ -206,8 +207,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvView kv, uint8_t* __rest
                           scale_offset<GPH>(kv, is_v, head, p.row, p.g)];
         e = e4m3_value(s & 127);
     }
-    // zeros where nothing is cached, whatever S is
-    const float S = p.page >= 0 ? (is_v ? kv.S_v : kv.S_k)[head] : 0.0f;
+    const float S = p.page >= 0 ? S_head : 0.0f;         // zeros where nothing is cached, whatever S is
     float v[16];
     e2m1_levels2<0>(c.x, v[0], v[1]);
     e2m1_levels2<1>(c.x, v[2], v[3]);
