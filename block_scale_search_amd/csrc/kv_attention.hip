@@ -761,12 +761,12 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
                                  : dim * p.tile_rows <= 128 * 16 ? 4 : dim * p.tile_rows <= 256 * 16 ? 2 : 1);
     p.least = prefill ? 2 : 1;
     // tiles of all items, a head: numbered by item and tile, or without gaps where bounds that are too wide
-    // would leave most of those numbers empty
+    // would leave most of those numbers empty, or have more of them than a launch
     int64_t most = seqs * p.tiles;
     const int64_t by_rows = seqs + ceil_div(tokens * group, p.tile_rows);
+    p.scan = by_rows < most && (most >= kMaxGrid / heads || (seqs <= kMaxScan && by_rows < most / 2));
+    if (p.scan || seqs <= kMaxScan) most = most < by_rows ? most : by_rows;
     if (seqs <= kMaxScan) {
-        p.scan = by_rows < most / 2;
-        most = most < by_rows ? most : by_rows;
         const int64_t all = most * heads;
         if (prefill ? all < kUnits && span > 6 * kUnit
                     : all < slots && span > (10 + all / 24) * (dim <= 128 ? kUnit : kUnit / 2)) {

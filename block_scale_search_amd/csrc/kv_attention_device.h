@@ -183,7 +183,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // workgroups without work and the others unevenly spread: 4 sequences of up to 131072 positions took 81 us
 // that way and 57 us so.)
 constexpr int kUnit = 128;       // positions by which chunks are cut
-constexpr int kMaxScan = 1024;   // items up to which a task is found by scanning them
+constexpr int kMaxScan = 1024;   // items up to which scanning them to find a task is worth its time
 
 struct KvPlan {
     int32_t tile_rows;       // query rows of a workgroup

@@ -875,7 +875,7 @@ def kv_attention(cache: KVCache, layer: int, Q: torch.Tensor, cu_tokens: torch.T
     """Attention of Q [tokens, q_heads, head_dim] over the cached keys and values; returns
     (out like Q, lse float32 [tokens, q_heads]). max_q and max_kv bound the items' rows and lengths
     (None: all rows, the table's capacity). Tight bounds give faster kernels: a decode step passes
-    max_q=1."""
+    max_q=1, and a batch of more than 1,024 items always its largest item's rows."""
     T, q_heads, D = Q.shape
     seqs = cu_tokens.numel() - 1
     max_q = T if max_q is None else max_q

@@ -565,9 +565,12 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, int64_t layer, void* K, 
  *          aligned, no initialisation needed (may be NULL when that is 0).
  * Rows of O and lse behind cu_tokens[seqs] are left as they are.
  * Requires heads <= 65,535, q_heads a multiple of heads, tokens * q_heads < 2^31, seqs <= 65,535,
- * max_q * (q_heads / heads) < 2^24, and fewer than 2^24 workgroups: with T = 128 query rows per
- * workgroup (32 for up to 32 rows an item, 16 for up to 16), heads * (seqs + tokens * (q_heads /
- * heads) / T + 1,024) for up to 1,024 items, heads * seqs * ceil(max_q * (q_heads / heads) / T) for more. */
+ * max_q * (q_heads / heads) < 2^24, and fewer than 2^24 workgroups by one of two counts: with T = 128
+ * query rows per workgroup (32 for up to 32 rows an item, 16 for up to 16),
+ * heads * (seqs + tokens * (q_heads / heads) / T + 1,024) or
+ * heads * seqs * ceil(max_q * (q_heads / heads) / T). More than 1,024 items are never split along the positions,
+ * and where a max_q far above their rows leaves them only the first count they are slow: each
+ * workgroup looks through all of them. */
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache* cache, int dtype, int64_t tokens,
                                          int64_t q_heads, int64_t seqs, int64_t max_q,
                                          int64_t max_kv);

@@ -143,3 +143,21 @@ def test_forks_of_many(nv, n):
     for a, b in copies:
         before[:, b] = before[:, a]
     assert torch.equal(c.pages, before)
+
+
+def test_thousands_of_items_with_no_bound(nv):
+    """6000 one-row items with max_q left at every row: too many workgroups by items and bounds, few enough
+    by rows. The bytes are those of the same items a thousand a call."""
+    H, G, D, n = 8, 8, 64, 6000
+    lens = [(i * 37) % 30 for i in range(n)]
+    c = make_cache(nv, lens, H, D, 16, seed=77)
+    fill_cache(nv, c, lens, 77)
+    new = [min(t, 1) if i % 10 else min(t, 3) for i, t in enumerate(lens)]
+    cu = [0] + torch.tensor(new).cumsum(0).tolist()
+    Q = _q(cu[-1], H * G, D, torch.bfloat16, 8)
+    out, lse = nv.kv_attention(c, 0, Q, i32(cu))
+    slots = i32(range(n))
+    for a in range(0, n, 1000):
+        t0, t1 = cu[a], cu[a + 1000]
+        part = nv.kv_attention(c, 0, Q[t0:t1], i32(x - t0 for x in cu[a:a + 1001]), slots[a:a + 1000])
+        assert torch.equal(out[t0:t1], part[0]) and torch.equal(lse[t0:t1], part[1]), a
