@@ -44,3 +44,30 @@ def test_the_largest_batches(n, heads, group, seqs, tokens, max_q, accepted):
     """Every batch that fits 2^24 workgroups by its rows, or by its items and bounds, is accepted."""
     got = _attend(n, _cache(n, heads, 64, 4), tokens, heads * group, 64, seqs, max_q, 64)
     assert got == (n.ERR_ALIGN if accepted else n.ERR_SHAPE)
+
+
+@pytest.mark.parametrize("tokens,max_q,heads,dim", [(4, 4, 2, 128), (1, 1, 8, 64), (300, 200, 2, 256)])
+def test_a_split_batch_needs_its_workspace(n, tokens, max_q, heads, dim):
+    """Batches that are split along the positions have a workspace, and a call without all of it is refused."""
+    cache = _cache(n, heads, dim, 1024)
+    need = n._lib.nvfp4_kv_attention_workspace_size(cache, 1, tokens, 4 * heads, 2, max_q, 16384)
+    assert need > 0
+    call = lambda **kw: _attend(n, cache, tokens, 4 * heads, dim, 2, max_q, 16384, lse=None, **kw)  # noqa: E731
+    assert call(ws_bytes=need - 1) == n.ERR_WORKSPACE
+    assert call(ws_bytes=0) == n.ERR_WORKSPACE
+    assert call(ws=None, ws_bytes=need) == n.ERR_WORKSPACE
+    assert call(ws=FAKE + 4, ws_bytes=need) == n.ERR_ALIGN
+
+
+def test_the_workspace_covers_smaller_plans(n):
+    """No bound on positions below the one a workspace was asked for needs more of it (a window shortens what a
+    call plans for)."""
+    size = n._lib.nvfp4_kv_attention_workspace_size
+    for heads, dim, group in ((1, 64, 1), (2, 128, 4), (8, 128, 4), (4, 256, 4), (3, 64, 7), (40, 128, 1)):
+        cache = _cache(n, heads, dim, 8192)
+        for seqs, new in ((1, 1), (4, 1), (16, 5), (60, 1), (3, 40), (2, 1000), (100, 2), (1024, 1), (1025, 1)):
+            last = 0
+            for span in (1, 31, 128, 129, 500, 641, 769, 1281, 1409, 2000, 5505, 9000, 40000, 131072):
+                need = size(cache, 1, seqs * new, heads * group, seqs, new, span)
+                assert need >= last, (heads, dim, group, seqs, new, span)
+                last = need
