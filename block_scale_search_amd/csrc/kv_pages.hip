@@ -44,7 +44,7 @@ __device__ __forceinline__ int wave_inclusive(int v) {
     return v;
 }
 
-// Exclusive prefix sum of v over a workgroup of WAVES waves; total gets the sum. `sums` holds WAVES + 1
+// Exclusive prefix sum of v over a workgroup of WAVES waves; total gets the sum. `sums` holds WAVES
 // words; the caller's threads may call it again at once.
 template <int WAVES>
 __device__ __forceinline__ int block_exclusive(int v, int* sums, int& total) {
