@@ -125,13 +125,13 @@ __device__ __forceinline__ int kv_find_item(const int32_t* __restrict__ cu, int 
     return lo;
 }
 
-// Two values rounded to bf16, to nearest even, a in the low half; NaN of any bits stays NaN.
+// Two values rounded to bf16, to nearest even, a in the low half; NaN of any bits stays NaN. The hardware's
+// conversion: for all 2^32 values the bits of rounding by integer steps (NaN aside), which takes several
+// instructions a value (a read of 4108 rows 9.6 us, with the conversion 8.8).
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-    const auto r = [](float v) {
-        const uint32_t u = __float_as_uint(v);
-        return v == v ? (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16 : 0x7FC0u;
-    };
-    return r(a) | (r(b) << 16);
+    typedef float f32_pair __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16_pair_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32_pair{a, b}), bf16_pair_t));
 }
 
 #endif  // __HIPCC__
