@@ -294,7 +294,8 @@ __device__ __forceinline__ void convert_query(QRow<D, BF16>& q, const RawQuery<D
     q.f = fmaxf(__builtin_ldexpf(scale, -k) * (S * kLog2e), 0x1p-126f);
 }
 
-// Waves a SIMD should hold: as many as the accumulators and two tiles in flight leave room for.
+// Waves a SIMD should hold: as many as the accumulators and two tiles in flight leave room for. (f32 queries take
+// more: at 32 rows 21 registers are spilled 64 wide, 36 at 256.)
 template <int D, int RT>
 constexpr int kOccupancy = D * RT <= 128 ? 4 : D * RT <= 256 ? 2 : 1;
 
@@ -748,6 +749,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // ragged, 63 and 83; 8 heads of 8: 4 over up to 131072 56 and 642). A prompt's tiles are 128 rows whose
 // partial outputs outweigh a few hundred positions: it is split below 256 tiles and from 6 units on, into
 // at least 2 units each (4 items of 200 rows over up to 2088 positions 26 us, not split 55).
+// Batches whose tiles fill the slots, or of more than kMaxScan items, are never split, however uneven: their
+// time is the longest item's in one workgroup a head (8 heads of 4, 127 slots of 2048 positions and one of
+// 131072: 867 us, where the bytes take 91).
 KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int64_t seqs, int64_t max_q,
                int64_t span) {
     const int64_t group = q_heads / heads, rows = max_q * group;
@@ -756,7 +760,8 @@ KvPlan plan_of(int64_t heads, int64_t dim, int64_t tokens, int64_t q_heads, int6
     p.tiles = (int32_t)ceil_div(rows, p.tile_rows);
     p.tiles = p.tiles > 0 ? p.tiles : 1;
     const bool prefill = p.tile_rows == kPrefillRows;
-    // workgroups that 256 compute units hold at once (registers and LDS)
+    // workgroups that 256 compute units are taken to hold at once; 64 wide the registers would let them hold
+    // three of prompts and six of few rows (bf16; f32 five of 16 rows)
     const int64_t slots = kUnits * (prefill ? (dim <= 128 ? 2 : 1)
                                  : dim * p.tile_rows <= 128 * 16 ? 4 : dim * p.tile_rows <= 256 * 16 ? 2 : 1);
     p.least = prefill ? 2 : 1;

@@ -84,6 +84,11 @@ __device__ __forceinline__ float row_factor(int k, float top, float S) {
                                                           : __builtin_nanf("");
 }
 
+// Weights enter the second product as f16, for f32 outputs in two halves (22 bits), for bf16 in one: an error of at
+// most 2^-11 of each weight, independent of the others, below the 2^-8 of the output's own rounding. Their sum
+// is taken in binary32, unrounded, for lse's sake. Error against 64 bits of 64 rows over up to 8192 positions:
+// 1.692e-3 with one half, 1.686e-3 with two, which take 55.9 us instead of 54.2 (one row over 1023 positions
+// 11.4 and 10.7, 32 drafts of 5 over up to 4096 36.3 and 32.9, two prompts of 8192 rows 1505 and 1138).
 constexpr float kUp = 8.0f;          // log2 of the weights' scale
 constexpr float kSlack = 7.0f;       // how far a logit may exceed the maximum in use, log2
 

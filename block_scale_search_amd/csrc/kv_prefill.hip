@@ -14,12 +14,14 @@
 // pieces of K, use all banks (4 heads of 4, 256 wide, two prompts of 4096 rows over 8192 positions: 1027 us,
 // with a permutation that only the reads need 1088).
 //
-// Rates (one MI355X): two prompts of 8192 rows, 8 heads of 4, 128 wide, bf16: 1.14 to 1.20 ms with the
-// clock, 920 to 965 TFLOP/s of the pairs that causal rows see; the matrix units are busy 46% of the cycles,
-// vector arithmetic 62%, one or the other 83%. 64 wide the exponentials weigh twice as much against the products (two prompts of 4096
-// rows over 8192 positions, 4 heads of 4: 313 us; 128 wide 472 us, 256 wide 1027 us). 256 wide a wave has a
-// SIMD for itself (registers and LDS), so its waits are not covered; making a tile's logits while the
-// previous tile's become weights gave nothing there (1059 us) nor 128 wide.
+// Rates (one MI355X): two prompts of 8192 rows, 8 heads of 4, 128 wide, bf16: 1.10 to 1.17 ms with the
+// clock, 940 to 1000 TFLOP/s of the pairs that causal rows see. Two prompts of 4096 rows over 8192 positions, 4
+// heads of 4: 128 wide 455 us, the matrix units busy 46% of the cycles, vector arithmetic 61%, one or the
+// other 82%; 64 wide, where the exponentials weigh twice as much against the products, 309 us (33%, 73%,
+// 85%); 256 wide 1011 us (34%, 45%, 67%): a wave has a SIMD for itself (registers and LDS), so its waits are
+// not covered; making a tile's logits while the previous tile's become weights gave nothing there (1059 us
+// against 1027) nor 128 wide. f32 has two products an operand: 64, 128 and 256 wide 452, 751 and 1742 us (the
+// last spills 36 registers).
 #include <hip/hip_runtime.h>
 
 #include "internal.h"

@@ -465,7 +465,9 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  * ceil(lens / page_size) pages; what the table's other entries hold does not matter. refs[p] is the number of
  * slots that hold page p (0: free). Full pages may be shared by several slots; a partly filled last
  * page belongs to one slot alone. A new cache has lens and refs zeroed and table filled with -1;
- * nvfp4_kv_reserve, _fork, _free and _compact keep these rules.
+ * nvfp4_kv_reserve, _fork, _free and _compact keep these rules. No call shortens a slot: a caller that
+ * lowers lens itself (rejected drafts) has to give the pages behind the new ceil(lens / page_size) back
+ * too (refs - 1), or the slot's next reserve takes others in their place and they are never free again.
  *
  * One layer of one page is a record of nvfp4_kv_page_bytes(heads, head_dim, page_size) =
  * heads * page_size * head_dim * 9 / 8 bytes with four regions back to back (H heads, P tokens,
@@ -547,6 +549,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, int64_t layer, void* K, 
  * infinity gets NaN, its lse too, as does every row of a head whose S_k is NaN or infinite. No row's bits
  * depend on another row's values. Query head j reads key/value head j / (q_heads / heads). Not causal:
  * every row sees the whole slot (e.g. an encoder's states).
+ *
+ * Logits are held in binary32: what a logit beyond its range gives is not specified. The call records no
+ * gradient: a 4-bit cache serves.
  *
  * The products run on f16 MFMA with binary32 sums: level * E4M3 has at most 6 significant bits and is
  * exact in f16; a bf16 query row is exact after a power-of-two scaling of the row; an f32 query
