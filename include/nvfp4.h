@@ -467,7 +467,8 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  * page belongs to one slot alone. A new cache has lens and refs zeroed and table filled with -1;
  * nvfp4_kv_reserve, _fork, _free and _compact keep these rules. No call shortens a slot: a caller that
  * lowers lens itself (rejected drafts) has to give the pages behind the new ceil(lens / page_size) back
- * too (refs - 1), or the slot's next reserve takes others in their place and they are never free again.
+ * too (refs - 1), or the slot's next reserve takes others in their place and they are never free again;
+ * and not to end inside a page that another slot holds, which the next append would change for both.
  *
  * One layer of one page is a record of nvfp4_kv_page_bytes(heads, head_dim, page_size) =
  * heads * page_size * head_dim * 9 / 8 bytes with four regions back to back (H heads, P tokens,
