@@ -1,0 +1,90 @@
+// Products with NVFP4 matrices: the views that the C-ABI layer (product_api.hip) makes of its checked
+// arguments, and the launchers of the kernel files.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace nvfp4 {
+
+// Matrices [out, in] of codes and scale bytes, `stride` weights apart, and their global scales.
+struct ProductMatrix {
+    const uint8_t* packed;
+    const uint8_t* scales;
+    const float* S;
+    int64_t stride;
+};
+
+// Which rows meet which matrix: rows seg[e] .. seg[e+1] - 1 matrix e; no seg: all rows matrix 0.
+struct ProductRows {
+    const int64_t* seg;
+    int64_t tokens;
+    int32_t batch;
+};
+
+// The activations' side, bf16 rows: `planes` parts of a value (1: bf16 itself, 3: the parts of a
+// binary32 value), `plane` elements apart. Columns past `k` up to the next multiple of 8 are zero.
+struct ProductOperand {
+    const uint16_t* p;
+    int64_t ld;
+};
+
+// One product. Forward: rows [in] times matrices' rows, out columns; gated: two matrices, out columns
+// each. Backward: rows [out] times matrices' columns, in columns; two matrices: their sum.
+struct Product {
+    ProductMatrix w[2];
+    int32_t matrices;
+    bool backward;
+    bool f32;                // outputs, bias and residual are binary32, else bf16
+    int64_t out, in;
+    ProductRows rows;
+    ProductOperand a[2];     // forward: a[0] only
+    int32_t planes;
+    int64_t plane;
+    // forward: y = act(z + bias) + residual, or act(g) * u; pre: z, or g and u. backward: y only.
+    int32_t act;
+    const void* bias;        // [batch, out] or null
+    const void* residual;    // or null
+    int64_t ldr;
+    void* pre[2];            // or null
+    int64_t ldpre[2];
+    void* y;
+    int64_t ldy;
+};
+
+// Workgroups of a product (its grid), for the caller's check that they fit.
+int64_t product_blocks(int64_t tokens, int64_t batch, bool segments, int64_t out, int64_t in,
+                       int32_t matrices, bool backward);
+hipError_t launch_product(const Product& p, hipStream_t stream);
+
+// bf16 parts of rows [tokens, cols] of dtype, padded with zeros to ld columns (a multiple of 8).
+hipError_t launch_product_parts(const void* X, bool f32, int64_t tokens, int64_t cols, int64_t ldx,
+                                uint16_t* parts, int64_t ld, int64_t plane, hipStream_t stream);
+
+// Gradients before a product's activation: dZ = dY act'(Z), or (U given) dG = dY U act'(G) and
+// dU = dY act(G), written to d1 (and d2) where given, and as parts where given. Rows of
+// no matrix are left alone.
+struct ProductSlopes {
+    ProductRows rows;
+    bool f32;
+    int64_t cols;
+    int32_t act;
+    const void* dY;
+    int64_t lddy;
+    const void* Z;           // null for no activation
+    int64_t ldz;
+    const void* U;
+    int64_t ldu;
+    void* d[2];
+    int64_t ldd[2];
+    uint16_t* parts[2];
+    int64_t ld, plane;
+};
+hipError_t launch_product_slopes(const ProductSlopes& p, hipStream_t stream);
+
+// dbias[e] = sum of dY act'(Z) over matrix e's rows, [batch, cols].
+size_t product_bias_workspace_bytes(int64_t tokens, int64_t batch, int64_t cols);
+hipError_t launch_product_bias(const ProductSlopes& p, float* dbias, void* workspace, hipStream_t stream);
+
+}  // namespace nvfp4

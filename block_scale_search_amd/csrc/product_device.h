@@ -1,0 +1,177 @@
+// Device pieces of the products with NVFP4 matrices for gfx950: codes to bf16 MFMA operands, activations
+// and their slopes, and the search for a workgroup's rows.
+//
+// Arithmetic. level * E4M3(scale) has at most 2 + 4 significant bits and lies in 2^-10 .. 2880, so it is
+// exact in bf16, and its product with a bf16 value is exact in binary32: the MFMA's sums are the only
+// roundings before the global scale S, which multiplies the sum. A scale byte is masked to 7 bits; the
+// codes of groups past the matrix's edge are multiplied by a scale of zero. (f16 operands would be a
+// third cheaper to make, but bf16 activations fit f16's range only after a scaling of each row, which
+// loses what is 2^-39 of the row's largest value even where that value meets zeros.)
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_formats.h"
+#include "kv_cache.h"
+#include "product.h"
+
+namespace nvfp4 {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Rows of codes start at multiples of 8 bytes, rows of scale bytes anywhere.
+typedef u32x4 u32x4_at8 __attribute__((aligned(8)));
+typedef u32x2 u32x2_at8 __attribute__((aligned(8)));
+typedef uint16_t u16_at1 __attribute__((aligned(1)));
+
+enum ProductAct { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3, kActRelu = 4 };
+
+// Scale byte B of `bytes` as binary32.
+template <int B>
+__device__ __forceinline__ float scale_value(uint32_t bytes) {
+    return __builtin_amdgcn_cvt_f32_fp8(bytes & 0x7F7F7F7Fu, B);
+}
+
+// Values of the two codes in byte B of w.
+template <int B>
+__device__ __forceinline__ void code_values(uint32_t w, float scale, float& x, float& y) {
+    const auto v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, B);
+    x = v[0] * scale;
+    y = v[1] * scale;
+}
+
+// Eight codes times their scale as bf16, exact.
+__device__ __forceinline__ u32x4 dequant8(uint32_t w, float scale) {
+    float x[8];
+    code_values<0>(w, scale, x[0], x[1]);
+    code_values<1>(w, scale, x[2], x[3]);
+    code_values<2>(w, scale, x[4], x[5]);
+    code_values<3>(w, scale, x[6], x[7]);
+    return u32x4{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
+}
+
+// act(z). bf16 outputs use the hardware's exponential and reciprocal (a few binary32 steps off, far
+// below 2^-9); binary32 ones the library's functions and IEEE division.
+template <bool F32>
+__device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (F32) return 1.0f / (1.0f + expf(-z));
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+}
+// 0.5 (1 + tanh v) is sigmoid(2 v), v = sqrt(2 / pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float gelu_tanh_arg(float z) {
+    return 1.5957691216057308f * z * __builtin_fmaf(0.044715f * z, z, 1.0f);
+}
+
+template <bool F32>
+__device__ __forceinline__ float act_value(int act, float z) {
+    switch (act) {
+        case kActSilu: return z * sigmoid<F32>(z);
+        case kActGelu: return 0.5f * z * erfcf(-0.7071067811865476f * z);
+        case kActGeluTanh: return z * sigmoid<F32>(gelu_tanh_arg(z));
+        case kActRelu: return z > 0.0f ? z : (z == z ? 0.0f : z);
+        default: return z;
+    }
+}
+
+// act(z) and act'(z).
+template <bool F32>
+__device__ __forceinline__ void act_slope(int act, float z, float& a, float& slope) {
+    switch (act) {
+        case kActSilu: {
+            const float p = sigmoid<F32>(z);
+            a = z * p;
+            slope = __builtin_fmaf(a, 1.0f - p, p);
+            return;
+        }
+        case kActGelu: {
+            const float cdf = 0.5f * erfcf(-0.7071067811865476f * z);
+            a = z * cdf;
+            slope = __builtin_fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), cdf);
+            return;
+        }
+        case kActGeluTanh: {
+            const float p = sigmoid<F32>(gelu_tanh_arg(z));
+            const float c = fminf(fmaxf(z, -32.0f), 32.0f);     // beyond, p is 0 or 1 and z^3 may overflow
+            a = z * p;
+            slope = __builtin_fmaf(c * p * (1.0f - p), 1.5957691216057308f * __builtin_fmaf(0.134145f * c, c, 1.0f), p);
+            return;
+        }
+        case kActRelu:
+            a = act_value<F32>(act, z);
+            slope = z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
+            return;
+        default:
+            a = z;
+            slope = 1.0f;
+    }
+}
+
+__device__ __forceinline__ float load_value(const void* p, int64_t i, bool f32) {
+    if (f32) return static_cast<const float*>(p)[i];
+    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+}
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return (uint16_t)bf16_pair(x, 0.0f); }
+__device__ __forceinline__ void store_value(void* p, int64_t i, float x, bool f32) {
+    if (f32) static_cast<float*>(p)[i] = x;
+    else static_cast<uint16_t*>(p)[i] = bf16_bits(x);
+}
+
+// Rows of matrix e, inside the tokens whatever the offsets hold.
+__device__ __forceinline__ void segment(const ProductRows& r, int e, int64_t& lo, int64_t& hi) {
+    lo = min(max(r.seg[e], (int64_t)0), r.tokens);
+    hi = min(max(r.seg[e + 1], lo), r.tokens);
+}
+
+// First row that belongs to no matrix.
+__device__ __forceinline__ int64_t rows_end(const ProductRows& r) {
+    return r.seg ? min(max(r.seg[r.batch], (int64_t)0), r.tokens) : r.tokens;
+}
+
+// A workgroup's rows: `rows` from `first`, all of matrix `e`.
+struct RowTile {
+    int32_t e, rows;
+    int64_t first;
+};
+
+// Tile `tile` of the matrices' rows in tiles of `size`, numbered matrix by matrix. Each wave finds it by
+// itself (64 matrices at a time); false past the last.
+__device__ __forceinline__ bool find_rows(const ProductRows& r, int tile, int size, RowTile& t) {
+    if (r.seg == nullptr) {
+        t.e = 0;
+        t.first = (int64_t)tile * size;
+        t.rows = (int32_t)min((int64_t)size, r.tokens - t.first);
+        return t.rows > 0;
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int base = 0; base < r.batch; base += 64) {
+        int64_t lo = 0, hi = 0;
+        if (base + lane < r.batch) segment(r, base + lane, lo, hi);
+        const int n = (int)((hi - lo + size - 1) / size);
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += v;
+        }
+        const uint64_t in = __ballot(before + upto > tile);
+        if (in) {
+            const int at = __builtin_ctzll(in);
+            const int64_t first = lo + (int64_t)(tile - before - (upto - n)) * size;
+            const int rows = (int)min((int64_t)size, hi - first);
+            t.e = base + at;
+            t.rows = __builtin_amdgcn_readlane(rows, at);
+            t.first = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)first, at) |
+                                ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(first >> 32), at) << 32));
+            return t.rows > 0;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+}  // namespace nvfp4

@@ -10,6 +10,7 @@ there is no CPU path. Importing this module fails if the library has not been bu
 The convenience wrappers at the end (``diag_hessian``, ``layer_statistics``, ``global_scale``,
 ``scale_search``, ``scale_search_rules``, ``scale_search_proposal``, ``pack``, ``quantize_activations``, ``gptq``,
 ``output_error``) allocate outputs and workspaces with torch and call the entry points.
+``Matrix`` describes quantised matrices; ``linear``, ``gated`` and their ``_backward`` multiply by them.
 ``KVCache`` describes a paged key/value cache; the ``kv_*`` wrappers take one and a layer.
 """
 from __future__ import annotations
@@ -28,6 +29,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_WINDOW, ERR_ARG, ERR_WORKSPAC
 DTYPE_F32, DTYPE_BF16 = 0, 1
 MSE, WMSE = 0, 1
 GS_AMAX_448, GS_AMAX_256 = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(5)
 
 _P, _I64, _I32, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_size_t
 
@@ -37,6 +39,12 @@ class SearchRule(ctypes.Structure):
                 ("exhaustive", ctypes.c_int32), ("scales", ctypes.c_void_p),
                 ("packed", ctypes.c_void_p), ("loss", ctypes.c_void_p),
                 ("offset", ctypes.c_void_p)]
+
+
+class MatrixStruct(ctypes.Structure):
+    """``nvfp4_matrix``."""
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("S", ctypes.c_void_p),
+                ("batch", _I64), ("out", _I64), ("in_", _I64), ("stride", _I64)]
 
 
 class KVCacheStruct(ctypes.Structure):
@@ -82,6 +90,16 @@ _SIGS = {
     "nvfp4_output_error_workspace_size": ([_I64, _I64, _I64], _SZ),
     "nvfp4_output_error": ([_P, _I, _I64, _I64, _I64, _P, _I, _I64, _I64, _P, _P, _P, _P, _I,
                             _P, _SZ, _P], _I),
+    "nvfp4_linear_workspace_size": ([_I, _I64, _I64, _I64, _I64], _SZ),
+    "nvfp4_linear": ([_P, _P, _I, _I64, _I64, _P, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P], _I),
+    "nvfp4_gated_workspace_size": ([_I, _I64, _I64, _I64, _I64], _SZ),
+    "nvfp4_gated": ([_P, _P, _P, _I, _I64, _I64, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P], _I),
+    "nvfp4_linear_backward_workspace_size": ([_I, _I64, _I64, _I64, _I64, _I], _SZ),
+    "nvfp4_linear_backward": ([_P, _P, _I, _I64, _I64, _P, _I, _P, _I64, _P, _I64, _P, _P, _I64, _P,
+                               _SZ, _P], _I),
+    "nvfp4_gated_backward_workspace_size": ([_I, _I64, _I64, _I64, _I64], _SZ),
+    "nvfp4_gated_backward": ([_P, _P, _P, _I, _I64, _I64, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P,
+                              _I64, _P, _I64, _P, _SZ, _P], _I),
     "nvfp4_kv_page_bytes": ([_I32, _I32, _I32], _SZ),
     "nvfp4_kv_append": ([_P, _I64, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I32,
                          _I32, _P], _I),
@@ -431,6 +449,170 @@ KV_DONE, KV_BAD_SLOT, KV_BAD_LENGTH, KV_NO_PAGES = range(4)
 
 def nvfp4_kv_page_bytes(heads: int, head_dim: int, page_size: int) -> int:
     return int(_lib.nvfp4_kv_page_bytes(heads, head_dim, page_size))
+
+
+class Matrix:
+    """``nvfp4_matrix``: codes, scale bytes and global scales of one matrix or a batch, as ``scale_search`` or
+    ``gptq`` return them: packed [out, in/2] or [batch, out, in/2] uint8, scales [out, in/16] or
+    [batch, out, in/16] uint8, S [batch] float32. Rows are contiguous; the matrices of a batch may lie
+    apart (a slice of rows of a larger batch). The tensors are kept, not copied."""
+
+    def __init__(self, packed, scales, S):
+        for name, t in (("packed", packed), ("scales", scales)):
+            _dev(t, name, (torch.uint8,))
+        if packed.dim() not in (2, 3) or scales.dim() != packed.dim():
+            raise ValueError("packed and scales must both be 2-D or both 3-D")
+        batch = packed.shape[0] if packed.dim() == 3 else 1
+        out, half = packed.shape[-2:]
+        if half % 8 or tuple(scales.shape) != tuple(packed.shape[:-1]) + (half // 8,):
+            raise ValueError("packed must be [.., out, in/2] and scales [.., out, in/16] of the same matrices")
+        rows = lambda t: t.stride(-1) == 1 and (out == 1 or t.stride(-2) == t.shape[-1])  # noqa: E731
+        if batch * out and half and not (rows(packed) and rows(scales)):
+            raise ValueError("rows of packed and scales must be contiguous")
+        stride = 2 * packed.stride(0) if batch > 1 else 2 * out * half
+        if batch > 1 and 16 * scales.stride(0) != stride:
+            raise ValueError("the matrices of packed and of scales must lie equally far apart")
+        _dev(S, "S", (torch.float32,))
+        _need(S, batch, "S")
+        if scales.device != packed.device or S.device != packed.device:
+            raise ValueError("packed, scales and S must be on one device")
+        self.packed, self.scales, self.S = packed, scales, S
+        self.batch, self.out, self.inp = batch, out, 2 * half
+        self.device, self.index = packed.device, packed.get_device()
+        self.struct = MatrixStruct(packed.data_ptr(), scales.data_ptr(), S.data_ptr(), batch, out, 2 * half,
+                                   stride)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _on_device(index: int, f, args: tuple, fname: str, stream, prepare: bool):
+    """Calls entry point f with args on `stream` (None: the device's current one), with that device current."""
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if not prepare and torch._C._cuda_getDevice() == index:
+        status = f(*args, s)
+        if status:
+            raise Nvfp4Error(status, fname)
+        return None
+
+    def call():
+        old = torch._C._cuda_getDevice()
+        torch.cuda.set_device(index)
+        try:
+            _check(f(*args, s), fname)
+        finally:
+            torch.cuda.set_device(old)
+    return call if prepare else call()
+
+
+def _on(W: Matrix, t, name: str, dtype=None, numel: int | None = None):
+    """Address of a tensor on the matrices' device, of this dtype and (contiguous) at least numel elements."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a tensor on the GPU")
+    if t.get_device() != W.index:
+        raise ValueError(f"{name} must be on the matrices' device {W.device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if numel is not None and (not t.is_contiguous() or t.numel() < numel):
+        _need(t, numel, name)
+    return t.data_ptr()
+
+
+def _rows(W: Matrix, t, tokens: int, cols: int, dtype, name: str):
+    """A row tensor [tokens, cols] with contiguous rows: address and row stride."""
+    if t is None:
+        return None, cols
+    p = _on(W, t, name, dtype)
+    if t.dim() != 2 or t.shape[0] != tokens or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{tokens}, {cols}] with contiguous rows")
+    return p, t.stride(0) if tokens > 1 else max(t.stride(0), cols)
+
+
+def _segments(W: Matrix, seg_offsets):
+    if seg_offsets is not None and seg_offsets.numel() != W.batch + 1:
+        raise ValueError(f"seg_offsets must have {W.batch + 1} elements")
+    return _on(W, seg_offsets, "seg_offsets", torch.int64, W.batch + 1)
+
+
+def _space(W: Matrix, t):
+    if t is None:
+        return None, 0
+    return _on(W, t, "workspace", None, 0), t.numel() * t.element_size()
+
+
+def _dtype_code(dtype) -> int:
+    """dtype: torch.bfloat16 or torch.float32."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype {dtype} is not supported: torch.bfloat16 or torch.float32")
+    return DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
+
+
+def nvfp4_linear_workspace_size(dtype, tokens, batch, out, inp) -> int:
+    return _lib.nvfp4_linear_workspace_size(_dtype_code(dtype), tokens, batch, out, inp)
+
+
+def nvfp4_linear(W: Matrix, X, tokens, seg_offsets, bias, activation, residual, Z, Y, workspace, stream=None,
+                 prepare=False):
+    dt = X.dtype
+    x, r = _rows(W, X, tokens, W.inp, None, "X"), _rows(W, residual, tokens, W.out, dt, "residual")
+    z, y = _rows(W, Z, tokens, W.out, dt, "Z"), _rows(W, Y, tokens, W.out, dt, "Y")
+    return _on_device(W.index, _lib.nvfp4_linear, (
+        W.ref, x[0], _dtype_code(dt), tokens, x[1], _segments(W, seg_offsets),
+        _on(W, bias, "bias", dt, W.batch * W.out), activation, *r, *z, *y, *_space(W, workspace)),
+        "nvfp4_linear", stream, prepare)
+
+
+def nvfp4_gated_workspace_size(dtype, tokens, batch, out, inp) -> int:
+    return _lib.nvfp4_gated_workspace_size(_dtype_code(dtype), tokens, batch, out, inp)
+
+
+def _pair(W_gate: Matrix, W_up: Matrix):
+    if W_up.index != W_gate.index:
+        raise ValueError("W_gate and W_up must be on one device")
+
+
+def nvfp4_gated(W_gate: Matrix, W_up: Matrix, X, tokens, seg_offsets, activation, G, U, H, workspace,
+                stream=None, prepare=False):
+    _pair(W_gate, W_up)
+    W, dt = W_gate, X.dtype
+    x, g = _rows(W, X, tokens, W.inp, None, "X"), _rows(W, G, tokens, W.out, dt, "G")
+    u, h = _rows(W, U, tokens, W.out, dt, "U"), _rows(W, H, tokens, W.out, dt, "H")
+    return _on_device(W.index, _lib.nvfp4_gated, (
+        W.ref, W_up.ref, x[0], _dtype_code(dt), tokens, x[1], _segments(W, seg_offsets), activation,
+        *g, *u, *h, *_space(W, workspace)), "nvfp4_gated", stream, prepare)
+
+
+def nvfp4_linear_backward_workspace_size(dtype, tokens, batch, out, inp, with_bias) -> int:
+    return _lib.nvfp4_linear_backward_workspace_size(_dtype_code(dtype), tokens, batch, out, inp,
+                                                     int(with_bias))
+
+
+def nvfp4_linear_backward(W: Matrix, dY, tokens, seg_offsets, activation, Z, dZ, dbias, dX, workspace,
+                          stream=None, prepare=False):
+    dt = dY.dtype
+    y, z = _rows(W, dY, tokens, W.out, None, "dY"), _rows(W, Z, tokens, W.out, dt, "Z")
+    d, x = _rows(W, dZ, tokens, W.out, dt, "dZ"), _rows(W, dX, tokens, W.inp, dt, "dX")
+    return _on_device(W.index, _lib.nvfp4_linear_backward, (
+        W.ref, y[0], _dtype_code(dt), tokens, y[1], _segments(W, seg_offsets), activation, *z, *d,
+        _on(W, dbias, "dbias", torch.float32, W.batch * W.out), *x, *_space(W, workspace)),
+        "nvfp4_linear_backward", stream, prepare)
+
+
+def nvfp4_gated_backward_workspace_size(dtype, tokens, batch, out, inp) -> int:
+    return _lib.nvfp4_gated_backward_workspace_size(_dtype_code(dtype), tokens, batch, out, inp)
+
+
+def nvfp4_gated_backward(W_gate: Matrix, W_up: Matrix, dH, tokens, seg_offsets, activation, G, U, dG, dU,
+                         dX, workspace, stream=None, prepare=False):
+    _pair(W_gate, W_up)
+    W, dt = W_gate, dH.dtype
+    rows = [_rows(W, t, tokens, W.out, dt, name) for t, name in
+            ((G, "G"), (U, "U"), (dG, "dG"), (dU, "dU"))]
+    h, x = _rows(W, dH, tokens, W.out, None, "dH"), _rows(W, dX, tokens, W.inp, dt, "dX")
+    return _on_device(W.index, _lib.nvfp4_gated_backward, (
+        W.ref, W_up.ref, h[0], _dtype_code(dt), tokens, h[1], _segments(W, seg_offsets), activation,
+        *rows[0], *rows[1], *rows[2], *rows[3], *x, *_space(W, workspace)),
+        "nvfp4_gated_backward", stream, prepare)
 
 
 class KVCache:
@@ -846,6 +1028,71 @@ def pack(W: torch.Tensor, scales: torch.Tensor, S: torch.Tensor, stream=None) ->
     packed = torch.empty(scales.shape[:-1] + (n // 2,), dtype=torch.uint8, device=W.device)
     nvfp4_pack(W, b, o, n, ldw, sw, scales, S, packed, stream)
     return packed
+
+
+def _empty(W: Matrix, shape, dtype, stream):
+    """A tensor on the matrices' device that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=W.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=W.device)
+
+
+def linear(W: Matrix, X: torch.Tensor, bias: torch.Tensor | None = None, activation: int = ACT_NONE,
+           residual: torch.Tensor | None = None, seg_offsets: torch.Tensor | None = None,
+           with_pre: bool = False, stream=None):
+    """act(X W^T + bias) + residual of X [tokens, in], bias [batch, out], residual [tokens, out]; returns
+    Y [tokens, out], or (Y, Z) with the values before the activation. seg_offsets int64 [batch + 1]: which
+    rows belong to which matrix of a batch; rows behind the last are not written. No gradient is
+    recorded: linear_backward computes it."""
+    T = X.shape[0]
+    Y = _empty(W, (T, W.out), X.dtype, stream)
+    Z = _empty(W, (T, W.out), X.dtype, stream) if with_pre else None
+    need = nvfp4_linear_workspace_size(X.dtype, T, W.batch, W.out, W.inp)
+    ws = _empty(W, need, torch.uint8, stream) if need else None
+    nvfp4_linear(W, X, T, seg_offsets, bias, activation, residual, Z, Y, ws, stream)
+    return (Y, Z) if with_pre else Y
+
+
+def gated(W_gate: Matrix, W_up: Matrix, X: torch.Tensor, activation: int = ACT_SILU,
+          seg_offsets: torch.Tensor | None = None, with_pre: bool = False, stream=None):
+    """act(X W_gate^T) * (X W_up^T) of X [tokens, in]; returns H [tokens, out], or (H, G, U) with the two
+    products. Rows and gradients as in linear."""
+    T, W = X.shape[0], W_gate
+    H = _empty(W, (T, W.out), X.dtype, stream)
+    G, U = (_empty(W, (T, W.out), X.dtype, stream) if with_pre else None for _ in range(2))
+    need = nvfp4_gated_workspace_size(X.dtype, T, W.batch, W.out, W.inp)
+    ws = _empty(W, need, torch.uint8, stream) if need else None
+    nvfp4_gated(W, W_up, X, T, seg_offsets, activation, G, U, H, ws, stream)
+    return (H, G, U) if with_pre else H
+
+
+def linear_backward(W: Matrix, dY: torch.Tensor, Z: torch.Tensor | None = None, activation: int = ACT_NONE,
+                    seg_offsets: torch.Tensor | None = None, with_bias: bool = False, stream=None) -> dict:
+    """Gradients of linear from dY [tokens, out] (the residual's is dY itself) and, with an activation, Z:
+    dX [tokens, in], dZ [tokens, out] (None without an activation: dY) and dbias float32 [batch, out]
+    (None unless asked for)."""
+    T = dY.shape[0]
+    dX = _empty(W, (T, W.inp), dY.dtype, stream)
+    dZ = _empty(W, (T, W.out), dY.dtype, stream) if activation != ACT_NONE else None
+    dbias = _empty(W, (W.batch, W.out), torch.float32, stream) if with_bias else None
+    need = nvfp4_linear_backward_workspace_size(dY.dtype, T, W.batch, W.out, W.inp, with_bias)
+    ws = _empty(W, need, torch.uint8, stream) if need else None
+    nvfp4_linear_backward(W, dY, T, seg_offsets, activation, Z, dZ, dbias, dX, ws, stream)
+    return {"dX": dX, "dZ": dZ, "dbias": dbias}
+
+
+def gated_backward(W_gate: Matrix, W_up: Matrix, dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
+                   activation: int = ACT_SILU, seg_offsets: torch.Tensor | None = None,
+                   stream=None) -> dict:
+    """Gradients of gated from dH, G and U [tokens, out]: dX [tokens, in], dG and dU [tokens, out]."""
+    T, W = dH.shape[0], W_gate
+    dX = _empty(W, (T, W.inp), dH.dtype, stream)
+    dG, dU = (_empty(W, (T, W.out), dH.dtype, stream) for _ in range(2))
+    need = nvfp4_gated_backward_workspace_size(dH.dtype, T, W.batch, W.out, W.inp)
+    ws = _empty(W, need, torch.uint8, stream) if need else None
+    nvfp4_gated_backward(W, W_up, dH, T, seg_offsets, activation, G, U, dG, dU, dX, ws, stream)
+    return {"dX": dX, "dG": dG, "dU": dU}
 
 
 def _kv_empty(cache: KVCache, shape, dtype, stream):

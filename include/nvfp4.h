@@ -453,6 +453,107 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
                                 size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Products with quantised matrices: what a layer computes with the codes and scale bytes that the search,
+ * GPTQ or the proposal search wrote ([SS] Experimental Results: weight-only and WA settings; [SR] §1: E2M1 values
+ * share an E4M3 scale), and the gradients that pass through it.
+ *
+ *   w[e, o, i] = S[e] * level * E4M3(scale byte)      level and scale byte as nvfp4_pack and the search write them
+ *
+ * The struct describes `batch` matrices [out, in] in device memory, `stride` weights apart (the codes
+ * stride / 2 bytes, the scale bytes stride / 16); it is read during the call only. batch 1 is one layer;
+ * the experts of a layer are a batch, and seg_offsets (device int64 [batch + 1], non-decreasing from 0, as
+ * in nvfp4_diag_hessian_batched) gives expert e the rows seg_offsets[e] .. seg_offsets[e+1] - 1 of every
+ * row tensor. Rows behind seg_offsets[batch] are not read as any expert's and are left as they are in the
+ * outputs. seg_offsets NULL: batch must be 1 and has all rows. Offsets are clamped to 0 .. tokens on the
+ * device; offsets that do not rise give unspecified values in the rows, nothing outside them.
+ *
+ * Row tensors are bf16 or f32 (dtype, the same for all of a call; bias too), with a row stride in elements
+ * of at least their columns. Sums are binary32: level * E4M3 is exact in bf16, a bf16 value enters the MFMA
+ * products as it is and an f32 value as three bf16 parts (exact for magnitudes that are zero or above 2^-100), so
+ * the products themselves are exact. Outputs are rounded once (to nearest even), from binary32. A row with
+ * a NaN or an infinity has unspecified results in that row (rows, never others). A tensor of outputs may
+ * not overlap any other tensor of the call, but Y may be the residual itself (same address, same stride).
+ *
+ * Requires in % 16 == 0, in >= 16, out >= 1 (a product with an empty matrix is refused), out * in / 16 < 2^31,
+ * tokens < 2^31, batch <= 65,535, packed 8-byte aligned, stride a multiple of 16. tokens == 0 is valid.
+ * Workspaces: 16-byte aligned, no initialisation needed, of at least the size that the query of the same
+ * name gives for the same sizes (NULL is valid where that is 0).
+ * ------------------------------------------------------------------------------------------- */
+typedef struct nvfp4_matrix {
+    const uint8_t* packed;   /* device, [batch][out, in/2] */
+    const uint8_t* scales;   /* device, [batch][out, in/16], codes 0..126 */
+    const float* S;          /* device, [batch], positive */
+    int64_t batch;
+    int64_t out;
+    int64_t in;
+    int64_t stride;          /* weights from one matrix to the next (not used when batch is 1) */
+} nvfp4_matrix;
+
+/* Activations. GELU is z * Phi(z), GELU_TANH its approximation 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+typedef enum nvfp4_activation {
+    NVFP4_ACT_NONE = 0,
+    NVFP4_ACT_SILU = 1,
+    NVFP4_ACT_GELU = 2,
+    NVFP4_ACT_GELU_TANH = 3,
+    NVFP4_ACT_RELU = 4
+} nvfp4_activation;
+
+/* Linear layer:
+ *   z[t, o] = sum_i X[t, i] w[e, o, i] + bias[e, o]         e: the row's matrix
+ *   Y[t, o] = act(z[t, o]) + residual[t, o]
+ * X        [tokens, in], 16-byte aligned rows.
+ * bias     [batch, out] or NULL; residual [tokens, out] or NULL.
+ * Z        [tokens, out] or NULL: receives z, which nvfp4_linear_backward takes.
+ * Y        [tokens, out]. */
+size_t nvfp4_linear_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out, int64_t in);
+
+nvfp4_status nvfp4_linear(const nvfp4_matrix* W, const void* X, int dtype, int64_t tokens, int64_t ldx,
+                          const int64_t* seg_offsets, const void* bias, int activation,
+                          const void* residual, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gated pair of projections, the first half of a gated feed-forward block:
+ *   g = X W_gate^T,  u = X W_up^T,  H[t, o] = act(g[t, o]) * u[t, o]
+ * The two matrices have the same batch, out and in.
+ * G, U     [tokens, out], both or neither NULL: receive g and u, which nvfp4_gated_backward takes.
+ * H        [tokens, out]. X as for nvfp4_linear. */
+size_t nvfp4_gated_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out, int64_t in);
+
+nvfp4_status nvfp4_gated(const nvfp4_matrix* W_gate, const nvfp4_matrix* W_up, const void* X, int dtype,
+                         int64_t tokens, int64_t ldx, const int64_t* seg_offsets, int activation, void* G,
+                         int64_t ldg, void* U, int64_t ldu, void* H, int64_t ldh, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Gradients of nvfp4_linear (the matrix itself is fixed and has none; the residual's is dY):
+ *   dZ = dY * act'(Z),   dX[t, i] = sum_o dZ[t, o] w[e, o, i],   dbias[e, o] = sum of dZ over e's rows
+ * dY       [tokens, out]. Z, dZ: [tokens, out], not used with NVFP4_ACT_NONE (may be NULL), where dZ is
+ *          dY. dZ enters dX's product as dtype holds it (bf16: rounded); dbias sums the unrounded.
+ * dbias    float [batch, out] or NULL (0 for a matrix without rows).
+ * dX       [tokens, in].
+ * bf16 with out % 8 == 0: rows of dY (NVFP4_ACT_NONE) or of dZ are 16-byte aligned. RELU's slope at 0 is 0. */
+size_t nvfp4_linear_backward_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out,
+                                            int64_t in, int with_bias);
+
+nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dtype, int64_t tokens,
+                                   int64_t lddy, const int64_t* seg_offsets, int activation,
+                                   const void* Z, int64_t ldz, void* dZ, int64_t lddz, float* dbias,
+                                   void* dX, int64_t lddx, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Gradients of nvfp4_gated:
+ *   dG = dH * U * act'(G),  dU = dH * act(G),  dX = dG W_gate + dU W_up
+ * dH, G, U, dG, dU  [tokens, out]; dX [tokens, in]. dG and dU enter the product as dtype holds them.
+ * bf16 with out % 8 == 0: rows of dG and dU are 16-byte aligned. */
+size_t nvfp4_gated_backward_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out,
+                                           int64_t in);
+
+nvfp4_status nvfp4_gated_backward(const nvfp4_matrix* W_gate, const nvfp4_matrix* W_up, const void* dH,
+                                  int dtype, int64_t tokens, int64_t lddh, const int64_t* seg_offsets,
+                                  int activation, const void* G, int64_t ldg, const void* U, int64_t ldu,
+                                  void* dG, int64_t lddg, void* dU, int64_t lddu, void* dX, int64_t lddx,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Key/value cache in NVFP4 ([SS] Experimental Results: the WAKV and WAKVQ settings quantise the KV
  * cache with the same sweep as weights and activations). Tokens' keys and values live in pages of
  * `page_size` tokens as 4-bit codes with one E4M3 scale byte per 16 values; the FP32 global scales

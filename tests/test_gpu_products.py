@@ -1,0 +1,189 @@
+"""Products with NVFP4 matrices against the 64-bit model: sizes around every tile's edge with sums that are
+exact in binary32 (the outputs then have to be the rounded exact values), activations, experts, gradients."""
+import pytest
+import torch
+
+from product_helpers import (ACTS, DEV, HALF_STEP, Weights, act, act_error, act_model, by_row, close, offsets,
+                             product, rows, sum_error)
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+DTYPES = pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "f32"))
+
+SIZES = [(1, 1, 16), (1, 16, 32), (2, 17, 48), (3, 128, 64), (1, 333, 2064), (5, 64, 1040), (15, 33, 80), (16, 129, 128),
+         (17, 127, 144), (31, 250, 16), (33, 128, 272), (48, 48, 512), (63, 257, 256), (64, 256, 336), (65, 96, 128),
+         (127, 130, 64), (128, 128, 1024), (129, 129, 528), (200, 1, 96), (255, 255, 256), (256, 512, 144),
+         (257, 300, 1040), (512, 640, 192), (700, 260, 64)]
+
+
+def same(got, want, dtype, what):
+    """Equal to the exact value rounded once (whole numbers: the sums are exact)."""
+    assert torch.equal(got.cpu(), want.to(F32).to(dtype)), what
+
+
+@DTYPES
+@pytest.mark.parametrize("T, out, inp", SIZES)
+def test_linear_is_the_rounded_exact_sum(nv, T, out, inp, dtype):
+    w = Weights(1, out, inp, 10 * T + out, whole=True)
+    x, r = rows((T, inp), dtype, 1, whole=True), rows((T, out), dtype, 2, whole=True)
+    b = rows((1, out), dtype, 3, whole=True)
+    z = product(x, w, [T])[0]
+    m = w.matrix(nv, squeeze=True)
+    same(nv.linear(m, x.to(DEV)), z, dtype, "Y")
+    y, pre = nv.linear(m, x.to(DEV), bias=b.to(DEV), activation=nv.ACT_RELU, residual=r.to(DEV), with_pre=True)
+    z = z + b.double()
+    same(pre, z, dtype, "Z")
+    same(y, z.clamp(min=0) + r.double(), dtype, "Y of all")
+
+
+@DTYPES
+@pytest.mark.parametrize("T, out, inp", SIZES)
+def test_gated_is_the_rounded_exact_sum(nv, T, out, inp, dtype):
+    w, v = Weights(1, out, inp, 10 * T + out, whole=True), Weights(1, out, inp, 7 * T + out, whole=True)
+    x = rows((T, inp), dtype, 1, whole=True)
+    x[:, 3:] = torch.where(torch.rand((T, inp - 3), generator=torch.Generator().manual_seed(5)) < 0.9, 0, x[:, 3:])
+    g, u = product(x, w, [T])[0], product(x, v, [T])[0]
+    h, gg, uu = nv.gated(w.matrix(nv), v.matrix(nv), x.to(DEV), activation=nv.ACT_RELU, with_pre=True)
+    same(gg, g, dtype, "G")
+    same(uu, u, dtype, "U")
+    # g and u are exact; their product is rounded to binary32, then to dtype
+    close(h, g.clamp(min=0) * u, (g * u).abs() * 2.0 ** -24, dtype, "H")
+    assert torch.equal(nv.gated(w.matrix(nv), v.matrix(nv), x.to(DEV), activation=nv.ACT_RELU), h)
+
+
+@DTYPES
+@pytest.mark.parametrize("T, out, inp", SIZES)
+def test_gradient_is_the_rounded_exact_sum(nv, T, out, inp, dtype):
+    w, v = Weights(1, out, inp, 10 * T + out, whole=True), Weights(1, out, inp, 7 * T + out, whole=True)
+    d = rows((T, out), dtype, 1, whole=True)
+    r = nv.linear_backward(w.matrix(nv), d.to(DEV), with_bias=True)
+    same(r["dX"], product(d, w, [T], False)[0], dtype, "dX")
+    same(r["dbias"], d.double().sum(0, keepdim=True), F32, "dbias")
+    assert r["dZ"] is None
+    # gate and up: relu and whole numbers; S of the two differ by powers of two
+    g, u = rows((T, out), dtype, 2, whole=True), rows((T, out), dtype, 3, whole=True)
+    r = nv.gated_backward(w.matrix(nv), v.matrix(nv), d.to(DEV), g.to(DEV), u.to(DEV), activation=nv.ACT_RELU)
+    dg, du = d.double() * u.double() * (g > 0), d.double() * g.double().clamp(min=0)
+    same(r["dG"], dg, dtype, "dG")
+    same(r["dU"], du, dtype, "dU")
+    same(r["dX"], product(dg, w, [T], False)[0] + product(du, v, [T], False)[0], dtype, "dX of two")
+
+
+@DTYPES
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("T, out, inp", [(1, 130, 272), (19, 70, 528), (150, 200, 336)])
+def test_linear_values(nv, T, out, inp, name, dtype):
+    w = Weights(1, out, inp, T, whole=False)
+    x, r, b = rows((T, inp), dtype, 1, 0.3), rows((T, out), dtype, 2), rows((1, out), dtype, 3)
+    z, size = product(x, w, [T])
+    z = z + b.double()
+    error = sum_error(size + b.double().abs(), inp, dtype)
+    y, pre = nv.linear(w.matrix(nv), x.to(DEV), bias=b.to(DEV), activation=act(nv, name), residual=r.to(DEV),
+                       with_pre=True)
+    close(pre, z, error, dtype, "Z")
+    # the slopes are at most 1.13; the residual's addition is one more rounding
+    a = act_model(z, name)[0]
+    room = 1.13 * error + (act_error(z, dtype) if name not in ("none", "relu") else 0)
+    close(y, a + r.double(), room + (a.abs() + r.double().abs()) * 2.0 ** -23, dtype, "Y")
+
+
+@DTYPES
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("T, out, inp", [(1, 130, 272), (19, 70, 528), (150, 200, 336)])
+def test_gated_values(nv, T, out, inp, name, dtype):
+    w, v = Weights(1, out, inp, T), Weights(1, out, inp, T + 1)
+    x = rows((T, inp), dtype, 1, 0.3)
+    (g, gs), (u, us) = product(x, w, [T]), product(x, v, [T])
+    h, gg, uu = nv.gated(w.matrix(nv), v.matrix(nv), x.to(DEV), activation=act(nv, name), with_pre=True)
+    ge, ue = sum_error(gs, inp, dtype), sum_error(us, inp, dtype)
+    close(gg, g, ge, dtype, "G")
+    close(uu, u, ue, dtype, "U")
+    a = act_model(g, name)[0]
+    ae = 1.13 * ge + act_error(g, dtype)
+    close(h, a * u, ae * (u.abs() + ue) + a.abs() * ue + (a * u).abs() * 2.0 ** -23, dtype, "H")
+
+
+@DTYPES
+@pytest.mark.parametrize("name", ACTS[1:])
+@pytest.mark.parametrize("T, out, inp", [(1, 130, 272), (19, 72, 528), (150, 203, 336)])
+def test_gradient_values(nv, T, out, inp, name, dtype):
+    w, v = Weights(1, out, inp, T), Weights(1, out, inp, T + 1)
+    d, z, u = rows((T, out), dtype, 1), rows((T, out), dtype, 2, 2.0), rows((T, out), dtype, 3)
+    z[0, :6] = torch.tensor([0.0, 30.0, -30.0, 1e4, -1e4, -0.0]).to(dtype)       # flat ends
+    a, slope = act_model(z.double(), name)
+    error = act_error(z.double().clamp(-40, 40), dtype)
+    r = nv.linear_backward(w.matrix(nv), d.to(DEV), Z=z.to(DEV), activation=act(nv, name), with_bias=True)
+    dz = d.double() * slope
+    dze = d.double().abs() * (error + slope.abs() * 2.0 ** -23)
+    close(r["dZ"], dz, dze, dtype, "dZ")
+    used = r["dZ"].cpu()                      # the product takes dZ as it is held
+    dx, size = product(used, w, [T], False)
+    close(r["dX"], dx, sum_error(size, out, dtype), dtype, "dX")
+    close(r["dbias"], dz.sum(0, keepdim=True), dze.sum(0) + T * 2.0 ** -23 * dz.abs().sum(0), F32, "dbias")
+    r = nv.gated_backward(w.matrix(nv), v.matrix(nv), d.to(DEV), z.to(DEV), u.to(DEV), activation=act(nv, name))
+    du, dg = d.double() * a, d.double() * u.double() * slope
+    big = (z.double().abs() + 1) * 2.0 ** -22
+    close(r["dU"], du, d.double().abs() * (error + a.abs() * 2.0 ** -23 + big * (name != "relu")), dtype, "dU")
+    close(r["dG"], dg, (d.double() * u.double()).abs() * (error + slope.abs() * 2.0 ** -22), dtype, "dG")
+    (x1, s1), (x2, s2) = product(r["dG"].cpu(), w, [T], False), product(r["dU"].cpu(), v, [T], False)
+    close(r["dX"], x1 + x2, sum_error(s1 + s2, 2 * out, dtype), dtype, "dX of two")
+
+
+COUNTS = [[0, 0, 5], [3, 0, 1, 129, 0, 17, 64], [1] * 70, [0] * 130 + [40] + [0] * 20, [300, 1, 2], [16, 32, 48, 65],
+          [2, 0, 1] * 30 + [200]]
+
+
+@DTYPES
+@pytest.mark.parametrize("behind", (0, 7))
+@pytest.mark.parametrize("counts", COUNTS, ids=range(len(COUNTS)))
+def test_experts(nv, counts, behind, dtype):
+    """Rows of several matrices, some without any; rows behind the last are left as they were."""
+    E, T, out, inp = len(counts), sum(counts), 72, 144
+    w, v = Weights(E, out, inp, 1, whole=True), Weights(E, out, inp, 2, whole=True)
+    pad = lambda t: torch.cat([t, torch.full((behind, t.shape[1]), float("nan"), dtype=dtype)]).to(DEV)  # noqa: E731
+    x, b = rows((T, inp), dtype, 3, whole=True), rows((E, out), dtype, 4, whole=True)
+    d, g, u = (rows((T, out), dtype, s, whole=True) for s in (5, 6, 7))
+    seg, m, n = offsets(counts).to(DEV), w.matrix(nv), v.matrix(nv)
+
+    def fresh(cols):
+        return torch.full((T + behind, cols), 77.0, dtype=dtype, device=DEV)
+
+    def check(got, want, what):
+        same(got[:T], want, dtype, what)
+        assert bool((got[T:] == 77).all()), f"{what}: rows behind the last matrix's"
+
+    def space(n):
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+
+    n_rows = T + behind
+    Y, Z = fresh(out), fresh(out)
+    nv.nvfp4_linear(m, pad(x), n_rows, seg, b.to(DEV), nv.ACT_RELU, None, Z, Y,
+                    space(nv.nvfp4_linear_workspace_size(dtype, n_rows, E, out, inp)))
+    z = product(x, w, counts)[0] + by_row(b, counts)
+    check(Z, z, "Z")
+    check(Y, z.clamp(min=0), "Y")
+    H, G, U = fresh(out), fresh(out), fresh(out)
+    nv.nvfp4_gated(m, n, pad(x), n_rows, seg, nv.ACT_RELU, G, U, H,
+                   space(nv.nvfp4_gated_workspace_size(dtype, n_rows, E, out, inp)))
+    z_g, z_u = product(x, w, counts)[0], product(x, v, counts)[0]
+    check(G, z_g, "G")
+    check(U, z_u, "U")
+    h = z_g.clamp(min=0) * z_u
+    close(H[:T], h, h.abs() * 2.0 ** -24, dtype, "H")
+    assert bool((H[T:] == 77).all())
+    dX, dZ = fresh(inp), fresh(out)
+    dbias = torch.full((E, out), 77.0, device=DEV)
+    nv.nvfp4_linear_backward(m, pad(d), n_rows, seg, nv.ACT_RELU, pad(g), dZ, dbias, dX,
+                             space(nv.nvfp4_linear_backward_workspace_size(dtype, n_rows, E, out, inp, True)))
+    dz = d.double() * (g > 0)
+    check(dZ, dz, "dZ")
+    check(dX, product(dz, w, counts, False)[0], "dX")
+    sums = torch.stack([c.sum(0) for c in dz.split(counts)])
+    same(dbias, sums, F32, "dbias")
+    dX, dG, dU = fresh(inp), fresh(out), fresh(out)
+    nv.nvfp4_gated_backward(m, n, pad(d), n_rows, seg, nv.ACT_RELU, pad(g), pad(u), dG, dU, dX,
+                            space(nv.nvfp4_gated_backward_workspace_size(dtype, n_rows, E, out, inp)))
+    dg, du = d.double() * u.double() * (g > 0), d.double() * g.double().clamp(min=0)
+    check(dG, dg, "dG")
+    check(dU, du, "dU")
+    check(dX, product(dg, w, counts, False)[0] + product(du, v, counts, False)[0], "dX of two")
