@@ -51,12 +51,36 @@ struct Product {
     int64_t ldpre[2];
     void* y;
     int64_t ldy;
+    float* partial;          // [splits][tokens][columns, gated: twice], where there are splits
 };
 
-// Workgroups of a product (its grid), for the caller's check that they fit.
-int64_t product_blocks(int64_t tokens, int64_t batch, bool segments, int64_t out, int64_t in,
-                       int32_t matrices, bool backward);
+// Tiles of `size` rows that the matrices' rows make at most.
+inline int64_t product_row_tiles(int64_t tokens, int64_t batch, int64_t size) {
+    if (batch <= 1) return (tokens + size - 1) / size;
+    return tokens / size + (batch < tokens ? batch : tokens);
+}
+
+// Which kernel computes a product, and in how many shares of its reduction (more than one: their sums go to the
+// workspace, and a second kernel adds them). A function of the sizes alone, since the workspace's size is.
+enum class ProductKernel { kRows, kMid, kTiles };
+struct ProductPlan {
+    ProductKernel kernel;
+    int32_t tile_rows;       // rows of X a workgroup
+    int32_t splits;
+    int64_t blocks;          // workgroups
+};
+ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in, int32_t matrices,
+                         bool backward, bool f32);
+size_t product_partial_bytes(const ProductPlan& plan, int64_t tokens, int64_t out, int64_t in,
+                             int32_t matrices, bool backward);
+
+// p.partial: a workspace of product_partial_bytes.
 hipError_t launch_product(const Product& p, hipStream_t stream);
+
+// The kernels' launchers.
+void launch_product_rows(const Product& p, hipStream_t stream);
+void launch_product_mid(const Product& p, const ProductPlan& plan, hipStream_t stream);
+void launch_product_tiles(const Product& p, const ProductPlan& plan, hipStream_t stream);
 
 // bf16 parts of rows [tokens, cols] of dtype, padded with zeros to ld columns (a multiple of 8).
 hipError_t launch_product_parts(const void* X, bool f32, int64_t tokens, int64_t cols, int64_t ldx,

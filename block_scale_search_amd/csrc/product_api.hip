@@ -8,6 +8,7 @@
 namespace {
 
 constexpr int64_t kInt32 = (int64_t)1 << 31;
+constexpr int64_t kMaxSide = (int64_t)1 << 24;
 constexpr int64_t kMaxSpan = (int64_t)1 << 56;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -24,7 +25,7 @@ int elem_size(int dtype) {
 
 bool sizes_ok(int64_t tokens, int64_t batch, int64_t out, int64_t in) {
     return tokens >= 0 && tokens < kInt32 && batch >= 0 && batch <= 65535 && out >= 1 && in >= 16 &&
-           in % 16 == 0 && in < kInt32 && out < kInt32 && out * (in / 16) < kInt32;
+           in % 16 == 0 && in < kMaxSide && out < kMaxSide && out * (in / 16) < kInt32;
 }
 
 nvfp4_status check_matrix(const nvfp4_matrix* m) {
@@ -53,7 +54,8 @@ nvfp4_status check_call(int dtype, const nvfp4_matrix* w, const nvfp4_matrix* w2
     if (!sizes_ok(tokens, w->batch, w->out, w->in)) return NVFP4_ERR_SHAPE;
     // one thread per 8 values in the element-wise kernels, and the product's grid
     if (tokens * ((w->out > w->in ? w->out : w->in) / 8 + 1) >= (int64_t)1 << 38 ||
-        nvfp4::product_blocks(tokens, w->batch, seg != nullptr, w->out, w->in, two ? 2 : 1, backward) >= kInt32)
+        nvfp4::product_plan(tokens, w->batch, w->out, w->in, two ? 2 : 1, backward,
+                            dtype == NVFP4_DTYPE_F32).blocks >= kInt32)
         return NVFP4_ERR_SHAPE;
     if (seg == nullptr && w->batch != 1) return NVFP4_ERR_NULL;
     if (!aligned(seg, 8)) return NVFP4_ERR_ALIGN;
@@ -74,21 +76,30 @@ nvfp4::ProductMatrix view_of(const nvfp4_matrix* m) {
     return nvfp4::ProductMatrix{m->packed, m->scales, m->S, m->batch > 1 ? m->stride : 0};
 }
 
-// Workspace: the operands' parts, where the rows given are not bf16 rows of whole 16-byte pieces, then a bias
-// gradient's sums.
+// Workspace: the operands' parts, where the rows given are not bf16 rows of whole 16-byte pieces, the sums of the
+// shares of a product's reduction, and those of a bias gradient.
 struct Space {
     bool parts;
     int planes;
     int64_t ld, plane;       // elements
     size_t operand;          // bytes of one operand
+    size_t partial, bias;
+    size_t total;
 };
-Space space_of(int dtype, int64_t tokens, int64_t cols) {
+Space space_of(int dtype, int64_t tokens, int64_t batch, int64_t out, int64_t in, int32_t matrices, bool backward,
+               bool with_bias) {
     Space s;
-    s.planes = dtype == NVFP4_DTYPE_F32 ? 3 : 1;
-    s.parts = s.planes == 3 || cols % 8 != 0;
+    const int64_t cols = backward ? out : in;
+    const bool f32 = dtype == NVFP4_DTYPE_F32;
+    s.planes = f32 ? 3 : 1;
+    s.parts = f32 || cols % 8 != 0;
     s.ld = up(cols, 8);
     s.plane = tokens * s.ld;
     s.operand = s.parts ? (size_t)up(s.planes * s.plane * 2, 256) : 0;
+    const nvfp4::ProductPlan plan = nvfp4::product_plan(tokens, batch, out, in, matrices, backward, f32);
+    s.partial = (size_t)up((int64_t)nvfp4::product_partial_bytes(plan, tokens, out, in, matrices, backward), 256);
+    s.bias = with_bias ? nvfp4::product_bias_workspace_bytes(tokens, batch, out) : 0;
+    s.total = s.operand * (backward ? matrices : 1) + s.partial + s.bias;
     return s;
 }
 
@@ -103,6 +114,7 @@ hipError_t forward_operand(nvfp4::Product& p, const Space& s, const void* X, int
     p.planes = s.planes;
     p.plane = s.plane;
     p.a[0] = nvfp4::ProductOperand{static_cast<const uint16_t*>(X), ldx};
+    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.operand);
     if (!s.parts) return hipSuccess;
     uint16_t* parts = static_cast<uint16_t*>(workspace);
     p.a[0] = nvfp4::ProductOperand{parts, s.ld};
@@ -130,6 +142,7 @@ nvfp4_status backward(nvfp4::Product& p, nvfp4::ProductSlopes& g, const Space& s
     p.planes = s.planes;
     p.plane = s.plane;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.partial = reinterpret_cast<float*>(ws + p.matrices * s.operand);
     for (int m = 0; m < p.matrices; ++m) {
         if (s.parts) {
             g.parts[m] = reinterpret_cast<uint16_t*>(ws + m * s.operand);
@@ -155,7 +168,7 @@ extern "C" {
 
 size_t nvfp4_linear_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out, int64_t in) {
     if (elem_size(dtype) == 0 || !sizes_ok(tokens, batch, out, in)) return 0;
-    return space_of(dtype, tokens, in).operand;
+    return space_of(dtype, tokens, batch, out, in, 1, false, false).total;
 }
 
 nvfp4_status nvfp4_linear(const nvfp4_matrix* W, const void* X, int dtype, int64_t tokens, int64_t ldx,
@@ -172,8 +185,8 @@ nvfp4_status nvfp4_linear(const nvfp4_matrix* W, const void* X, int dtype, int64
     if (st == NVFP4_OK) st = check_rows(Y, esz, tokens, W->out, ldy, esz);
     if (st != NVFP4_OK) return st;
     if (!aligned(bias, esz)) return NVFP4_ERR_ALIGN;
-    const Space s = space_of(dtype, tokens, W->in);
-    st = check_workspace(s.operand, workspace, workspace_bytes);
+    const Space s = space_of(dtype, tokens, W->batch, W->out, W->in, 1, false, false);
+    st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::Product p = product_of(W, nullptr, false, dtype, tokens, seg_offsets, activation);
     p.bias = bias;
@@ -189,7 +202,8 @@ nvfp4_status nvfp4_linear(const nvfp4_matrix* W, const void* X, int dtype, int64
 }
 
 size_t nvfp4_gated_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out, int64_t in) {
-    return nvfp4_linear_workspace_size(dtype, tokens, batch, out, in);
+    if (elem_size(dtype) == 0 || !sizes_ok(tokens, batch, out, in)) return 0;
+    return space_of(dtype, tokens, batch, out, in, 2, false, false).total;
 }
 
 nvfp4_status nvfp4_gated(const nvfp4_matrix* W_gate, const nvfp4_matrix* W_up, const void* X, int dtype,
@@ -207,8 +221,8 @@ nvfp4_status nvfp4_gated(const nvfp4_matrix* W_gate, const nvfp4_matrix* W_up, c
     if (st == NVFP4_OK && U) st = check_rows(U, esz, tokens, out, ldu, esz);
     if (st == NVFP4_OK) st = check_rows(H, esz, tokens, out, ldh, esz);
     if (st != NVFP4_OK) return st;
-    const Space s = space_of(dtype, tokens, W_gate->in);
-    st = check_workspace(s.operand, workspace, workspace_bytes);
+    const Space s = space_of(dtype, tokens, W_gate->batch, out, W_gate->in, 2, false, false);
+    st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::Product p = product_of(W_gate, W_up, false, dtype, tokens, seg_offsets, activation);
     p.pre[0] = G;
@@ -225,8 +239,7 @@ nvfp4_status nvfp4_gated(const nvfp4_matrix* W_gate, const nvfp4_matrix* W_up, c
 size_t nvfp4_linear_backward_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out,
                                             int64_t in, int with_bias) {
     if (elem_size(dtype) == 0 || !sizes_ok(tokens, batch, out, in)) return 0;
-    return space_of(dtype, tokens, out).operand +
-           (with_bias ? nvfp4::product_bias_workspace_bytes(tokens, batch, out) : 0);
+    return space_of(dtype, tokens, batch, out, in, 1, true, with_bias != 0).total;
 }
 
 nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dtype, int64_t tokens,
@@ -239,7 +252,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
     if (W->batch == 0) return NVFP4_OK;
     const int esz = elem_size(dtype);
     const bool act = activation != NVFP4_ACT_NONE;
-    const Space s = space_of(dtype, tokens, W->out);
+    const Space s = space_of(dtype, tokens, W->batch, W->out, W->in, 1, true, dbias != nullptr);
     if (tokens > 0) {
         // the product reads dY, or dZ, as they are where no parts are made
         st = check_rows(dY, esz, tokens, W->out, lddy, !act && !s.parts ? 16 : esz);
@@ -249,8 +262,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
         if (st != NVFP4_OK) return st;
     }
     if (!aligned(dbias, 4)) return NVFP4_ERR_ALIGN;
-    const size_t need = nvfp4_linear_backward_workspace_size(dtype, tokens, W->batch, W->out, W->in, dbias != nullptr);
-    st = check_workspace(need, workspace, workspace_bytes);
+    st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::ProductSlopes g = {};
     g.rows = nvfp4::ProductRows{seg_offsets, tokens, (int32_t)W->batch};
@@ -266,7 +278,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
     const hipStream_t on = static_cast<hipStream_t>(stream);
     if (dbias) {
         const hipError_t e =
-            nvfp4::launch_product_bias(g, dbias, static_cast<uint8_t*>(workspace) + s.operand, on);
+            nvfp4::launch_product_bias(g, dbias, static_cast<uint8_t*>(workspace) + s.operand + s.partial, on);
         if (e != hipSuccess) return NVFP4_ERR_HIP;
     }
     if (tokens == 0) return NVFP4_OK;
@@ -279,7 +291,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
 size_t nvfp4_gated_backward_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out,
                                            int64_t in) {
     if (elem_size(dtype) == 0 || !sizes_ok(tokens, batch, out, in)) return 0;
-    return 2 * space_of(dtype, tokens, out).operand;
+    return space_of(dtype, tokens, batch, out, in, 2, true, false).total;
 }
 
 nvfp4_status nvfp4_gated_backward(const nvfp4_matrix* W_gate, const nvfp4_matrix* W_up, const void* dH,
@@ -292,7 +304,7 @@ nvfp4_status nvfp4_gated_backward(const nvfp4_matrix* W_gate, const nvfp4_matrix
     if (tokens == 0 || W_gate->batch == 0) return NVFP4_OK;
     const int esz = elem_size(dtype);
     const int64_t out = W_gate->out;
-    const Space s = space_of(dtype, tokens, out);
+    const Space s = space_of(dtype, tokens, W_gate->batch, out, W_gate->in, 2, true, false);
     const int64_t to = s.parts ? esz : 16;               // the product reads dG and dU where no parts are made
     st = check_rows(dH, esz, tokens, out, lddh, esz);
     if (st == NVFP4_OK) st = check_rows(G, esz, tokens, out, ldg, esz);
@@ -301,7 +313,7 @@ nvfp4_status nvfp4_gated_backward(const nvfp4_matrix* W_gate, const nvfp4_matrix
     if (st == NVFP4_OK) st = check_rows(dU, esz, tokens, out, lddu, to);
     if (st == NVFP4_OK) st = check_rows(dX, esz, tokens, W_gate->in, lddx, esz);
     if (st != NVFP4_OK) return st;
-    st = check_workspace(2 * s.operand, workspace, workspace_bytes);
+    st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::ProductSlopes g = {};
     g.rows = nvfp4::ProductRows{seg_offsets, tokens, (int32_t)W_gate->batch};

@@ -120,6 +120,46 @@ __device__ __forceinline__ void store_value(void* p, int64_t i, float x, bool f3
     else static_cast<uint16_t*>(p)[i] = bf16_bits(x);
 }
 
+// The value that a product's columns make: z of a linear layer, g and u of a gated pair.
+__device__ __forceinline__ void product_linear(const Product& p, int64_t t, int64_t n, float z, bool f32) {
+    if (p.pre[0]) store_value(p.pre[0], t * p.ldpre[0] + n, z, f32);
+    float y = f32 ? act_value<true>(p.act, z) : act_value<false>(p.act, z);
+    if (p.residual) y += load_value(p.residual, t * p.ldr + n, f32);
+    store_value(p.y, t * p.ldy + n, y, f32);
+}
+__device__ __forceinline__ void product_gated(const Product& p, int64_t t, int64_t n, float g, float u, bool f32) {
+    if (p.pre[0]) {
+        store_value(p.pre[0], t * p.ldpre[0] + n, g, f32);
+        store_value(p.pre[1], t * p.ldpre[1] + n, u, f32);
+    }
+    store_value(p.y, t * p.ldy + n, (f32 ? act_value<true>(p.act, g) : act_value<false>(p.act, g)) * u, f32);
+}
+
+// Where share `split` of a product's reduction leaves its sum (times S) of row t and column n of `cols`.
+__device__ __forceinline__ float& product_partial(const Product& p, int split, int64_t t, int64_t n, int64_t cols) {
+    return p.partial[((int64_t)split * p.rows.tokens + t) * cols + n];
+}
+
+typedef __attribute__((address_space(1))) const void* GlobalPtr;
+typedef __attribute__((address_space(3))) void* LdsPtr;
+
+// 16 (4) bytes a lane from global memory to lds + 16 (4) * lane (lds uniform).
+__device__ __forceinline__ void copy16(const void* src, void* lds) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void copy4(const void* src, void* lds) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)lds, 4, 0, 0);
+}
+
+// Waits until at most N of the wave's loads and copies are under way, and for its LDS accesses.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    static_assert(N < 64, "vmcnt has six bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);
+}
+// The bare barrier: the waits that it needs are explicit (__syncthreads would wait for every copy under way).
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
 // Rows of matrix e, inside the tokens whatever the offsets hold.
 __device__ __forceinline__ void segment(const ProductRows& r, int e, int64_t& lo, int64_t& hi) {
     lo = min(max(r.seg[e], (int64_t)0), r.tokens);

@@ -1,0 +1,131 @@
+// Products with NVFP4 matrices for gfx950: which kernel computes one, in how many shares of the reduction, and the
+// kernel that adds the shares.
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+#include "product_device.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// One thread per output column of a row: the shares' sums (each times S already) in order, then what the
+// product's own kernel does with whole sums.
+template <bool GATED, bool F32>
+__global__ __launch_bounds__(kThreads) void k_product_join(Product p, int splits, int64_t N, int64_t total) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= total) return;
+    const int64_t t = i / N, n = i - t * N;
+    if (t >= rows_end(p.rows)) return;
+    const auto sum = [&](int64_t c) {
+        float s = 0.0f;
+        for (int k = 0; k < splits; ++k) s += product_partial(p, k, t, c, GATED ? 2 * N : N);
+        return s;
+    };
+    if constexpr (GATED) {
+        product_gated(p, t, n, sum(n), sum(N + n), F32);
+    } else {
+        float v = sum(n);
+        if (p.backward) {
+            store_value(p.y, t * p.ldy + n, v, F32);
+            return;
+        }
+        if (p.bias) {
+            int e = 0;
+            if (p.rows.seg) {                            // the last matrix whose rows start at or before t
+                int hi = p.rows.batch;
+                while (hi - e > 1) {
+                    const int mid = (e + hi) >> 1;
+                    if (p.rows.seg[mid] <= t) e = mid;
+                    else hi = mid;
+                }
+            }
+            v += load_value(p.bias, e * N + n, F32);
+        }
+        product_linear(p, t, n, v, F32);
+    }
+}
+
+}  // namespace
+
+ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in, int32_t matrices,
+                         bool backward, bool f32) {
+    ProductPlan plan;
+    const int64_t N = backward ? in : out, K = backward ? out : in;
+    const int64_t each = batch > 0 ? (tokens + batch - 1) / batch : 0;
+    int64_t steps, tiles;
+    // rows of a matrix (on average): up to 4 of them pass through the kernel that keeps them in registers (8192 x 28672:
+    // 39.2 us at 4 rows, 48.3 at 8; by tiles of 32 rows 46.1 and 45.7), up to 128 through tiles whose weights are
+    // converted where they are used (64 rows 60 us, 128 rows 101 us; by tiles through LDS 103 and 112)
+    if (!backward && each <= 4) {
+        plan.kernel = ProductKernel::kRows;
+        plan.tile_rows = 4;
+        plan.splits = 1;
+        plan.blocks = product_row_tiles(tokens, batch, 4) * ((out * matrices + 15) / 16);
+        return plan;
+    }
+    if (!backward && !f32 && in % 64 == 0 && each <= 128) {
+        plan.kernel = ProductKernel::kMid;
+        plan.tile_rows = each <= 32 ? 32 : each <= 64 ? 64 : 128;
+        steps = (K + 127) / 128;
+        tiles = product_row_tiles(tokens, batch, plan.tile_rows) * ((N * matrices + 127) / 128);
+    } else {
+        plan.kernel = ProductKernel::kTiles;
+        plan.tile_rows = 128;
+        steps = (K + 63) / 64 * (f32 ? 3 : 1) * (backward ? matrices : 1);
+        tiles = product_row_tiles(tokens, batch, 128) * ((N * (backward ? 1 : matrices) + 127) / 128);
+    }
+    // shares: about two workgroups a compute unit, of at least 4 steps each (64 rows by 8192 x 28672 in 8 shares 59.7 us,
+    // in 4 69.2, in 12 64.0)
+    int64_t splits = tiles > 0 ? 512 / tiles : 1;
+    if (splits > steps / 4) splits = steps / 4;
+    if (splits > 32) splits = 32;
+    if (splits < 1) splits = 1;
+    splits = (steps + (steps + splits - 1) / splits - 1) / ((steps + splits - 1) / splits);     // none empty
+    plan.splits = (int32_t)splits;
+    plan.blocks = tiles * splits;
+    return plan;
+}
+
+size_t product_partial_bytes(const ProductPlan& plan, int64_t tokens, int64_t out, int64_t in,
+                             int32_t matrices, bool backward) {
+    if (plan.splits <= 1) return 0;
+    return (size_t)(plan.splits * tokens * (backward ? in : out * matrices)) * 4;
+}
+
+hipError_t launch_product(const Product& p, hipStream_t stream) {
+    ProductPlan plan = product_plan(p.rows.tokens, p.rows.batch, p.out, p.in, p.matrices, p.backward, p.f32);
+    // the tile kernel asks for less: alignment beyond what codes and scale bytes need have, and rows close enough
+    // together for 32-bit offsets
+    const auto at = [](const void* q, uintptr_t to) { return (reinterpret_cast<uintptr_t>(q) & (to - 1)) == 0; };
+    bool fits = plan.kernel != ProductKernel::kRows || p.a[0].ld < (int64_t)1 << 24;
+    for (int m = 0; plan.kernel == ProductKernel::kMid && m < p.matrices; ++m)
+        fits = fits && at(p.w[m].packed, 16) && at(p.w[m].scales, 4) && p.w[m].stride % 64 == 0;
+    if (!fits) plan = ProductPlan{ProductKernel::kTiles, 128, 1, 0};
+    if (plan.kernel == ProductKernel::kRows) {
+        launch_product_rows(p, stream);
+        return hipGetLastError();
+    }
+    if (plan.kernel == ProductKernel::kMid) {
+        launch_product_mid(p, plan, stream);
+    } else {
+        launch_product_tiles(p, plan, stream);
+    }
+    if (plan.splits > 1) {
+        const int64_t N = p.backward ? p.in : p.out, total = p.rows.tokens * N;
+        const dim3 grid((uint32_t)((total + kThreads - 1) / kThreads));
+        const bool gated = !p.backward && p.matrices == 2;
+        if (gated && p.f32)
+            hipLaunchKernelGGL((k_product_join<true, true>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+        else if (gated)
+            hipLaunchKernelGGL((k_product_join<true, false>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+        else if (p.f32)
+            hipLaunchKernelGGL((k_product_join<false, true>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+        else
+            hipLaunchKernelGGL((k_product_join<false, false>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,205 @@
+// Products of few rows with NVFP4 matrices for gfx950, forward and gated: a token's or a small batch's pass,
+// bound by reading the codes.
+//
+// A wave owns a slice of the reduction, 1024 columns, and keeps the rows' values of that slice in registers, as operands
+// of MFMA 16x16x32; the codes stream past. The 16 lanes that give the MFMA 16 rows of its left operand
+// hold 4 rows of the matrix by 4 pieces of the slice, the right operand's 16 columns 4 rows of X by the same 4
+// pieces: of the 16 x 16 sums the quarter where the pieces are the same is wanted. What that wastes of the matrix units
+// is idle here anyway, and it lets four neighbouring lanes read neighbouring bytes of a row (16 rows side by
+// side, a lane each, took 1.5 to 2 times as long: the loads' addresses were the bound). A lane converts 64
+// codes of 4 groups a step (level * E4M3 is exact in bf16). The slices' sums meet in LDS, in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+#include "product_device.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kSlice = 1024;
+constexpr int kRows = 4;             // rows of X of a workgroup
+template <bool F32>
+constexpr int kWaves = F32 ? 8 : 16; // at most (registers)
+constexpr int kDepth = 4;            // groups of 4 matrix rows in flight
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                   c, 0, 0, 0);
+}
+
+// Loads through a buffer descriptor over everything from p: an offset of kNowhere reads zeros.
+constexpr uint32_t kReach = 0x80000000u, kNowhere = 0xC0000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, kReach, 0x00027000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+}
+__device__ __forceinline__ u32x2 load8(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+}
+__device__ __forceinline__ uint32_t load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+}
+__device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, at, 0, 0);
+}
+
+// Sum over four neighbouring lanes, in each of them.
+__device__ __forceinline__ float sum_quad(float v) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
+}
+
+// A lane's 64 codes of a group of 4 matrix rows, and their scale bytes.
+struct Codes {
+    u32x4 code[2];
+    uint32_t scale;
+};
+
+// Up to kRows rows of X, `block` rows of each matrix (a multiple of 16). WHOLE: in is a multiple of 64, so a lane's 64
+// columns are all inside the matrix or all outside.
+template <bool GATED, bool F32, bool WHOLE>
+__global__ __launch_bounds__(64 * kWaves<F32>) void k_product_rows(Product p, int nn, int block) {
+    constexpr int P = F32 ? 3 : 1;                       // parts of a value
+    extern __shared__ float sums[];                      // [wave][group][64]
+    const int lane = threadIdx.x & 63, seg = lane & 3, n4 = lane >> 2 & 3, kg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int tile = (int)(blockIdx.x / (uint32_t)nn), tn = (int)(blockIdx.x - (uint32_t)tile * (uint32_t)nn);
+    RowTile rows;
+    if (!find_rows(p.rows, tile, kRows, rows)) return;
+    const int n0 = tn * block, N = (int)p.out, K = (int)p.in;
+    const int slices = (K + kSlice - 1) / kSlice;
+    const int half = block / 4, groups = GATED ? 2 * half : half;
+
+    __amdgpu_buffer_rsrc_t codes[GATED ? 2 : 1], scales[GATED ? 2 : 1];
+#pragma unroll
+    for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+        const int64_t at = rows.e * p.w[m].stride + (int64_t)n0 * K;
+        codes[m] = window(p.w[m].packed + at / 2);
+        scales[m] = window(p.w[m].scales + at / 16);
+    }
+
+    for (int slice = wave; slice < slices; slice += waves) {
+        const int k = slice * kSlice + kg * 256 + seg * 64;          // the lane's 64 columns
+        // its values of row n4
+        u32x4 x[P][8];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const __amdgpu_buffer_rsrc_t from = window(p.a[0].p + i * p.plane + rows.first * p.a[0].ld);
+            const uint32_t at = (uint32_t)(n4 * p.a[0].ld + k) * 2;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) x[i][s] = load16(from, n4 < rows.rows && k + 8 * s < K ? at + 16 * s : kNowhere);
+        }
+        const uint32_t first = (uint32_t)n4 * (uint32_t)(K / 16) + (uint32_t)(k / 16);   // in groups of 16 weights
+        const auto load = [&](Codes& b, int g) {
+            const int j = GATED && g >= half ? g - half : g;
+            const bool second = GATED && g >= half;
+            const uint32_t at = first + (uint32_t)j * 4u * (uint32_t)(K / 16);
+            const bool live = n0 + 4 * j + n4 < N && g < groups;
+            const __amdgpu_buffer_rsrc_t c = GATED && second ? codes[GATED ? 1 : 0] : codes[0];
+            const __amdgpu_buffer_rsrc_t e = GATED && second ? scales[GATED ? 1 : 0] : scales[0];
+            if constexpr (WHOLE) {
+                const bool in = live && k < K;
+                b.code[0] = load16(c, in ? at * 8 : kNowhere);
+                b.code[1] = load16(c, in ? at * 8 + 16 : kNowhere);
+                b.scale = load4(e, in ? at : kNowhere);
+            } else {
+                u32x2 w[4];
+                b.scale = 0;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const bool in = live && k + 16 * s < K;
+                    w[s] = load8(c, in ? at * 8 + 8 * s : kNowhere);
+                    b.scale |= load1(e, in ? at + s : kNowhere) << (8 * s);
+                }
+                b.code[0] = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
+                b.code[1] = u32x4{w[2][0], w[2][1], w[3][0], w[3][1]};
+            }
+        };
+        Codes buf[kDepth];
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            load(buf[d], d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int g0 = 0; g0 < groups; g0 += kDepth) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                Codes& b = buf[d];
+                f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+                const float e[4] = {scale_value<0>(b.scale), scale_value<1>(b.scale), scale_value<2>(b.scale),
+                                    scale_value<3>(b.scale)};
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const u32x4 w = dequant8(b.code[s >> 2][s & 3], e[s >> 1]);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) acc[s & 1] = mfma(w, x[i][s], acc[s & 1]);
+                }
+                load(b, g0 + d + kDepth);
+                // register r of a lane holds piece r of matrix row kg; the lane's own piece is seg
+                const f32x4 a = acc[0] + acc[1];
+                const float v = sum_quad(seg < 2 ? (seg == 0 ? a[0] : a[1]) : (seg == 2 ? a[2] : a[3]));
+                float* to = sums + (wave * groups + g0 + d) * 64 + lane;
+                *to = slice == wave ? v : *to + v;
+                __builtin_amdgcn_sched_barrier(0);       // else all loads are issued together, and waited for together
+            }
+        }
+    }
+    __syncthreads();
+
+    const int used = min(waves, slices);
+    const float S0 = p.w[0].S[rows.e], S1 = GATED ? p.w[1].S[rows.e] : 0.0f;
+    const auto total = [&](int g, int at) {
+        float s = 0.0f;
+        for (int w = 0; w < used; ++w) s += sums[(w * groups + g) * 64 + at];
+        return s;
+    };
+    for (int o = threadIdx.x; o < block * rows.rows; o += blockDim.x) {
+        const int row = o / block, c = o - row * block;
+        const int64_t n = n0 + c, t = rows.first + row;
+        if (n >= N) continue;
+        const int g = c >> 2, at = (c & 3) * 16 + row * 4;
+        if constexpr (GATED) {
+            const float gate = total(g, at) * S0, up = total(g + half, at) * S1;
+            product_gated(p, t, n, gate, up, F32);
+        } else {
+            const float bias = p.bias ? load_value(p.bias, rows.e * (int64_t)N + n, F32) : 0.0f;
+            product_linear(p, t, n, __builtin_fmaf(total(g, at), S0, bias), F32);
+        }
+    }
+}
+
+template <bool GATED, bool F32>
+void launch(const Product& p, hipStream_t stream) {
+    const int64_t slices = (p.in + kSlice - 1) / kSlice;
+    const int waves = (int)(slices < kWaves<F32> ? slices : kWaves<F32>);
+    // 32 matrix rows a workgroup where that makes enough of them, else 16 (one row, 8192 x 28672: 30.1 us, with 16
+    // rows 35.5; 4096 x 14336 11.6, with 32 rows 15.9)
+    const int64_t tiles = product_row_tiles(p.rows.tokens, p.rows.batch, kRows);
+    const bool wide = tiles * ((p.out * p.matrices + 31) / 32) >= 256;
+    const int block = wide && !GATED ? 32 : 16;
+    const int64_t nn = (p.out + block - 1) / block;
+    const dim3 grid((uint32_t)(tiles * nn)), threads(64 * waves);
+    const size_t lds = (size_t)waves * (GATED ? 2 : 1) * block * 64;
+    if (p.in % 64 == 0)
+        hipLaunchKernelGGL((k_product_rows<GATED, F32, true>), grid, threads, lds, stream, p, (int)nn, block);
+    else
+        hipLaunchKernelGGL((k_product_rows<GATED, F32, false>), grid, threads, lds, stream, p, (int)nn, block);
+}
+
+}  // namespace
+
+void launch_product_rows(const Product& p, hipStream_t stream) {
+    if (p.matrices == 2) {
+        if (p.f32) launch<true, true>(p, stream);
+        else launch<true, false>(p, stream);
+    } else {
+        if (p.f32) launch<false, true>(p, stream);
+        else launch<false, false>(p, stream);
+    }
+}
+
+}  // namespace nvfp4

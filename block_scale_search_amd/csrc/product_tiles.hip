@@ -28,14 +28,6 @@ struct Shape {
     static_assert(BN * BK / kThreads == 32, "a thread converts 32 weights a step");
 };
 
-typedef __attribute__((address_space(1))) const void* GlobalPtr;
-typedef __attribute__((address_space(3))) void* LdsPtr;
-
-// 16 bytes a lane from global memory to lds + 16 * lane (lds uniform).
-__device__ __forceinline__ void copy16(const uint16_t* src, uint16_t* lds) {
-    __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)lds, 16, 0, 0);
-}
-
 // Piece c (8 values) of LDS row r sits at c ^ swizzle(r).
 __device__ __forceinline__ int swizzle(int r) { return (r ^ (r >> 3)) & 7; }
 
@@ -49,6 +41,11 @@ struct Raw {
 // Where in the reduction a step lies: step `kt` of plane `plane` of matrix `m`.
 struct Cursor {
     int kt = 0, plane = 0, m = 0;
+    __device__ __forceinline__ void at(int step, int nk, int planes) {
+        kt = step % nk;
+        plane = step / nk % planes;
+        m = step / nk / planes;
+    }
     __device__ __forceinline__ void next(int nk, int planes) {
         if (++kt == nk) {
             kt = 0;
@@ -61,7 +58,7 @@ struct Cursor {
 };
 
 template <int M_, int N_, int WM_, int WN_, int MODE, bool F32>
-__global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int nn) {
+__global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int nn, int splits, int each) {
     typedef Shape<M_, N_, WM_, WN_> S;
     constexpr int BM = S::BM, BN = S::BN, TM = S::TM, TN = S::TN;
     __shared__ __align__(1024) uint16_t lds_a[2][BM][BK];
@@ -69,7 +66,9 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
-    const int tile = (int)(blockIdx.x / (uint32_t)nn), tn = (int)(blockIdx.x - (uint32_t)tile * (uint32_t)nn);
+    const uint32_t of = blockIdx.x / (uint32_t)splits;
+    const int split = (int)(blockIdx.x - of * (uint32_t)splits);
+    const int tile = (int)(of / (uint32_t)nn), tn = (int)(of - (uint32_t)tile * (uint32_t)nn);
     RowTile rows;
     if (!find_rows(p.rows, tile, BM, rows)) return;
 
@@ -80,7 +79,7 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     const int64_t k_pad = (K + 7) / 8 * 8;
     const int nk = (int)((K + BK - 1) / BK);
     const int matrices = MODE == kBackward ? p.matrices : 1;
-    const int steps = nk * p.planes * matrices;
+    const int begin = split * each, steps = min(each, nk * p.planes * matrices - begin);
 
     const auto load_a = [&](int buf, const Cursor& c) {
         const ProductOperand& a = p.a[MODE == kBackward ? c.m : 0];
@@ -173,7 +172,9 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
 
     const int r32 = lane & 31, kg = lane >> 5;
     Cursor ca, cb;
-    int to_switch = MODE == kBackward && matrices == 2 ? nk * p.planes : -1;
+    cb.at(begin, nk, p.planes);
+    ca = cb;
+    const int to_switch = nk * p.planes - begin;         // the step at which the second matrix begins
     Raw raw;
     load_b(raw, cb);
     load_a(0, ca);
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         ca.next(nk, p.planes);
         if (s + 2 < steps) load_b(raw, cb);
         if constexpr (MODE == kBackward) {
-            if (s == to_switch) {                        // the second matrix's sums carry its S
+            if (s == to_switch && s > 0) {                      // the second matrix's sums carry its S
                 const float f = p.w[0].S[rows.e] / p.w[1].S[rows.e];
 #pragma unroll
                 for (int a = 0; a < TM; ++a)
@@ -224,8 +225,10 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         __syncthreads();
     }
 
-    // a lane holds rows 8 (e / 4) + 4 kg + e % 4 of column r32 of each 32 x 32 tile
-    const float S0 = p.w[MODE == kBackward ? matrices - 1 : 0].S[rows.e];
+    // a lane holds rows 8 (e / 4) + 4 kg + e % 4 of column r32 of each 32 x 32 tile; backward, the sums are over the
+    // S of the last matrix met
+    const int at = MODE == kBackward && to_switch < steps ? 1 : 0;
+    const float S0 = p.w[at].S[rows.e];
     const float S1 = MODE == kGated ? p.w[1].S[rows.e] : 0.0f;
 #pragma unroll
     for (int a = 0; a < TM; ++a)
@@ -239,21 +242,21 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
                 const int row = (wm * TM + a) * 32 + (e >> 2) * 8 + kg * 4 + (e & 3);
                 if (row >= rows.rows) continue;
                 const int64_t t = rows.first + row;
-                if constexpr (MODE == kBackward) {
-                    store_value(p.y, t * p.ldy + n, acc[a][b][e] * S0, F32);
-                } else if constexpr (MODE == kGated) {
-                    const float g = acc[a][b][e] * S0, u = acc[a][b + 1][e] * S1;
-                    if (p.pre[0]) {
-                        store_value(p.pre[0], t * p.ldpre[0] + n, g, F32);
-                        store_value(p.pre[1], t * p.ldpre[1] + n, u, F32);
+                const float v = acc[a][b][e] * S0;
+                if constexpr (MODE == kGated) {
+                    const float u = acc[a][b + 1][e] * S1;
+                    if (splits > 1) {
+                        product_partial(p, split, t, n, 2 * N) = v;
+                        product_partial(p, split, t, N + n, 2 * N) = u;
+                    } else {
+                        product_gated(p, t, n, v, u, F32);
                     }
-                    store_value(p.y, t * p.ldy + n, act_value<F32>(p.act, g) * u, F32);
+                } else if (splits > 1) {
+                    product_partial(p, split, t, n, N) = v;
+                } else if constexpr (MODE == kBackward) {
+                    store_value(p.y, t * p.ldy + n, v, F32);
                 } else {
-                    const float z = __builtin_fmaf(acc[a][b][e], S0, bias);
-                    if (p.pre[0]) store_value(p.pre[0], t * p.ldpre[0] + n, z, F32);
-                    float y = act_value<F32>(p.act, z);
-                    if (p.residual) y += load_value(p.residual, t * p.ldr + n, F32);
-                    store_value(p.y, t * p.ldy + n, y, F32);
+                    product_linear(p, t, n, v + bias, F32);
                 }
             }
         }
@@ -261,35 +264,27 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
 
 typedef Shape<128, 128, 2, 2> Small;
 
-int64_t row_tiles(int64_t tokens, int64_t batch, bool segments, int64_t size) {
-    if (!segments) return (tokens + size - 1) / size;
-    return tokens / size + (batch < tokens ? batch : tokens);
-}
-
 template <typename S, int MODE>
-void launch(const Product& p, hipStream_t stream) {
-    const int64_t N = MODE == kBackward ? p.in : p.out, cols = MODE == kGated ? S::BN / 2 : S::BN;
-    const int64_t nn = (N + cols - 1) / cols;
-    const dim3 grid((uint32_t)(row_tiles(p.rows.tokens, p.rows.batch, p.rows.seg != nullptr, S::BM) * nn));
+void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
+    const int64_t N = MODE == kBackward ? p.in : p.out, K = MODE == kBackward ? p.out : p.in;
+    const int64_t cols = MODE == kGated ? S::BN / 2 : S::BN, nn = (N + cols - 1) / cols;
+    const int64_t steps = (K + BK - 1) / BK * p.planes * (MODE == kBackward ? p.matrices : 1);
+    const int64_t each = (steps + plan.splits - 1) / plan.splits;
+    const dim3 grid((uint32_t)(product_row_tiles(p.rows.tokens, p.rows.batch, S::BM) * nn * plan.splits));
     if (p.f32)
-        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, true>), grid, dim3(S::kThreads), 0, stream, p, (int)nn);
+        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, true>), grid, dim3(S::kThreads), 0,
+                           stream, p, (int)nn, plan.splits, (int)each);
     else
-        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, false>), grid, dim3(S::kThreads), 0, stream, p, (int)nn);
+        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, false>), grid, dim3(S::kThreads), 0,
+                           stream, p, (int)nn, plan.splits, (int)each);
 }
 
 }  // namespace
 
-int64_t product_blocks(int64_t tokens, int64_t batch, bool segments, int64_t out, int64_t in,
-                       int32_t matrices, bool backward) {
-    const int64_t N = backward ? in : out, cols = !backward && matrices == 2 ? Small::BN / 2 : Small::BN;
-    return row_tiles(tokens, batch, segments, Small::BM) * ((N + cols - 1) / cols);
-}
-
-hipError_t launch_product(const Product& p, hipStream_t stream) {
-    if (p.backward) launch<Small, kBackward>(p, stream);
-    else if (p.matrices == 2) launch<Small, kGated>(p, stream);
-    else launch<Small, kLinear>(p, stream);
-    return hipGetLastError();
+void launch_product_tiles(const Product& p, const ProductPlan& plan, hipStream_t stream) {
+    if (p.backward) launch<Small, kBackward>(p, plan, stream);
+    else if (p.matrices == 2) launch<Small, kGated>(p, plan, stream);
+    else launch<Small, kLinear>(p, plan, stream);
 }
 
 }  // namespace nvfp4

@@ -474,7 +474,7 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  * a NaN or an infinity has unspecified results in that row (rows, never others). A tensor of outputs may
  * not overlap any other tensor of the call, but Y may be the residual itself (same address, same stride).
  *
- * Requires in % 16 == 0, in >= 16, out >= 1 (a product with an empty matrix is refused), out * in / 16 < 2^31,
+ * Requires in % 16 == 0, in >= 16, out >= 1 (a product with an empty matrix is refused), in and out < 2^24, out * in / 16 < 2^31,
  * tokens < 2^31, batch <= 65,535, packed 8-byte aligned, stride a multiple of 16. tokens == 0 is valid.
  * Workspaces: 16-byte aligned, no initialisation needed, of at least the size that the query of the same
  * name gives for the same sizes (NULL is valid where that is 0).
