@@ -51,7 +51,8 @@ struct Product {
     int64_t ldpre[2];
     void* y;
     int64_t ldy;
-    float* partial;          // [splits][tokens][columns, gated: twice], where there are splits
+    bool wide;               // rows of y, pre, residual and bias are whole 16-byte pieces
+    float* partial;          // [splits][tokens][columns up to a multiple of 8, gated: twice], where there are splits
 };
 
 // Tiles of `size` rows that the matrices' rows make at most.

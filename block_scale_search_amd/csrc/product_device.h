@@ -135,9 +135,93 @@ __device__ __forceinline__ void product_gated(const Product& p, int64_t t, int64
     store_value(p.y, t * p.ldy + n, (f32 ? act_value<true>(p.act, g) : act_value<false>(p.act, g)) * u, f32);
 }
 
-// Where share `split` of a product's reduction leaves its sum (times S) of row t and column n of `cols`.
-__device__ __forceinline__ float& product_partial(const Product& p, int split, int64_t t, int64_t n, int64_t cols) {
-    return p.partial[((int64_t)split * p.rows.tokens + t) * cols + n];
+// Columns of a product's partial sums: whole pieces of 8 (a gated pair's u behind its g).
+__device__ __forceinline__ int64_t partial_cols(int64_t N) { return (N + 7) & ~(int64_t)7; }
+
+// Values c .. c + 7 of a row, zeros from `cols`; `wide`: rows are laid out for 16-byte accesses.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, int64_t row, int64_t c, int64_t cols, bool wide, float (&x)[8]) {
+    if (wide && c + 8 <= cols) {
+        if constexpr (F32) {
+            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + c);
+            const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + c + 4);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+            const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + row + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = bf16_lo(a[k]);
+                x[2 * k + 1] = bf16_hi(a[k]);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = c + k < cols ? load_value(p, row + c + k, F32) : 0.0f;
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t row, int64_t c, int64_t cols, bool wide, const float (&x)[8]) {
+    if (wide && c + 8 <= cols) {
+        if constexpr (F32) {
+            float* to = static_cast<float*>(p) + row + c;
+            *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + row + c) =
+                u32x4{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (c + k < cols) store_value(p, row + c + k, x[k], F32);
+}
+
+// Columns n .. n + 7 (a multiple of 8) of row t, which is matrix e's: a share's sums (of several) to the workspace,
+// else what the product makes of them. v: sums times S; gated, u: the second matrix's.
+template <bool GATED, bool F32>
+__device__ __forceinline__ void product_out8(const Product& p, int splits, int split, int64_t e, int64_t t, int64_t n,
+                                             int64_t N, float (&v)[8], float (&u)[8]) {
+    if (splits > 1) {
+        const int64_t cols = partial_cols(N);
+        float* to = p.partial + ((int64_t)split * p.rows.tokens + t) * (GATED ? 2 * cols : cols) + n;
+        reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if constexpr (GATED) {
+            reinterpret_cast<float4*>(to + cols)[0] = make_float4(u[0], u[1], u[2], u[3]);
+            reinterpret_cast<float4*>(to + cols)[1] = make_float4(u[4], u[5], u[6], u[7]);
+        }
+        return;
+    }
+    if constexpr (GATED) {
+        if (p.pre[0]) {
+            store8<F32>(p.pre[0], t * p.ldpre[0], n, N, p.wide, v);
+            store8<F32>(p.pre[1], t * p.ldpre[1], n, N, p.wide, u);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = act_value<F32>(p.act, v[k]) * u[k];
+    } else if (!p.backward) {
+        if (p.bias) {
+            float b[8];
+            load8<F32>(p.bias, e * N, n, N, p.wide, b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] += b[k];
+        }
+        if (p.pre[0]) store8<F32>(p.pre[0], t * p.ldpre[0], n, N, p.wide, v);
+        if (p.act != kActNone) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = act_value<F32>(p.act, v[k]);
+        }
+        if (p.residual) {
+            float r[8];
+            load8<F32>(p.residual, t * p.ldr, n, N, p.wide, r);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] += r[k];
+        }
+    }
+    store8<F32>(p.y, t * p.ldy, n, N, p.wide, v);
 }
 
 typedef __attribute__((address_space(1))) const void* GlobalPtr;
@@ -149,6 +233,43 @@ __device__ __forceinline__ void copy16(const void* src, void* lds) {
 }
 __device__ __forceinline__ void copy4(const void* src, void* lds) {
     __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)lds, 4, 0, 0);
+}
+
+// Loads through a buffer descriptor over `bytes` from p, from a lane's offset plus a uniform one: an offset of
+// kNowhere reads zeros.
+constexpr uint32_t kReach = 0x80000000u, kNowhere = 0xC0000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void* p, uint32_t bytes = kReach) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+// `at` where in, else kNowhere; by a select (the compiler would make two loads and a branch of it).
+__device__ __forceinline__ uint32_t offset_if(bool in, uint32_t at) {
+    uint32_t v = in ? at : kNowhere;
+    asm("" : "+v"(v));
+    return v;
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t plus = 0) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, plus, 0));
+}
+__device__ __forceinline__ u32x2 load8(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t plus = 0) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at, plus, 0));
+}
+__device__ __forceinline__ uint32_t load4(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t plus = 0) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, at, plus, 0);
+}
+__device__ __forceinline__ uint32_t load2(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t plus = 0) {
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, plus, 0);
+}
+__device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t plus = 0) {
+    return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, at, plus, 0);
+}
+
+// copy16, from a uniform address plus a lane's offset, that the compiler does not see as one: it would wait for all
+// copies under way before the next write to LDS, whichever part of it they are for. The caller waits, by wait_copies.
+__device__ __forceinline__ void copy16_unseen(const void* src, uint32_t at, void* lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(at), "s"(src), "s"((uint32_t)(uintptr_t)(LdsPtr)lds)
+                 : "memory", "m0");
 }
 
 // Waits until at most N of the wave's loads and copies are under way, and for its LDS accesses.
@@ -176,6 +297,12 @@ struct RowTile {
     int32_t e, rows;
     int64_t first;
 };
+
+// A value that is the same in every lane, for the compiler to keep it in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+                     ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32));
+}
 
 // Tile `tile` of the matrices' rows in tiles of `size`, numbered matrix by matrix. Each wave finds it by
 // itself (64 matrices at a time); false past the last.

@@ -10,41 +10,39 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One thread per output column of a row: the shares' sums (each times S already) in order, then what the
+// One thread per 8 output columns of a row: the shares' sums (each times S already) in order, then what the
 // product's own kernel does with whole sums.
 template <bool GATED, bool F32>
-__global__ __launch_bounds__(kThreads) void k_product_join(Product p, int splits, int64_t N, int64_t total) {
+__global__ __launch_bounds__(kThreads) void k_product_join(Product p, int splits, int64_t N, int64_t pieces, int64_t total) {
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i >= total) return;
-    const int64_t t = i / N, n = i - t * N;
+    const int64_t t = i / pieces, n = (i - t * pieces) * 8;
     if (t >= rows_end(p.rows)) return;
-    const auto sum = [&](int64_t c) {
-        float s = 0.0f;
-        for (int k = 0; k < splits; ++k) s += product_partial(p, k, t, c, GATED ? 2 * N : N);
-        return s;
+    const int64_t cols = partial_cols(N), stride = p.rows.tokens * (GATED ? 2 * cols : cols);
+    const float* from = p.partial + t * (GATED ? 2 * cols : cols) + n;
+    const auto sum = [&](const float* q, float (&s)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k] = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < splits; ++k, q += stride) {
+            const float4 a = reinterpret_cast<const float4*>(q)[0], b = reinterpret_cast<const float4*>(q)[1];
+            s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+            s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+        }
     };
-    if constexpr (GATED) {
-        product_gated(p, t, n, sum(n), sum(N + n), F32);
-    } else {
-        float v = sum(n);
-        if (p.backward) {
-            store_value(p.y, t * p.ldy + n, v, F32);
-            return;
+    float v[8], u[8];
+    sum(from, v);
+    if constexpr (GATED) sum(from + cols, u);
+    int e = 0;
+    if (p.bias && p.rows.seg) {                          // the last matrix whose rows start at or before t
+        int hi = p.rows.batch;
+        while (hi - e > 1) {
+            const int mid = (e + hi) >> 1;
+            if (p.rows.seg[mid] <= t) e = mid;
+            else hi = mid;
         }
-        if (p.bias) {
-            int e = 0;
-            if (p.rows.seg) {                            // the last matrix whose rows start at or before t
-                int hi = p.rows.batch;
-                while (hi - e > 1) {
-                    const int mid = (e + hi) >> 1;
-                    if (p.rows.seg[mid] <= t) e = mid;
-                    else hi = mid;
-                }
-            }
-            v += load_value(p.bias, e * N + n, F32);
-        }
-        product_linear(p, t, n, v, F32);
     }
+    product_out8<GATED, F32>(p, 1, 0, e, t, n, N, v, u);
 }
 
 }  // namespace
@@ -91,10 +89,17 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
 size_t product_partial_bytes(const ProductPlan& plan, int64_t tokens, int64_t out, int64_t in,
                              int32_t matrices, bool backward) {
     if (plan.splits <= 1) return 0;
-    return (size_t)(plan.splits * tokens * (backward ? in : out * matrices)) * 4;
+    const int64_t N = backward ? in : out;
+    return (size_t)(plan.splits * tokens * ((N + 7) / 8 * 8) * (backward ? 1 : matrices)) * 4;
 }
 
-hipError_t launch_product(const Product& p, hipStream_t stream) {
+hipError_t launch_product(const Product& given, hipStream_t stream) {
+    Product p = given;
+    const auto wide = [&](const void* q, int64_t ld) {
+        return q == nullptr || ((reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld % (p.f32 ? 4 : 8) == 0);
+    };
+    p.wide = wide(p.y, p.ldy) && wide(p.pre[0], p.ldpre[0]) && wide(p.pre[1], p.ldpre[1]) &&
+             wide(p.residual, p.ldr) && wide(p.bias, p.out);
     ProductPlan plan = product_plan(p.rows.tokens, p.rows.batch, p.out, p.in, p.matrices, p.backward, p.f32);
     // the tile kernel asks for less: alignment beyond what codes and scale bytes need have, and rows close enough
     // together for 32-bit offsets
@@ -113,17 +118,17 @@ hipError_t launch_product(const Product& p, hipStream_t stream) {
         launch_product_tiles(p, plan, stream);
     }
     if (plan.splits > 1) {
-        const int64_t N = p.backward ? p.in : p.out, total = p.rows.tokens * N;
+        const int64_t N = p.backward ? p.in : p.out, pieces = (N + 7) / 8, total = p.rows.tokens * pieces;
         const dim3 grid((uint32_t)((total + kThreads - 1) / kThreads));
         const bool gated = !p.backward && p.matrices == 2;
         if (gated && p.f32)
-            hipLaunchKernelGGL((k_product_join<true, true>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+            hipLaunchKernelGGL((k_product_join<true, true>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, pieces, total);
         else if (gated)
-            hipLaunchKernelGGL((k_product_join<true, false>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+            hipLaunchKernelGGL((k_product_join<true, false>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, pieces, total);
         else if (p.f32)
-            hipLaunchKernelGGL((k_product_join<false, true>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+            hipLaunchKernelGGL((k_product_join<false, true>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, pieces, total);
         else
-            hipLaunchKernelGGL((k_product_join<false, false>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, total);
+            hipLaunchKernelGGL((k_product_join<false, false>), grid, dim3(kThreads), 0, stream, p, plan.splits, N, pieces, total);
     }
     return hipGetLastError();
 }

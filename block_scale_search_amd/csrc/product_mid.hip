@@ -123,28 +123,32 @@ __global__ __launch_bounds__(kThreads) void k_product_mid(Product p, int nn, int
         }
     }
 
-    // a lane holds rows 8 (e / 4) + 4 kg + e % 4 of matrix row n32
-    const bool second = GATED && n32 >= 16;
-    const float S = p.w[second ? 1 : 0].S[rows.e];
-    const int64_t n = n0 + (GATED ? wave * 16 + (n32 & 15) : wave * 32 + n32);
-    const float bias = !GATED && p.bias && n < N ? load_value(p.bias, rows.e * (int64_t)N + n, false) : 0.0f;
+    // a lane holds rows 8 (e / 4) + 4 kg + e % 4 of matrix row n32; by way of LDS it gets 8 columns of a row
+    const float S = p.w[GATED && n32 >= 16 ? 1 : 0].S[rows.e];
+    constexpr int kWide = kCols + 4, kLanes = kOut / 8;
+    static_assert(sizeof(float) * 32 * kWide <= sizeof(stage), "LDS of the outputs");
+    float* out = reinterpret_cast<float*>(stage);
+    const int column = GATED ? (n32 >> 4) * kOut + wave * 16 + (n32 & 15) : wave * 32 + n32;
 #pragma unroll
-    for (int a = 0; a < TM; ++a)
+    for (int a = 0; a < TM; ++a) {
+        __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int row = 32 * a + (e >> 2) * 8 + kg * 4 + (e & 3);
-            const int64_t t = rows.first + row;
-            const float v = acc[a][e] * S;
-            const float other = GATED ? __shfl_xor(v, 16, 64) : 0.0f;
-            if (n >= N || row >= rows.rows) continue;
-            if (splits > 1) {
-                product_partial(p, split, t, second ? N + n : n, GATED ? 2 * N : N) = v;
-            } else if constexpr (GATED) {
-                if (!second) product_gated(p, t, n, v, other, false);
-            } else {
-                product_linear(p, t, n, v + bias, false);
+        for (int e = 0; e < 16; ++e) out[((e >> 2) * 8 + kg * 4 + (e & 3)) * kWide + column] = acc[a][e] * S;
+        __syncthreads();
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += kThreads / kLanes) {
+            const int r = r0 + (int)threadIdx.x / kLanes, c = (int)threadIdx.x % kLanes * 8, row = 32 * a + r;
+            const float* from = out + r * kWide + c;
+            float v[8], u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = from[k];
+                u[k] = GATED ? from[kOut + k] : 0.0f;
             }
+            if (row < rows.rows && n0 + c < N)
+                product_out8<GATED, false>(p, splits, split, rows.e, rows.first + row, n0 + c, N, v, u);
         }
+    }
 }
 
 template <int BM, int STAGES, bool GATED>

@@ -50,47 +50,6 @@ __device__ __forceinline__ void store_parts(const float (&x)[8], uint16_t* parts
         *reinterpret_cast<u32x4*>(parts + k * plane + at) = pack8(b[k]);
 }
 
-// Values c .. c + 7 of a row, zeros from `cols`; `wide`: rows are laid out for 16-byte accesses.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t row, int64_t c, int64_t cols, bool wide, float (&x)[8]) {
-    if (wide && c + 8 <= cols) {
-        if constexpr (F32) {
-            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + c);
-            const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + c + 4);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
-            const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + row + c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[2 * k] = bf16_lo(a[k]);
-                x[2 * k + 1] = bf16_hi(a[k]);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = c + k < cols ? load_value(p, row + c + k, F32) : 0.0f;
-}
-
-template <bool F32>
-__device__ __forceinline__ void store8(void* p, int64_t row, int64_t c, int64_t cols, bool wide, const float (&x)[8]) {
-    if (wide && c + 8 <= cols) {
-        if constexpr (F32) {
-            float* to = static_cast<float*>(p) + row + c;
-            *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + row + c) =
-                u32x4{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
-        }
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (c + k < cols) store_value(p, row + c + k, x[k], F32);
-}
-
 // One thread per piece of 8 values, `pieces` a row.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void k_product_parts(const void* X, int64_t cols, int64_t ldx, bool wide,

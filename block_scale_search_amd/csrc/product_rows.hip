@@ -29,24 +29,6 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                    c, 0, 0, 0);
 }
 
-// Loads through a buffer descriptor over everything from p: an offset of kNowhere reads zeros.
-constexpr uint32_t kReach = 0x80000000u, kNowhere = 0xC0000000u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void* p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, kReach, 0x00027000);
-}
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
-}
-__device__ __forceinline__ u32x2 load8(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
-}
-__device__ __forceinline__ uint32_t load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-    return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
-}
-__device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-    return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, at, 0, 0);
-}
-
 // Sum over four neighbouring lanes, in each of them.
 __device__ __forceinline__ float sum_quad(float v) {
     v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));

@@ -10,6 +10,9 @@
 // both values of an output are in the same lane.
 #include <hip/hip_runtime.h>
 
+#include <stdlib.h>
+#include <type_traits>
+
 #include "internal.h"
 #include "product_device.h"
 
@@ -35,8 +38,16 @@ __device__ __forceinline__ int swizzle(int r) { return (r ^ (r >> 3)) & 7; }
 // four rows, their scale bytes.
 struct Raw {
     u32x4 code;
-    uint32_t scale;
+    uint32_t scale[4];
 };
+
+template <typename F>
+__device__ __forceinline__ void unroll4(F&& f) {
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
+}
 
 // Where in the reduction a step lies: step `kt` of plane `plane` of matrix `m`.
 struct Cursor {
@@ -46,119 +57,152 @@ struct Cursor {
         plane = step / nk % planes;
         m = step / nk / planes;
     }
-    __device__ __forceinline__ void next(int nk, int planes) {
-        if (++kt == nk) {
-            kt = 0;
-            if (++plane == planes) {
-                plane = 0;
-                ++m;
-            }
-        }
+    __device__ __forceinline__ void next(bool really, int nk, int planes) {
+        const int k = kt + (really ? 1 : 0), q = plane + (k == nk ? 1 : 0);
+        kt = k == nk ? 0 : k;
+        plane = q == planes ? 0 : q;
+        m += q == planes ? 1 : 0;
     }
 };
 
-template <int M_, int N_, int WM_, int WN_, int MODE, bool F32>
-__global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int nn, int splits, int each) {
+// Workgroup -> tile. Workgroups go to the 8 XCDs in turn: XCD x takes a run of tiles, and a run walks down 4 row tiles
+// before the next column tile, so that the 32 workgroups on an XCD read 4 row tiles and 8 column tiles together.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t blocks, uint32_t nm, uint32_t nn, int& tm, int& tn) {
+    const uint32_t xcd = id & 7, rest = blocks & 7;
+    const uint32_t q = xcd * (blocks >> 3) + min(xcd, rest) + (id >> 3);
+    const uint32_t group = q / (4 * nn), l = q - group * 4 * nn;
+    const uint32_t high = min(4u, nm - 4 * group);
+    tn = (int)(l / high);
+    tm = (int)(4 * group + l - (uint32_t)tn * high);
+}
+
+// WHOLE (forward): in is a multiple of 32, so a thread's 32 columns are all inside the matrix or all outside.
+template <int M_, int N_, int WM_, int WN_, int MODE, bool F32, bool WHOLE>
+__global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int nm, int nn, int splits, int each) {
     typedef Shape<M_, N_, WM_, WN_> S;
     constexpr int BM = S::BM, BN = S::BN, TM = S::TM, TN = S::TN;
-    __shared__ __align__(1024) uint16_t lds_a[2][BM][BK];
-    __shared__ __align__(1024) uint16_t lds_b[2][BN][BK];
+    __shared__ __align__(1024) uint16_t lds[2 * (BM + BN) * BK];
+    uint16_t (&lds_a)[2][BM][BK] = *reinterpret_cast<uint16_t (*)[2][BM][BK]>(lds);
+    uint16_t (&lds_b)[2][BN][BK] = *reinterpret_cast<uint16_t (*)[2][BN][BK]>(lds + 2 * BM * BK);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
     const uint32_t of = blockIdx.x / (uint32_t)splits;
     const int split = (int)(blockIdx.x - of * (uint32_t)splits);
-    const int tile = (int)(of / (uint32_t)nn), tn = (int)(of - (uint32_t)tile * (uint32_t)nn);
+    int tile, tn;
+    tile_of(of, (uint32_t)nm * (uint32_t)nn, (uint32_t)nm, (uint32_t)nn, tile, tn);
     RowTile rows;
     if (!find_rows(p.rows, tile, BM, rows)) return;
+    rows.e = __builtin_amdgcn_readfirstlane(rows.e);
+    rows.first = uniform(rows.first);
 
     constexpr int kCols = MODE == kGated ? BN / 2 : BN;            // output columns of a tile
     const int64_t n0 = (int64_t)tn * kCols;
     const int64_t N = MODE == kBackward ? p.in : p.out;
-    const int64_t K = MODE == kBackward ? p.out : p.in;
-    const int64_t k_pad = (K + 7) / 8 * 8;
-    const int nk = (int)((K + BK - 1) / BK);
+    const int K = (int)(MODE == kBackward ? p.out : p.in);
+    const int k_pad = (K + 7) & ~7;
+    const int nk = (K + BK - 1) / BK;
     const int matrices = MODE == kBackward ? p.matrices : 1;
     const int begin = split * each, steps = min(each, nk * p.planes * matrices - begin);
+    const int to_switch = nk * p.planes - begin;         // the step at which the second matrix begins
 
-    const auto load_a = [&](int buf, const Cursor& c) {
-        const ProductOperand& a = p.a[MODE == kBackward ? c.m : 0];
-        const uint16_t* base = a.p + c.plane * p.plane;
-        const int64_t k0 = (int64_t)c.kt * BK;
+    // copies of the rows' side: a thread's piece is the same in each of its rows
+    const uint16_t* const a0 = p.a[0].p + rows.first * p.a[0].ld;
+    const uint16_t* const a1 = p.a[1].p + rows.first * p.a[1].ld;
+    uint32_t xrow[S::kLoads];
 #pragma unroll
-        for (int r = 0; r < S::kLoads; ++r) {
-            const int id = tid + S::kThreads * r, row = id >> 3;
-            const int64_t k = k0 + ((id & 7) ^ swizzle(row)) * 8;
-            // rows past the tile read its last row, pieces past the edge the row's first: both meet
-            // columns that are not stored or weights of zero
-            const uint16_t* from = base + (rows.first + min(row, rows.rows - 1)) * a.ld + (k < k_pad ? k : 0);
-            copy16(from, &lds_a[buf][(S::kThreads * r + 64 * wave) >> 3][0]);
-        }
+    for (int r = 0; r < S::kLoads; ++r)                  // rows past the tile read its last row: they are not stored
+        xrow[r] = (uint32_t)min((tid + S::kThreads * r) >> 3, rows.rows - 1) * (uint32_t)p.a[0].ld * 2;
+    // rows 32 apart differ in bit 2 of the swizzle, rows 64 apart have the same
+    constexpr int kPieces = S::kThreads == 256 ? 2 : 1;
+    static_assert(S::kThreads == 256 || S::kThreads == 512, "32 or 64 rows a turn");
+    const int xpiece = ((tid & 7) ^ swizzle(tid >> 3)) * 16;
+    struct Source {
+        const uint16_t* p;
+        uint32_t at[kPieces];
+    };
+    const auto source = [&](const Cursor& c) {
+        // pieces past the edge read the row's last: they meet weights of zero
+        const uint16_t* base = MODE == kBackward && c.m ? a1 : a0;
+        base += c.plane * p.plane + c.kt * BK;
+        const int last = (k_pad - c.kt * BK) * 2 - 16;
+        Source s;
+        s.p = reinterpret_cast<const uint16_t*>(uniform(reinterpret_cast<int64_t>(base)));
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) s.at[k] = (uint32_t)min(xpiece ^ (64 * k), last);
+        return s;
+    };
+    const auto load_a = [&](int buf, const Source& from, int r) {
+        copy16_unseen(from.p, xrow[r] + from.at[r % kPieces], &lds_a[buf][(S::kThreads * r + 64 * wave) >> 3][0]);
     };
 
     // forward: row b_row of lds_b, half b_half of its 64 values
     const int b_row = tid >> 1, b_half = tid & 1;
     // backward: columns 8 b_block .. + 7, values 8 b_octet + 4 b_half .. + 3
     const int b_block = (tid >> 1) % (BN / 8), b_octet = (tid >> 1) / (BN / 8);
-    const auto load_b = [&](Raw& raw, const Cursor& c) {
-        const int64_t k0 = (int64_t)c.kt * BK;
+    uint32_t b_code, b_scale;                            // of the thread's first code: bytes from the windows' start
+    const uint8_t *codes, *scales;                       // forward: from row n0 (of the wave's matrix)
+    if constexpr (MODE == kBackward) {
+        const uint32_t at = (uint32_t)(b_octet * 8 + b_half * 4) * (uint32_t)N + (uint32_t)min(n0 + b_block * 8, N - 8);
+        b_code = at / 2;
+        b_scale = at / 16;
+    } else {
+        const int second = MODE == kGated ? wave & 1 : 0;              // a wave's 32 rows are of one matrix
+        const int c32 = MODE == kGated ? (b_row >> 6) * 32 + (b_row & 31) : b_row;
+        const ProductMatrix& w = p.w[second];
+        const int64_t at = rows.e * w.stride + n0 * K;
+        codes = w.packed + at / 2;
+        scales = w.scales + at / 16;
+        b_scale = (uint32_t)(min(n0 + c32, N - 1) - n0) * (uint32_t)(K / 16) + 2 * b_half;
+        b_code = b_scale * 8;
+    }
+    const auto load_b = [&](Raw& raw, const Cursor& c, int step) {
+        const int left = K - c.kt * BK;                  // of the reduction
+        const uint32_t reach = step < steps ? kReach : 0;              // no codes past the last step
         if constexpr (MODE == kBackward) {
             const ProductMatrix& w = p.w[c.m];
-            const int64_t col = min(n0 + b_block * 8, N - 8);
-            raw.scale = 0;
+            const int64_t at = rows.e * w.stride + (int64_t)c.kt * BK * N;
+            const __amdgpu_buffer_rsrc_t from = window(w.packed + at / 2, reach), bytes = window(w.scales + at / 16, reach);
+            const int mine = left - (b_octet * 8 + b_half * 4);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t o = k0 + b_octet * 8 + b_half * 4 + r;
-                const int64_t at = rows.e * w.stride + min(o, K - 1) * p.in + col;
-                raw.code[r] = *reinterpret_cast<const uint32_t*>(w.packed + at / 2);
-                const uint32_t s = w.scales[at / 16];
-                raw.scale |= (o < K ? s : 0u) << (8 * r);
+            for (int r = 0; r < 4; ++r) {                // N / 2 and N / 16 are whole
+                raw.code[r] = load4(from, offset_if(r < mine, b_code), (uint32_t)r * (uint32_t)(N / 2));
+                raw.scale[r] = load1(bytes, offset_if(r < mine, b_scale), (uint32_t)r * (uint32_t)(N / 16));
             }
         } else {
-            const int second = MODE == kGated ? (b_row >> 5) & 1 : 0;
-            const int c32 = MODE == kGated ? (b_row >> 6) * 32 + (b_row & 31) : b_row;
-            const ProductMatrix& w = p.w[second];
-            const int64_t k = k0 + b_half * 32;
-            const int64_t at = rows.e * w.stride + min(n0 + c32, N - 1) * K + k;
-            if (k + 32 <= K) {
-                raw.code = *reinterpret_cast<const u32x4_at8*>(w.packed + at / 2);
-                raw.scale = *reinterpret_cast<const u16_at1*>(w.scales + at / 16);
+            const __amdgpu_buffer_rsrc_t from = window(codes, reach), bytes = window(scales, reach);
+            const uint32_t k = (uint32_t)c.kt * (BK / 16);
+            const bool in = b_half * 32 < left;
+            if constexpr (WHOLE) {
+                raw.code = load16(from, offset_if(in, b_code), k * 8);
+                raw.scale[0] = load2(bytes, offset_if(in, b_scale), k);
             } else {
-                raw.code = u32x4{0u, 0u, 0u, 0u};
-                raw.scale = 0;
-                if (k + 16 <= K) {
-                    const u32x2 half = *reinterpret_cast<const u32x2_at8*>(w.packed + at / 2);
-                    raw.code[0] = half[0];
-                    raw.code[1] = half[1];
-                    raw.scale = w.scales[at / 16];
-                }
+                const bool in2 = b_half * 32 + 16 < left;
+                const u32x2 lo = load8(from, offset_if(in, b_code), k * 8), hi = load8(from, offset_if(in2, b_code + 8), k * 8);
+                raw.code = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                raw.scale[0] = load1(bytes, offset_if(in, b_scale), k);
+                raw.scale[1] = load1(bytes, offset_if(in2, b_scale + 1), k);
             }
         }
     };
-    const auto store_b = [&](int buf, const Raw& raw) {
+    // a quarter of a thread's weights, converted and written: piece 0 .. 3
+    const auto store_b = [&](int buf, const Raw& raw, auto which) {
+        constexpr int I = decltype(which)::value;
         if constexpr (MODE == kBackward) {
-            float x[4][8];
+            float x[4][2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float s = r == 0 ? scale_value<0>(raw.scale) : r == 1 ? scale_value<1>(raw.scale)
-                              : r == 2 ? scale_value<2>(raw.scale) : scale_value<3>(raw.scale);
-                code_values<0>(raw.code[r], s, x[r][0], x[r][1]);
-                code_values<1>(raw.code[r], s, x[r][2], x[r][3]);
-                code_values<2>(raw.code[r], s, x[r][4], x[r][5]);
-                code_values<3>(raw.code[r], s, x[r][6], x[r][7]);
-            }
+            for (int r = 0; r < 4; ++r) code_values<I>(raw.code[r], scale_value<0>(raw.scale[r]), x[r][0], x[r][1]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = b_block * 8 + j;
+            for (int j = 0; j < 2; ++j) {
+                const int row = b_block * 8 + 2 * I + j;
                 *reinterpret_cast<u32x2*>(&lds_b[buf][row][(b_octet ^ swizzle(row)) * 8 + b_half * 4]) =
                     u32x2{bf16_pair(x[0][j], x[1][j]), bf16_pair(x[2][j], x[3][j])};
             }
         } else {
-            const float s0 = scale_value<0>(raw.scale), s1 = scale_value<1>(raw.scale);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<u32x4*>(&lds_b[buf][b_row][((b_half * 4 + j) ^ swizzle(b_row)) * 8]) =
-                    dequant8(raw.code[j], j < 2 ? s0 : s1);
+            const float s = I < 2 ? scale_value<0>(raw.scale[0]) : WHOLE ? scale_value<1>(raw.scale[0])
+                                                                         : scale_value<0>(raw.scale[1]);
+            *reinterpret_cast<u32x4*>(&lds_b[buf][b_row][((b_half * 4 + I) ^ swizzle(b_row)) * 8]) =
+                dequant8(raw.code[I], s);
         }
     };
 
@@ -170,99 +214,164 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.0f;
 
+    // operands of one slice of 16: a lane holds values 8 kg .. + 7 of row r32 of each 32-row block
+    struct Frag {
+        bf16x8 a[TM], b[TN];
+    };
     const int r32 = lane & 31, kg = lane >> 5;
+    const auto read = [&](Frag& f, int buf, int slice) {
+        const int c = 2 * slice + kg;
+#pragma unroll
+        for (int b = 0; b < TN; ++b) {
+            const int row = (wn * TN + b) * 32 + r32;
+            f.b[b] = *reinterpret_cast<const bf16x8*>(&lds_b[buf][row][(c ^ swizzle(row)) * 8]);
+        }
+#pragma unroll
+        for (int a = 0; a < TM; ++a) {
+            const int row = (wm * TM + a) * 32 + r32;
+            f.a[a] = *reinterpret_cast<const bf16x8*>(&lds_a[buf][row][(c ^ swizzle(row)) * 8]);
+        }
+    };
+    const auto multiply = [&](const Frag& f) {
+#pragma unroll
+        for (int a = 0; a < TM; ++a)
+#pragma unroll
+            for (int b = 0; b < TN; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[a], f.b[b], acc[a][b], 0, 0, 0);
+    };
+    // the order of a slice: its matrix instructions with the next slice's reads and a quarter of the conversion between
+    const auto interleave = [&]() {
+#pragma unroll
+        for (int i = 0; i < TM * TN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, (24 + TM * TN - 1) / (TM * TN), 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x200, 2, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // Step s is multiplied from one half of LDS while step s + 1 is made in the other: its rows are copied, its
+    // codes converted from registers, and the codes of the steps after it loaded. A step's one barrier stands before
+    // its last slice, whose operands are in registers by then: behind it the first half is free, and the last
+    // slice's matrix instructions cover the reads of step s + 1's first operands. Steps go in pairs: past the last,
+    // copies are of the last step again and codes zeros (two ways out of the loop would cost registers).
     Cursor ca, cb;
     cb.at(begin, nk, p.planes);
     ca = cb;
-    const int to_switch = nk * p.planes - begin;         // the step at which the second matrix begins
-    Raw raw;
-    load_b(raw, cb);
-    load_a(0, ca);
-    store_b(0, raw);
-    ca.next(nk, p.planes);
-    cb.next(nk, p.planes);
-    if (steps > 1) load_b(raw, cb);
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        const int buf = s & 1;
-        if (s + 1 < steps) load_a(buf ^ 1, ca);
-        const Raw now = raw;
-        cb.next(nk, p.planes);
-        ca.next(nk, p.planes);
-        if (s + 2 < steps) load_b(raw, cb);
+    Raw raw[2];                                          // of even and odd steps
+    const auto load_all = [&](int buf) {
+        const Source from = source(ca);
+#pragma unroll
+        for (int r = 0; r < S::kLoads; ++r) load_a(buf, from, r);
+    };
+    load_b(raw[0], cb, 0);
+    load_all(0);
+    unroll4([&](auto i) { store_b(0, raw[0], i); });
+    cb.next(1 < steps, nk, p.planes);
+    ca.next(1 < steps, nk, p.planes);
+    load_b(raw[1], cb, 1);
+    load_all(1);
+    cb.next(2 < steps, nk, p.planes);
+    ca.next(2 < steps, nk, p.planes);
+    load_b(raw[0], cb, 2);
+    wait_copies<0>();
+    barrier();
+    Frag f[2];
+    read(f[0], 0, 0);
+    store_b(1, raw[1], std::integral_constant<int, 0>{});
+    __builtin_amdgcn_sched_barrier(0);
+    // next: the codes of step s + 1, after: of step s + 2
+    const auto step = [&](int s, auto buffer, Raw& next, Raw& after) {
+        constexpr int buf = decltype(buffer)::value;
         if constexpr (MODE == kBackward) {
-            if (s == to_switch && s > 0) {                      // the second matrix's sums carry its S
-                const float f = p.w[0].S[rows.e] / p.w[1].S[rows.e];
+            if (s == to_switch && s > 0 && s < steps) {  // the second matrix's sums carry its S
+                const float r = p.w[0].S[rows.e] / p.w[1].S[rows.e];
 #pragma unroll
                 for (int a = 0; a < TM; ++a)
 #pragma unroll
                     for (int b = 0; b < TN; ++b)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[a][b][e] *= f;
+                        for (int e = 0; e < 16; ++e) acc[a][b][e] *= r;
             }
         }
+        read(f[1], buf, 1);
+        multiply(f[0]);
+        store_b(buf ^ 1, next, std::integral_constant<int, 1>{});
+        interleave();
+        read(f[0], buf, 2);
+        multiply(f[1]);
+        store_b(buf ^ 1, next, std::integral_constant<int, 2>{});
+        interleave();
+        read(f[1], buf, 3);
+        multiply(f[0]);
+        store_b(buf ^ 1, next, std::integral_constant<int, 3>{});
+        interleave();
+        const Source from = source(ca);
+        ca.next(s + 3 < steps, nk, p.planes);
+        cb.next(s + 3 < steps, nk, p.planes);
+        wait_copies<0>();                                // step s + 1's rows and step s + 2's codes
+        barrier();
+        // the last slice: its matrix instructions in TM groups, with the copies between
+        read(f[0], buf ^ 1, 0);
 #pragma unroll
-        for (int ks = 0; ks < BK / 16; ++ks) {
-            bf16x8 fa[TM], fb[TN];
-            const int c = 2 * ks + kg;
+        for (int a = 0; a < TM; ++a) {
 #pragma unroll
-            for (int a = 0; a < TM; ++a) {
-                const int row = (wm * TM + a) * 32 + r32;
-                fa[a] = *reinterpret_cast<const bf16x8*>(&lds_a[buf][row][(c ^ swizzle(row)) * 8]);
-            }
+            for (int b = 0; b < TN; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[1].a[a], f[1].b[b], acc[a][b], 0, 0, 0);
 #pragma unroll
-            for (int b = 0; b < TN; ++b) {
-                const int row = (wn * TN + b) * 32 + r32;
-                fb[b] = *reinterpret_cast<const bf16x8*>(&lds_b[buf][row][(c ^ swizzle(row)) * 8]);
-            }
-#pragma unroll
-            for (int a = 0; a < TM; ++a)
-#pragma unroll
-                for (int b = 0; b < TN; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[a], fb[b], acc[a][b], 0, 0, 0);
+            for (int r = a * S::kLoads / TM; r < (a + 1) * S::kLoads / TM; ++r) load_a(buf, from, r);
+            if (a == TM / 2 - 1) load_b(next, cb, s + 3);
+            if (a == TM - 1) store_b(buf, after, std::integral_constant<int, 0>{});
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (s + 1 < steps) store_b(buf ^ 1, now);
-        __syncthreads();
+    };
+    for (int s = 0; s < steps; s += 2) {
+        step(s, std::integral_constant<int, 0>{}, raw[1], raw[0]);
+        step(s + 1, std::integral_constant<int, 1>{}, raw[0], raw[1]);
     }
+    wait_copies<0>();
+    barrier();
 
     // a lane holds rows 8 (e / 4) + 4 kg + e % 4 of column r32 of each 32 x 32 tile; backward, the sums are over the
     // S of the last matrix met
     const int at = MODE == kBackward && to_switch < steps ? 1 : 0;
     const float S0 = p.w[at].S[rows.e];
     const float S1 = MODE == kGated ? p.w[1].S[rows.e] : 0.0f;
+    // 32 rows at a time by way of the wave's own part of LDS, so that a lane has 8 columns of a row
+    constexpr int kWide = TN * 32 + 4, kLanes = (MODE == kGated ? TN * 16 : TN * 32) / 8;
+    static_assert(sizeof(float) * 32 * kWide * S::WM * S::WN <= sizeof(lds_a) + sizeof(lds_b), "LDS of the outputs");
+    float* mine = reinterpret_cast<float*>(lds) + wave * 32 * kWide;
+    const int64_t n_wave = n0 + wn * (MODE == kGated ? TN * 16 : TN * 32);
 #pragma unroll
-    for (int a = 0; a < TM; ++a)
+    for (int a = 0; a < TM; ++a) {
 #pragma unroll
-        for (int b = 0; b < TN; b += MODE == kGated ? 2 : 1) {
-            const int64_t n = n0 + (MODE == kGated ? (wn * TN + b) * 16 : (wn * TN + b) * 32) + r32;
-            if (n >= N) continue;
-            const float bias = MODE == kLinear && p.bias ? load_value(p.bias, rows.e * N + n, F32) : 0.0f;
+        for (int b = 0; b < TN; ++b)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = (wm * TM + a) * 32 + (e >> 2) * 8 + kg * 4 + (e & 3);
-                if (row >= rows.rows) continue;
-                const int64_t t = rows.first + row;
-                const float v = acc[a][b][e] * S0;
-                if constexpr (MODE == kGated) {
-                    const float u = acc[a][b + 1][e] * S1;
-                    if (splits > 1) {
-                        product_partial(p, split, t, n, 2 * N) = v;
-                        product_partial(p, split, t, N + n, 2 * N) = u;
-                    } else {
-                        product_gated(p, t, n, v, u, F32);
-                    }
-                } else if (splits > 1) {
-                    product_partial(p, split, t, n, N) = v;
-                } else if constexpr (MODE == kBackward) {
-                    store_value(p.y, t * p.ldy + n, v, F32);
-                } else {
-                    product_linear(p, t, n, v + bias, F32);
-                }
+            for (int e = 0; e < 16; ++e)
+                mine[((e >> 2) * 8 + kg * 4 + (e & 3)) * kWide + b * 32 + r32] =
+                    acc[a][b][e] * (MODE == kGated && b % 2 ? S1 : S0);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += 64 / kLanes) {
+            const int r = r0 + lane / kLanes, c = lane % kLanes * 8, row = (wm * TM + a) * 32 + r;
+            // gated: 8 of the 32 columns of a pair of MFMA tiles
+            const float* from = mine + r * kWide + (MODE == kGated ? c / 32 * 64 + c % 32 : c);
+            float v[8], u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = from[k];
+                u[k] = MODE == kGated ? from[32 + k] : 0.0f;
             }
+            if (row < rows.rows && n_wave + c < N)
+                product_out8<MODE == kGated, F32>(p, splits, split, rows.e, rows.first + row, n_wave + c, N, v, u);
         }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 typedef Shape<128, 128, 2, 2> Small;
+typedef Shape<256, 256, 2, 4> Big;
 
 template <typename S, int MODE>
 void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
@@ -270,18 +379,34 @@ void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
     const int64_t cols = MODE == kGated ? S::BN / 2 : S::BN, nn = (N + cols - 1) / cols;
     const int64_t steps = (K + BK - 1) / BK * p.planes * (MODE == kBackward ? p.matrices : 1);
     const int64_t each = (steps + plan.splits - 1) / plan.splits;
-    const dim3 grid((uint32_t)(product_row_tiles(p.rows.tokens, p.rows.batch, S::BM) * nn * plan.splits));
-    if (p.f32)
-        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, true>), grid, dim3(S::kThreads), 0,
-                           stream, p, (int)nn, plan.splits, (int)each);
-    else
-        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, false>), grid, dim3(S::kThreads), 0,
-                           stream, p, (int)nn, plan.splits, (int)each);
+    const int64_t nm = product_row_tiles(p.rows.tokens, p.rows.batch, S::BM);
+    const dim3 grid((uint32_t)(nm * nn * plan.splits)), threads(S::kThreads);
+    const bool whole = MODE == kBackward || p.in % 32 == 0;
+    if (p.f32 && whole)
+        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, true, true>), grid, threads, 0, stream, p,
+                           (int)nm, (int)nn, plan.splits, (int)each);
+    else if (whole)
+        hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, false, true>), grid, threads, 0, stream, p,
+                           (int)nm, (int)nn, plan.splits, (int)each);
+    else if constexpr (MODE != kBackward) {
+        if (p.f32)
+            hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, true, false>), grid, threads, 0,
+                               stream, p, (int)nm, (int)nn, plan.splits, (int)each);
+        else
+            hipLaunchKernelGGL((k_product_tiles<S::BM, S::BN, S::WM, S::WN, MODE, false, false>), grid, threads, 0,
+                               stream, p, (int)nm, (int)nn, plan.splits, (int)each);
+    }
 }
 
 }  // namespace
 
 void launch_product_tiles(const Product& p, const ProductPlan& plan, hipStream_t stream) {
+    if (getenv("BIG")) {
+        if (p.backward) launch<Big, kBackward>(p, plan, stream);
+        else if (p.matrices == 2) launch<Big, kGated>(p, plan, stream);
+        else launch<Big, kLinear>(p, plan, stream);
+        return;
+    }
     if (p.backward) launch<Small, kBackward>(p, plan, stream);
     else if (p.matrices == 2) launch<Small, kGated>(p, plan, stream);
     else launch<Small, kLinear>(p, plan, stream);
