@@ -17,10 +17,19 @@ struct ProductMatrix {
 };
 
 // Which rows meet which matrix: rows seg[e] .. seg[e+1] - 1 matrix e; no seg: all rows matrix 0.
+// map: with more than kMapped matrices, what each tile of rows is (filled by a kernel of its own, which costs what
+// searching the offsets in each workgroup does at about 128: gate and up of 128 matrices of 768 x 2048, 512 rows, 71.6
+// us with a map and 65.6 without); else not used.
+constexpr int kMapped = 128;
+struct RowTile {
+    int32_t e, rows;         // rows 0: none
+    int64_t first;
+};
 struct ProductRows {
     const int64_t* seg;
     int64_t tokens;
     int32_t batch;
+    RowTile* map;
 };
 
 // The activations' side, bf16 rows: `planes` parts of a value (1: bf16 itself, 3: the parts of a
@@ -61,12 +70,19 @@ inline int64_t product_row_tiles(int64_t tokens, int64_t batch, int64_t size) {
     return tokens / size + (batch < tokens ? batch : tokens);
 }
 
+// Rows of tiles in the tile kernel's grid: with several matrices, whole turns of the 8 XCDs.
+inline int64_t product_tile_rows(int64_t tokens, int64_t batch, int64_t size) {
+    const int64_t n = product_row_tiles(tokens, batch, size);
+    return batch > 1 ? (n + 7) / 8 * 8 : n;
+}
+
 // Which kernel computes a product, and in how many shares of its reduction (more than one: their sums go to the
 // workspace, and a second kernel adds them). A function of the sizes alone, since the workspace's size is.
 enum class ProductKernel { kRows, kMid, kTiles };
 struct ProductPlan {
     ProductKernel kernel;
     int32_t tile_rows;       // rows of X a workgroup
+    int32_t tile_cols;       // matrix rows (backward: columns) a workgroup
     int32_t splits;
     int64_t blocks;          // workgroups
 };
@@ -75,7 +91,8 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
 size_t product_partial_bytes(const ProductPlan& plan, int64_t tokens, int64_t out, int64_t in,
                              int32_t matrices, bool backward);
 
-// p.partial: a workspace of product_partial_bytes.
+// p.partial: a workspace of product_partial_bytes; p.rows.map, with several matrices: of product_map_bytes.
+size_t product_map_bytes(const ProductPlan& plan, int64_t tokens, int64_t batch);
 hipError_t launch_product(const Product& p, hipStream_t stream);
 
 // The kernels' launchers.

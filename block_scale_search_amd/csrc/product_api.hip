@@ -77,13 +77,13 @@ nvfp4::ProductMatrix view_of(const nvfp4_matrix* m) {
 }
 
 // Workspace: the operands' parts, where the rows given are not bf16 rows of whole 16-byte pieces, the sums of the
-// shares of a product's reduction, and those of a bias gradient.
+// shares of a product's reduction, the map of its tiles of rows, and the sums of a bias gradient.
 struct Space {
     bool parts;
     int planes;
     int64_t ld, plane;       // elements
     size_t operand;          // bytes of one operand
-    size_t partial, bias;
+    size_t partial, map, bias;
     size_t total;
 };
 Space space_of(int dtype, int64_t tokens, int64_t batch, int64_t out, int64_t in, int32_t matrices, bool backward,
@@ -98,8 +98,9 @@ Space space_of(int dtype, int64_t tokens, int64_t batch, int64_t out, int64_t in
     s.operand = s.parts ? (size_t)up(s.planes * s.plane * 2, 256) : 0;
     const nvfp4::ProductPlan plan = nvfp4::product_plan(tokens, batch, out, in, matrices, backward, f32);
     s.partial = (size_t)up((int64_t)nvfp4::product_partial_bytes(plan, tokens, out, in, matrices, backward), 256);
+    s.map = (size_t)up((int64_t)nvfp4::product_map_bytes(plan, tokens, batch), 256);
     s.bias = with_bias ? nvfp4::product_bias_workspace_bytes(tokens, batch, out) : 0;
-    s.total = s.operand * (backward ? matrices : 1) + s.partial + s.bias;
+    s.total = s.operand * (backward ? matrices : 1) + s.partial + s.map + s.bias;
     return s;
 }
 
@@ -108,13 +109,19 @@ nvfp4_status check_workspace(size_t need, const void* ws, size_t bytes) {
     return aligned(ws, 16) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
+// The product's own part of the workspace, behind the operands.
+void place_sums(nvfp4::Product& p, const Space& s, uint8_t* at) {
+    p.partial = reinterpret_cast<float*>(at);
+    p.rows.map = reinterpret_cast<nvfp4::RowTile*>(at + s.partial);
+}
+
 // The rows' side of a forward product: X itself, or its parts.
 hipError_t forward_operand(nvfp4::Product& p, const Space& s, const void* X, int64_t ldx, void* workspace,
                            hipStream_t stream) {
     p.planes = s.planes;
     p.plane = s.plane;
     p.a[0] = nvfp4::ProductOperand{static_cast<const uint16_t*>(X), ldx};
-    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.operand);
+    place_sums(p, s, static_cast<uint8_t*>(workspace) + s.operand);
     if (!s.parts) return hipSuccess;
     uint16_t* parts = static_cast<uint16_t*>(workspace);
     p.a[0] = nvfp4::ProductOperand{parts, s.ld};
@@ -131,7 +138,7 @@ nvfp4::Product product_of(const nvfp4_matrix* w, const nvfp4_matrix* w2, bool ba
     p.f32 = dtype == NVFP4_DTYPE_F32;
     p.out = w->out;
     p.in = w->in;
-    p.rows = nvfp4::ProductRows{seg, tokens, (int32_t)w->batch};
+    p.rows = nvfp4::ProductRows{seg, tokens, (int32_t)w->batch, nullptr};
     p.act = activation;
     return p;
 }
@@ -142,7 +149,7 @@ nvfp4_status backward(nvfp4::Product& p, nvfp4::ProductSlopes& g, const Space& s
     p.planes = s.planes;
     p.plane = s.plane;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.partial = reinterpret_cast<float*>(ws + p.matrices * s.operand);
+    place_sums(p, s, ws + p.matrices * s.operand);
     for (int m = 0; m < p.matrices; ++m) {
         if (s.parts) {
             g.parts[m] = reinterpret_cast<uint16_t*>(ws + m * s.operand);
@@ -265,7 +272,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
     st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::ProductSlopes g = {};
-    g.rows = nvfp4::ProductRows{seg_offsets, tokens, (int32_t)W->batch};
+    g.rows = nvfp4::ProductRows{seg_offsets, tokens, (int32_t)W->batch, nullptr};
     g.f32 = dtype == NVFP4_DTYPE_F32;
     g.cols = W->out;
     g.act = activation;
@@ -278,7 +285,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
     const hipStream_t on = static_cast<hipStream_t>(stream);
     if (dbias) {
         const hipError_t e =
-            nvfp4::launch_product_bias(g, dbias, static_cast<uint8_t*>(workspace) + s.operand + s.partial, on);
+            nvfp4::launch_product_bias(g, dbias, static_cast<uint8_t*>(workspace) + s.operand + s.partial + s.map, on);
         if (e != hipSuccess) return NVFP4_ERR_HIP;
     }
     if (tokens == 0) return NVFP4_OK;
@@ -316,7 +323,7 @@ nvfp4_status nvfp4_gated_backward(const nvfp4_matrix* W_gate, const nvfp4_matrix
     st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::ProductSlopes g = {};
-    g.rows = nvfp4::ProductRows{seg_offsets, tokens, (int32_t)W_gate->batch};
+    g.rows = nvfp4::ProductRows{seg_offsets, tokens, (int32_t)W_gate->batch, nullptr};
     g.f32 = dtype == NVFP4_DTYPE_F32;
     g.cols = out;
     g.act = activation;

@@ -292,11 +292,10 @@ __device__ __forceinline__ int64_t rows_end(const ProductRows& r) {
     return r.seg ? min(max(r.seg[r.batch], (int64_t)0), r.tokens) : r.tokens;
 }
 
-// A workgroup's rows: `rows` from `first`, all of matrix `e`.
-struct RowTile {
-    int32_t e, rows;
-    int64_t first;
-};
+// v of the lane whose number differs in bit 1.
+__device__ __forceinline__ uint32_t swap_pairs(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
+}
 
 // A value that is the same in every lane, for the compiler to keep it in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t v) {
@@ -304,41 +303,48 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
                      ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32));
 }
 
-// Tile `tile` of the matrices' rows in tiles of `size`, numbered matrix by matrix. Each wave finds it by
-// itself (64 matrices at a time); false past the last.
+// A workgroup's rows: tile `tile` of the matrices' rows in tiles of `size`, numbered matrix by matrix; false past the
+// last. Uniform. A few matrices each wave searches by itself, 64 at a time; for many there is a map.
 __device__ __forceinline__ bool find_rows(const ProductRows& r, int tile, int size, RowTile& t) {
-    if (r.seg == nullptr) {
-        t.e = 0;
-        t.first = (int64_t)tile * size;
-        t.rows = (int32_t)min((int64_t)size, r.tokens - t.first);
-        return t.rows > 0;
-    }
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int base = 0; base < r.batch; base += 64) {
-        int64_t lo = 0, hi = 0;
-        if (base + lane < r.batch) segment(r, base + lane, lo, hi);
-        const int n = (int)((hi - lo + size - 1) / size);
-        int upto = n;
+    t = RowTile{0, 0, 0};
+    if (r.batch <= 1) {
+        int64_t lo = 0, hi = r.tokens;
+        if (r.seg) segment(r, 0, lo, hi);
+        t.first = lo + (int64_t)tile * size;
+        t.rows = (int32_t)min(max(hi - t.first, (int64_t)0), (int64_t)size);
+    } else if (r.batch > kMapped) {
+        t = r.map[tile];
+    } else {
+        const int lane = threadIdx.x & 63;
+        int before = 0;
+        for (int base = 0; base < r.batch; base += 64) {
+            int64_t lo = 0, hi = 0;
+            if (base + lane < r.batch) segment(r, base + lane, lo, hi);
+            const int n = (int)((hi - lo + size - 1) / size);
+            int upto = n;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(upto, d, 64);
-            if (lane >= d) upto += v;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int v = __shfl_up(upto, d, 64);
+                if (lane >= d) upto += v;
+            }
+            const uint64_t in = __ballot(before + upto > tile);
+            if (in) {
+                const int at = __builtin_ctzll(in);
+                const int k = tile - before - (upto - n);            // of the matrix's own tiles
+                const int64_t first = lo + (int64_t)k * size;
+                t.e = base + at;
+                t.rows = __builtin_amdgcn_readlane(k >= 0 && k < n ? (int)min((int64_t)size, hi - first) : 0, at);
+                t.first = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)first, at) |
+                                    ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(first >> 32), at) << 32));
+                break;
+            }
+            before += __builtin_amdgcn_readlane(upto, 63);
         }
-        const uint64_t in = __ballot(before + upto > tile);
-        if (in) {
-            const int at = __builtin_ctzll(in);
-            const int64_t first = lo + (int64_t)(tile - before - (upto - n)) * size;
-            const int rows = (int)min((int64_t)size, hi - first);
-            t.e = base + at;
-            t.rows = __builtin_amdgcn_readlane(rows, at);
-            t.first = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)first, at) |
-                                ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(first >> 32), at) << 32));
-            return t.rows > 0;
-        }
-        before += __builtin_amdgcn_readlane(upto, 63);
     }
-    return false;
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    t.first = uniform(t.first);
+    return t.rows > 0;
 }
 
 }  // namespace nvfp4

@@ -45,6 +45,52 @@ __global__ __launch_bounds__(kThreads) void k_product_join(Product p, int splits
     product_out8<GATED, F32>(p, 1, 0, e, t, n, N, v, u);
 }
 
+// What each of `tiles` tiles of rows is. One thread a tile; a workgroup takes the matrices 256 at a time, sums their
+// tiles and lets those of its threads whose tile is among them search the sums.
+__global__ __launch_bounds__(kThreads) void k_product_map(ProductRows r, int size, int tiles) {
+    __shared__ int upto[kThreads], waves[kThreads / 64];
+    __shared__ int64_t from[kThreads], to[kThreads];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int tile = blockIdx.x * kThreads + threadIdx.x;
+    RowTile mine{0, 0, 0};
+    int before = 0;
+    for (int base = 0; base < r.batch; base += kThreads) {
+        int64_t lo = 0, hi = 0;
+        if (base + (int)threadIdx.x < r.batch) segment(r, base + threadIdx.x, lo, hi);
+        int sum = (int)((hi - lo + size - 1) / size);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += v;
+        }
+        if (lane == 63) waves[wave] = sum;
+        __syncthreads();
+        int all = before;
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w) {
+            if (w == wave) sum += all;
+            all += waves[w];
+        }
+        upto[threadIdx.x] = sum;
+        from[threadIdx.x] = lo;
+        to[threadIdx.x] = hi;
+        __syncthreads();
+        if (tile >= before && tile < all) {
+            int at = 0;                                  // the first whose sum is above the tile
+#pragma unroll
+            for (int d = kThreads / 2; d > 0; d >>= 1)
+                if (upto[at + d - 1] <= tile) at += d;
+            const int k = tile - (at ? upto[at - 1] : before);
+            mine.e = base + at;
+            mine.first = from[at] + (int64_t)k * size;
+            mine.rows = k >= 0 ? (int32_t)min((int64_t)size, to[at] - mine.first) : 0;
+        }
+        before = all;
+        __syncthreads();
+    }
+    if (tile < tiles) r.map[tile] = mine;
+}
+
 }  // namespace
 
 ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in, int32_t matrices,
@@ -54,33 +100,43 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
     const int64_t each = batch > 0 ? (tokens + batch - 1) / batch : 0;
     int64_t steps, tiles;
     // rows of a matrix (on average): up to 4 of them pass through the kernel that keeps them in registers (8192 x 28672:
-    // 39.2 us at 4 rows, 48.3 at 8; by tiles of 32 rows 46.1 and 45.7), up to 128 through tiles whose weights are
-    // converted where they are used (64 rows 60 us, 128 rows 101 us; by tiles through LDS 103 and 112)
+    // 39.2 us at 4 rows, 48.3 at 8; by tiles of 32 rows 46.1 and 45.7), up to 64 through tiles whose weights are
+    // converted where they are used (64 rows 57 us, 128 rows 106 us; by tiles through LDS 83 and 93)
     if (!backward && each <= 4) {
         plan.kernel = ProductKernel::kRows;
         plan.tile_rows = 4;
+        plan.tile_cols = 16;
         plan.splits = 1;
         plan.blocks = product_row_tiles(tokens, batch, 4) * ((out * matrices + 15) / 16);
         return plan;
     }
-    if (!backward && !f32 && in % 64 == 0 && each <= 128) {
+    if (!backward && !f32 && in % 64 == 0 && each <= 64) {
         plan.kernel = ProductKernel::kMid;
-        plan.tile_rows = each <= 32 ? 32 : each <= 64 ? 64 : 128;
+        plan.tile_rows = each <= 32 ? 32 : 64;
+        plan.tile_cols = 128;
         steps = (K + 127) / 128;
         tiles = product_row_tiles(tokens, batch, plan.tile_rows) * ((N * matrices + 127) / 128);
     } else {
         plan.kernel = ProductKernel::kTiles;
-        plan.tile_rows = 128;
-        steps = (K + 63) / 64 * (f32 ? 3 : 1) * (backward ? matrices : 1);
-        tiles = product_row_tiles(tokens, batch, 128) * ((N * (backward ? 1 : matrices) + 127) / 128);
+        steps = (K + 127) / 128 * 2 * (f32 ? 3 : 1) * (backward ? matrices : 1);
+        const int64_t cols = N * (backward ? 1 : matrices);
+        // tiles of 256 x 256 where they have work of 32 steps a compute unit at least (512 rows by 8192 x 8192 89 us, by
+        // tiles of 128 x 128 96; 1024 by 4096 x 4096 63 and 56; 4096 by 4096 x 14336 400 and 560)
+        const int64_t big = product_tile_rows(tokens, batch, 256) * ((cols + 255) / 256);
+        const int side = each >= 256 && big * steps >= 256 * 32 ? 256 : 128;
+        plan.tile_rows = plan.tile_cols = side;
+        tiles = side == 256 ? big : product_tile_rows(tokens, batch, 128) * ((cols + 127) / 128);
     }
     // shares: about two workgroups a compute unit, of at least 4 steps each (64 rows by 8192 x 28672 in 8 shares 59.7 us,
     // in 4 69.2, in 12 64.0)
-    int64_t splits = tiles > 0 ? 512 / tiles : 1;
-    if (splits > steps / 4) splits = steps / 4;
+    const int64_t unit = plan.kernel == ProductKernel::kTiles ? 4 : 1;
+    const int64_t want = plan.kernel == ProductKernel::kTiles && plan.tile_rows == 256 ? 256 : 512;
+    int64_t splits = tiles > 0 ? want / tiles : 1;
+    if (splits > steps / (2 * unit)) splits = steps / (2 * unit);
     if (splits > 32) splits = 32;
     if (splits < 1) splits = 1;
-    splits = (steps + (steps + splits - 1) / splits - 1) / ((steps + splits - 1) / splits);     // none empty
+    const int64_t share = ((steps + splits - 1) / splits + unit - 1) / unit * unit;
+    splits = (steps + share - 1) / share;                // none empty
     plan.splits = (int32_t)splits;
     plan.blocks = tiles * splits;
     return plan;
@@ -91,6 +147,10 @@ size_t product_partial_bytes(const ProductPlan& plan, int64_t tokens, int64_t ou
     if (plan.splits <= 1) return 0;
     const int64_t N = backward ? in : out;
     return (size_t)(plan.splits * tokens * ((N + 7) / 8 * 8) * (backward ? 1 : matrices)) * 4;
+}
+
+size_t product_map_bytes(const ProductPlan& plan, int64_t tokens, int64_t batch) {
+    return batch > kMapped ? (size_t)product_tile_rows(tokens, batch, plan.tile_rows) * sizeof(RowTile) : 0;
 }
 
 hipError_t launch_product(const Product& given, hipStream_t stream) {
@@ -107,7 +167,12 @@ hipError_t launch_product(const Product& given, hipStream_t stream) {
     bool fits = plan.kernel != ProductKernel::kRows || p.a[0].ld < (int64_t)1 << 24;
     for (int m = 0; plan.kernel == ProductKernel::kMid && m < p.matrices; ++m)
         fits = fits && at(p.w[m].packed, 16) && at(p.w[m].scales, 4) && p.w[m].stride % 64 == 0;
-    if (!fits) plan = ProductPlan{ProductKernel::kTiles, 128, 1, 0};
+    if (!fits) plan = ProductPlan{ProductKernel::kTiles, 128, 128, 1, 0};   // no smaller tiles: no larger map
+    if (p.rows.batch > kMapped) {
+        const int tiles = (int)product_tile_rows(p.rows.tokens, p.rows.batch, plan.tile_rows);   // all that a grid has
+        hipLaunchKernelGGL(k_product_map, dim3((uint32_t)((tiles + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                           stream, p.rows, plan.tile_rows, tiles);
+    }
     if (plan.kernel == ProductKernel::kRows) {
         launch_product_rows(p, stream);
         return hipGetLastError();

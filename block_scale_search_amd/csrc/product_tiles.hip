@@ -10,7 +10,6 @@
 // both values of an output are in the same lane.
 #include <hip/hip_runtime.h>
 
-#include <stdlib.h>
 #include <type_traits>
 
 #include "internal.h"
@@ -34,11 +33,15 @@ struct Shape {
 // Piece c (8 values) of LDS row r sits at c ^ swizzle(r).
 __device__ __forceinline__ int swizzle(int r) { return (r ^ (r >> 3)) & 7; }
 
-// A thread's codes of one step. Forward: 32 columns of one row, two scale bytes. Backward: 8 columns of
-// four rows, their scale bytes.
+// A thread's codes. Forward, of two steps: 32 columns of each, two scale bytes of each. Backward, of one step: 8
+// columns of four rows, their scale bytes.
+template <bool BACKWARD>
 struct Raw {
-    u32x4 code;
-    uint32_t scale[4];
+    uint32_t code[2][4], scale[2][2];
+};
+template <>
+struct Raw<true> {
+    uint32_t code[4], scale[4];
 };
 
 template <typename F>
@@ -65,11 +68,20 @@ struct Cursor {
     }
 };
 
-// Workgroup -> tile. Workgroups go to the 8 XCDs in turn: XCD x takes a run of tiles, and a run walks down 4 row tiles
-// before the next column tile, so that the 32 workgroups on an XCD read 4 row tiles and 8 column tiles together.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t blocks, uint32_t nm, uint32_t nn, int& tm, int& tn) {
-    const uint32_t xcd = id & 7, rest = blocks & 7;
-    const uint32_t q = xcd * (blocks >> 3) + min(xcd, rest) + (id >> 3);
+// Workgroup -> tile. Workgroups go to the 8 XCDs in turn. One matrix: XCD x takes a run of tiles, and a run walks down 4
+// row tiles before the next column tile, so that the 32 workgroups on an XCD read 4 row tiles and 8 column tiles together.
+// Several: how many row tiles there are is not known here, and rows of different matrices share nothing but their own
+// column tiles: XCD x takes every eighth row tile (with runs, 2048 x 768 by 128 rows each of 128 matrices left half
+// of the XCDs without work, 165 us).
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t nm, uint32_t nn, bool several, int& tm, int& tn) {
+    const uint32_t xcd = id & 7, j = id >> 3;
+    if (several) {
+        tm = (int)(j / nn * 8 + xcd);
+        tn = (int)(j % nn);
+        return;
+    }
+    const uint32_t blocks = nm * nn, rest = blocks & 7;
+    const uint32_t q = xcd * (blocks >> 3) + min(xcd, rest) + j;
     const uint32_t group = q / (4 * nn), l = q - group * 4 * nn;
     const uint32_t high = min(4u, nm - 4 * group);
     tn = (int)(l / high);
@@ -90,18 +102,16 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     const uint32_t of = blockIdx.x / (uint32_t)splits;
     const int split = (int)(blockIdx.x - of * (uint32_t)splits);
     int tile, tn;
-    tile_of(of, (uint32_t)nm * (uint32_t)nn, (uint32_t)nm, (uint32_t)nn, tile, tn);
+    tile_of(of, (uint32_t)nm, (uint32_t)nn, p.rows.batch > 1, tile, tn);
     RowTile rows;
     if (!find_rows(p.rows, tile, BM, rows)) return;
-    rows.e = __builtin_amdgcn_readfirstlane(rows.e);
-    rows.first = uniform(rows.first);
 
     constexpr int kCols = MODE == kGated ? BN / 2 : BN;            // output columns of a tile
     const int64_t n0 = (int64_t)tn * kCols;
     const int64_t N = MODE == kBackward ? p.in : p.out;
     const int K = (int)(MODE == kBackward ? p.out : p.in);
     const int k_pad = (K + 7) & ~7;
-    const int nk = (K + BK - 1) / BK;
+    const int nk = (K + 2 * BK - 1) / (2 * BK) * 2;      // steps go in pairs: the last one may be empty
     const int matrices = MODE == kBackward ? p.matrices : 1;
     const int begin = split * each, steps = min(each, nk * p.planes * matrices - begin);
     const int to_switch = nk * p.planes - begin;         // the step at which the second matrix begins
@@ -124,8 +134,9 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     const auto source = [&](const Cursor& c) {
         // pieces past the edge read the row's last: they meet weights of zero
         const uint16_t* base = MODE == kBackward && c.m ? a1 : a0;
-        base += c.plane * p.plane + c.kt * BK;
-        const int last = (k_pad - c.kt * BK) * 2 - 16;
+        const int kt = min(c.kt, (K - 1) / BK);
+        base += c.plane * p.plane + kt * BK;
+        const int last = (k_pad - kt * BK) * 2 - 16;
         Source s;
         s.p = reinterpret_cast<const uint16_t*>(uniform(reinterpret_cast<int64_t>(base)));
 #pragma unroll
@@ -136,58 +147,75 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         copy16_unseen(from.p, xrow[r] + from.at[r % kPieces], &lds_a[buf][(S::kThreads * r + 64 * wave) >> 3][0]);
     };
 
-    // forward: row b_row of lds_b, half b_half of its 64 values
-    const int b_row = tid >> 1, b_half = tid & 1;
-    // backward: columns 8 b_block .. + 7, values 8 b_octet + 4 b_half .. + 3
-    const int b_block = (tid >> 1) % (BN / 8), b_octet = (tid >> 1) / (BN / 8);
-    uint32_t b_code, b_scale;                            // of the thread's first code: bytes from the windows' start
+    // forward: row b_row of lds_b, half b_half of its 64 values. The codes of two steps are loaded together, 64
+    // bytes of a row by four lanes (32 bytes by two cost 8% of the whole): a lane loads a quarter of row lane / 4 and
+    // of the row 16 behind, and lanes 2 apart then exchange so that each has half a row of either step.
+    const bool b_high = lane & 2;
+    const int b_row = 32 * wave + (lane >> 2) + (b_high ? 16 : 0), b_half = lane & 1;
+    // backward: columns 8 b_block .. + 7, values 8 b_octet + 4 b_quad .. + 3
+    const int b_block = (tid >> 1) % (BN / 8), b_octet = (tid >> 1) / (BN / 8), b_quad = tid & 1;
+    uint32_t b_code[2], b_scale[2];                      // of the thread's first codes: bytes from the windows' start
     const uint8_t *codes, *scales;                       // forward: from row n0 (of the wave's matrix)
     if constexpr (MODE == kBackward) {
-        const uint32_t at = (uint32_t)(b_octet * 8 + b_half * 4) * (uint32_t)N + (uint32_t)min(n0 + b_block * 8, N - 8);
-        b_code = at / 2;
-        b_scale = at / 16;
+        const uint32_t at = (uint32_t)(b_octet * 8 + b_quad * 4) * (uint32_t)N + (uint32_t)min(n0 + b_block * 8, N - 8);
+        b_code[0] = at / 2;
+        b_scale[0] = at / 16;
     } else {
-        const int second = MODE == kGated ? wave & 1 : 0;              // a wave's 32 rows are of one matrix
-        const int c32 = MODE == kGated ? (b_row >> 6) * 32 + (b_row & 31) : b_row;
-        const ProductMatrix& w = p.w[second];
+        const ProductMatrix& w = p.w[MODE == kGated ? wave & 1 : 0];   // a wave's 32 rows are of one matrix
         const int64_t at = rows.e * w.stride + n0 * K;
         codes = w.packed + at / 2;
         scales = w.scales + at / 16;
-        b_scale = (uint32_t)(min(n0 + c32, N - 1) - n0) * (uint32_t)(K / 16) + 2 * b_half;
-        b_code = b_scale * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c32 = (MODE == kGated ? (wave >> 1) * 32 : wave * 32) + (lane >> 2) + 16 * h;
+            b_scale[h] = (uint32_t)(min(n0 + c32, N - 1) - n0) * (uint32_t)(K / 16) + 2 * (lane & 3);
+            b_code[h] = b_scale[h] * 8;
+        }
     }
-    const auto load_b = [&](Raw& raw, const Cursor& c, int step) {
+    const auto load_b = [&](Raw<MODE == kBackward>& raw, const Cursor& c, int step) {
         const int left = K - c.kt * BK;                  // of the reduction
         const uint32_t reach = step < steps ? kReach : 0;              // no codes past the last step
         if constexpr (MODE == kBackward) {
             const ProductMatrix& w = p.w[c.m];
             const int64_t at = rows.e * w.stride + (int64_t)c.kt * BK * N;
             const __amdgpu_buffer_rsrc_t from = window(w.packed + at / 2, reach), bytes = window(w.scales + at / 16, reach);
-            const int mine = left - (b_octet * 8 + b_half * 4);
+            const int mine = left - (b_octet * 8 + b_quad * 4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {                // N / 2 and N / 16 are whole
-                raw.code[r] = load4(from, offset_if(r < mine, b_code), (uint32_t)r * (uint32_t)(N / 2));
-                raw.scale[r] = load1(bytes, offset_if(r < mine, b_scale), (uint32_t)r * (uint32_t)(N / 16));
+                raw.code[r] = load4(from, offset_if(r < mine, b_code[0]), (uint32_t)r * (uint32_t)(N / 2));
+                raw.scale[r] = load1(bytes, offset_if(r < mine, b_scale[0]), (uint32_t)r * (uint32_t)(N / 16));
             }
         } else {
             const __amdgpu_buffer_rsrc_t from = window(codes, reach), bytes = window(scales, reach);
             const uint32_t k = (uint32_t)c.kt * (BK / 16);
-            const bool in = b_half * 32 < left;
-            if constexpr (WHOLE) {
-                raw.code = load16(from, offset_if(in, b_code), k * 8);
-                raw.scale[0] = load2(bytes, offset_if(in, b_scale), k);
-            } else {
-                const bool in2 = b_half * 32 + 16 < left;
-                const u32x2 lo = load8(from, offset_if(in, b_code), k * 8), hi = load8(from, offset_if(in2, b_code + 8), k * 8);
-                raw.code = u32x4{lo[0], lo[1], hi[0], hi[1]};
-                raw.scale[0] = load1(bytes, offset_if(in, b_scale), k);
-                raw.scale[1] = load1(bytes, offset_if(in2, b_scale + 1), k);
+            const bool in = (lane & 3) * 32 < left, in2 = (lane & 3) * 32 + 16 < left;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 w;
+                if constexpr (WHOLE) {
+                    w = load16(from, offset_if(in, b_code[h]), k * 8);
+                    raw.scale[h][0] = load2(bytes, offset_if(in, b_scale[h]), k);
+                } else {
+                    const u32x2 lo = load8(from, offset_if(in, b_code[h]), k * 8);
+                    const u32x2 hi = load8(from, offset_if(in2, b_code[h] + 8), k * 8);
+                    w = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                    raw.scale[h][0] = load1(bytes, offset_if(in, b_scale[h]), k);
+                    raw.scale[h][1] = load1(bytes, offset_if(in2, b_scale[h] + 1), k);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) raw.code[h][j] = w[j];
             }
         }
     };
-    // a quarter of a thread's weights, converted and written: piece 0 .. 3
-    const auto store_b = [&](int buf, const Raw& raw, auto which) {
-        constexpr int I = decltype(which)::value;
+    const auto exchange = [&](uint32_t& a, uint32_t& b) {
+        const uint32_t got = swap_pairs(b_high ? a : b);
+        a = b_high ? got : a;
+        b = b_high ? b : got;
+    };
+    // a quarter of a thread's weights of a step, converted and written: piece 0 .. 3. Forward, of the even or odd step of
+    // the two; the even step's come first and make the exchange.
+    const auto store_b = [&](int buf, Raw<MODE == kBackward>& raw, auto odd, auto which) {
+        constexpr int I = decltype(which)::value, ODD = decltype(odd)::value;
         if constexpr (MODE == kBackward) {
             float x[4][2];
 #pragma unroll
@@ -195,14 +223,19 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = b_block * 8 + 2 * I + j;
-                *reinterpret_cast<u32x2*>(&lds_b[buf][row][(b_octet ^ swizzle(row)) * 8 + b_half * 4]) =
+                *reinterpret_cast<u32x2*>(&lds_b[buf][row][(b_octet ^ swizzle(row)) * 8 + b_quad * 4]) =
                     u32x2{bf16_pair(x[0][j], x[1][j]), bf16_pair(x[2][j], x[3][j])};
             }
         } else {
-            const float s = I < 2 ? scale_value<0>(raw.scale[0]) : WHOLE ? scale_value<1>(raw.scale[0])
-                                                                         : scale_value<0>(raw.scale[1]);
+            if constexpr (ODD == 0) {
+                exchange(raw.code[0][I], raw.code[1][I]);
+                if constexpr (I == 0) exchange(raw.scale[0][0], raw.scale[1][0]);
+                if constexpr (!WHOLE && I == 2) exchange(raw.scale[0][1], raw.scale[1][1]);
+            }
+            const float s = I < 2 ? scale_value<0>(raw.scale[ODD][0]) : WHOLE ? scale_value<1>(raw.scale[ODD][0])
+                                                                              : scale_value<0>(raw.scale[ODD][1]);
             *reinterpret_cast<u32x4*>(&lds_b[buf][b_row][((b_half * 4 + I) ^ swizzle(b_row)) * 8]) =
-                dequant8(raw.code[I], s);
+                dequant8(raw.code[ODD][I], s);
         }
     };
 
@@ -254,36 +287,51 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     // Step s is multiplied from one half of LDS while step s + 1 is made in the other: its rows are copied, its
     // codes converted from registers, and the codes of the steps after it loaded. A step's one barrier stands before
     // its last slice, whose operands are in registers by then: behind it the first half is free, and the last
-    // slice's matrix instructions cover the reads of step s + 1's first operands. Steps go in pairs: past the last,
-    // copies are of the last step again and codes zeros (two ways out of the loop would cost registers).
+    // slice's matrix instructions cover the reads of step s + 1's first operands. Steps go in fours: past the last,
+    // copies are of the last step again and codes zeros (more ways out of the loop would cost registers).
     Cursor ca, cb;
     cb.at(begin, nk, p.planes);
     ca = cb;
-    Raw raw[2];                                          // of even and odd steps
-    const auto load_all = [&](int buf) {
+    constexpr int kAhead = MODE == kBackward ? 1 : 2;    // steps that one load of codes serves
+    Raw<MODE == kBackward> raw[2];
+    int loaded = 0;
+    const auto load_next = [&](Raw<MODE == kBackward>& r) {
+        load_b(r, cb, loaded);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) cb.next(++loaded < steps, nk, p.planes);
+    };
+    int copied = 0;
+    const auto source_next = [&]() {
         const Source from = source(ca);
+        ca.next(++copied < steps, nk, p.planes);
+        return from;
+    };
+    const auto load_all = [&](int buf) {
+        const Source from = source_next();
 #pragma unroll
         for (int r = 0; r < S::kLoads; ++r) load_a(buf, from, r);
     };
-    load_b(raw[0], cb, 0);
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
+    load_next(raw[0]);
     load_all(0);
-    unroll4([&](auto i) { store_b(0, raw[0], i); });
-    cb.next(1 < steps, nk, p.planes);
-    ca.next(1 < steps, nk, p.planes);
-    load_b(raw[1], cb, 1);
+    load_next(raw[1]);
     load_all(1);
-    cb.next(2 < steps, nk, p.planes);
-    ca.next(2 < steps, nk, p.planes);
-    load_b(raw[0], cb, 2);
+    unroll4([&](auto i) { store_b(0, raw[0], even, i); });
+    if constexpr (MODE == kBackward) load_next(raw[0]);
     wait_copies<0>();
     barrier();
     Frag f[2];
     read(f[0], 0, 0);
-    store_b(1, raw[1], std::integral_constant<int, 0>{});
+    store_b(1, MODE == kBackward ? raw[1] : raw[0], odd, even);
     __builtin_amdgcn_sched_barrier(0);
-    // next: the codes of step s + 1, after: of step s + 2
-    const auto step = [&](int s, auto buffer, Raw& next, Raw& after) {
-        constexpr int buf = decltype(buffer)::value;
+    const auto step = [&](int s, auto which) {
+        constexpr int J = decltype(which)::value, buf = J & 1;
+        // where step s + 1's codes are, and step s + 2's
+        constexpr int X = MODE == kBackward ? (J + 1) & 1 : ((J + 1) >> 1) & 1;
+        constexpr int Y = MODE == kBackward ? J & 1 : ((J + 2) >> 1) & 1;
+        const std::integral_constant<int, (J + 1) & 1> x_odd;
+        const std::integral_constant<int, J & 1> y_odd;
         if constexpr (MODE == kBackward) {
             if (s == to_switch && s > 0 && s < steps) {  // the second matrix's sums carry its S
                 const float r = p.w[0].S[rows.e] / p.w[1].S[rows.e];
@@ -297,19 +345,17 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         }
         read(f[1], buf, 1);
         multiply(f[0]);
-        store_b(buf ^ 1, next, std::integral_constant<int, 1>{});
+        store_b(buf ^ 1, raw[X], x_odd, std::integral_constant<int, 1>{});
         interleave();
         read(f[0], buf, 2);
         multiply(f[1]);
-        store_b(buf ^ 1, next, std::integral_constant<int, 2>{});
+        store_b(buf ^ 1, raw[X], x_odd, std::integral_constant<int, 2>{});
         interleave();
         read(f[1], buf, 3);
         multiply(f[0]);
-        store_b(buf ^ 1, next, std::integral_constant<int, 3>{});
+        store_b(buf ^ 1, raw[X], x_odd, std::integral_constant<int, 3>{});
         interleave();
-        const Source from = source(ca);
-        ca.next(s + 3 < steps, nk, p.planes);
-        cb.next(s + 3 < steps, nk, p.planes);
+        const Source from = source_next();
         wait_copies<0>();                                // step s + 1's rows and step s + 2's codes
         barrier();
         // the last slice: its matrix instructions in TM groups, with the copies between
@@ -321,14 +367,19 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
                 acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[1].a[a], f[1].b[b], acc[a][b], 0, 0, 0);
 #pragma unroll
             for (int r = a * S::kLoads / TM; r < (a + 1) * S::kLoads / TM; ++r) load_a(buf, from, r);
-            if (a == TM / 2 - 1) load_b(next, cb, s + 3);
-            if (a == TM - 1) store_b(buf, after, std::integral_constant<int, 0>{});
+            if (a == TM - 1) {
+                // raw[X] has been used up, forward every other step
+                if constexpr (MODE == kBackward || J % 2 == 0) load_next(raw[X]);
+                store_b(buf, raw[Y], y_odd, even);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    for (int s = 0; s < steps; s += 2) {
-        step(s, std::integral_constant<int, 0>{}, raw[1], raw[0]);
-        step(s + 1, std::integral_constant<int, 1>{}, raw[0], raw[1]);
+    for (int s = 0; s < steps; s += 4) {
+        step(s, std::integral_constant<int, 0>{});
+        step(s + 1, std::integral_constant<int, 1>{});
+        step(s + 2, std::integral_constant<int, 2>{});
+        step(s + 3, std::integral_constant<int, 3>{});
     }
     wait_copies<0>();
     barrier();
@@ -377,9 +428,9 @@ template <typename S, int MODE>
 void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
     const int64_t N = MODE == kBackward ? p.in : p.out, K = MODE == kBackward ? p.out : p.in;
     const int64_t cols = MODE == kGated ? S::BN / 2 : S::BN, nn = (N + cols - 1) / cols;
-    const int64_t steps = (K + BK - 1) / BK * p.planes * (MODE == kBackward ? p.matrices : 1);
-    const int64_t each = (steps + plan.splits - 1) / plan.splits;
-    const int64_t nm = product_row_tiles(p.rows.tokens, p.rows.batch, S::BM);
+    const int64_t steps = (K + 2 * BK - 1) / (2 * BK) * 2 * p.planes * (MODE == kBackward ? p.matrices : 1);
+    const int64_t each = ((steps + plan.splits - 1) / plan.splits + 3) / 4 * 4;
+    const int64_t nm = product_tile_rows(p.rows.tokens, p.rows.batch, S::BM);
     const dim3 grid((uint32_t)(nm * nn * plan.splits)), threads(S::kThreads);
     const bool whole = MODE == kBackward || p.in % 32 == 0;
     if (p.f32 && whole)
@@ -398,18 +449,18 @@ void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
     }
 }
 
+template <typename S>
+void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
+    if (p.backward) launch<S, kBackward>(p, plan, stream);
+    else if (p.matrices == 2) launch<S, kGated>(p, plan, stream);
+    else launch<S, kLinear>(p, plan, stream);
+}
+
 }  // namespace
 
 void launch_product_tiles(const Product& p, const ProductPlan& plan, hipStream_t stream) {
-    if (getenv("BIG")) {
-        if (p.backward) launch<Big, kBackward>(p, plan, stream);
-        else if (p.matrices == 2) launch<Big, kGated>(p, plan, stream);
-        else launch<Big, kLinear>(p, plan, stream);
-        return;
-    }
-    if (p.backward) launch<Small, kBackward>(p, plan, stream);
-    else if (p.matrices == 2) launch<Small, kGated>(p, plan, stream);
-    else launch<Small, kLinear>(p, plan, stream);
+    if (plan.tile_cols == 128) launch<Small>(p, plan, stream);
+    else launch<Big>(p, plan, stream);
 }
 
 }  // namespace nvfp4

@@ -69,6 +69,29 @@ def test_gradient_is_the_rounded_exact_sum(nv, T, out, inp, dtype):
     same(r["dX"], product(dg, w, [T], False)[0] + product(du, v, [T], False)[0], dtype, "dX of two")
 
 
+# sizes that have enough tiles of 256 x 256 for them, with edges inside; reductions of an odd number of steps
+LARGE = [(1030, 8200, 4112), (300, 4104, 16416), (777, 20008, 1040)]
+
+
+@DTYPES
+@pytest.mark.parametrize("T, out, inp", LARGE)
+def test_large_sums_are_rounded_once(nv, T, out, inp, dtype):
+    """Forward, gated and backward by the largest tiles (the reference in 64 bits on the GPU: whole numbers)."""
+    w, v = Weights(1, out, inp, 1, whole=True), Weights(1, out, inp, 2, whole=True)
+    x, d = rows((T, inp), dtype, 3, whole=True).to(DEV), rows((T, out), dtype, 4, whole=True).to(DEV)
+    g, u = rows((T, out), dtype, 5, whole=True).to(DEV), rows((T, out), dtype, 6, whole=True).to(DEV)
+    wv, vv = w.values[0].to(DEV), v.values[0].to(DEV)
+    m, n = w.matrix(nv), v.matrix(nv)
+    same(nv.linear(m, x, residual=g), (x.double() @ wv.t() + g.double()).cpu(), dtype, "Y")
+    h, gate, up = nv.gated(m, n, x, activation=nv.ACT_RELU, with_pre=True)
+    same(gate, (x.double() @ wv.t()).cpu(), dtype, "G")
+    same(up, (x.double() @ vv.t()).cpu(), dtype, "U")
+    same(nv.linear_backward(m, d)["dX"], (d.double() @ wv).cpu(), dtype, "dX")
+    r = nv.gated_backward(m, n, d, g, u, activation=nv.ACT_RELU)
+    dg, du = d.double() * u.double() * (g > 0), d.double() * g.double().clamp(min=0)
+    same(r["dX"], (dg @ wv + du @ vv).cpu(), dtype, "dX of two")
+
+
 @DTYPES
 @pytest.mark.parametrize("name", ACTS)
 @pytest.mark.parametrize("T, out, inp", [(1, 130, 272), (19, 70, 528), (150, 200, 336)])
