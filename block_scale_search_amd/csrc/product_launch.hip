@@ -101,7 +101,9 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
     int64_t steps, tiles;
     // rows of a matrix (on average): up to 4 of them pass through the kernel that keeps them in registers (8192 x 28672:
     // 39.2 us at 4 rows, 48.3 at 8; by tiles of 32 rows 46.1 and 45.7), up to 64 through tiles whose weights are
-    // converted where they are used (64 rows 57 us, 128 rows 106 us; by tiles through LDS 83 and 93)
+    // converted where they are used (64 rows 57 us, 128 rows 106 us; by tiles through LDS 83 and 93; several
+    // matrices leave part of a tile empty each: 128 rows on average of 128 matrices of 2048 x 768 118 us, by tiles of 128
+    // rows 150)
     if (!backward && each <= 4) {
         plan.kernel = ProductKernel::kRows;
         plan.tile_rows = 4;
@@ -110,7 +112,7 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
         plan.blocks = product_row_tiles(tokens, batch, 4) * ((out * matrices + 15) / 16);
         return plan;
     }
-    if (!backward && !f32 && in % 64 == 0 && each <= 64) {
+    if (!backward && !f32 && in % 64 == 0 && each <= (batch > 1 ? 128 : 64)) {
         plan.kernel = ProductKernel::kMid;
         plan.tile_rows = each <= 32 ? 32 : 64;
         plan.tile_cols = 128;

@@ -96,30 +96,43 @@ __global__ __launch_bounds__(kThreads) void k_product_mid(Product p, int nn, int
     int at = 0;
     for (int s = first; s < last; ++s) {
         // the copies of step s are done; those of the steps after it may be under way
-        if (STAGES == 3 && s + 1 < last) wait_copies<kLoads + 3>();
+        if (STAGES >= 4 && s + 2 < last) wait_copies<2 * (kLoads + 3)>();
+        else if (STAGES >= 3 && s + 1 < last) wait_copies<kLoads + 3>();
         else wait_copies<0>();
         barrier();
         const Stage<BM>& st = stage[at];
         if (s + STAGES - 1 < last) copy(stage[at == 0 ? STAGES - 1 : at - 1], s + STAGES - 1);
         at = at + 1 == STAGES ? 0 : at + 1;
+        // 8 slices of 16: half h's codes are 64 h + 32 kg .. + 31. Operands are read kAhead slices before their use.
+        constexpr int kAhead = 4;
         const int row = 32 * wave + n32, left = K - s * kStep;
+        u32x4 code[2];
+        uint32_t sc[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            // half h: codes 64 h + 32 kg .. + 31
-            const u32x4 code = *reinterpret_cast<const u32x4*>(&st.code[row][code_piece(n32, 2 * h + kg) * 16]);
-            uint32_t sc = *reinterpret_cast<const uint16_t*>(&st.scale[row][4 * h + 2 * kg]);
-            sc = 64 * h + 32 * kg < left ? sc : 0;
-            const float s0 = scale_value<0>(sc), s1 = scale_value<1>(sc);
+            code[h] = *reinterpret_cast<const u32x4*>(&st.code[row][code_piece(n32, 2 * h + kg) * 16]);
+            sc[h] = *reinterpret_cast<const uint16_t*>(&st.scale[row][4 * h + 2 * kg]);
+        }
+        bf16x8 x[8][TM];
+        const auto read = [&](int z) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const u32x4 w = dequant8(code[j], j < 2 ? s0 : s1);
-#pragma unroll
-                for (int a = 0; a < TM; ++a) {
-                    const int r = 32 * a + n32;
-                    const bf16x8 x = *reinterpret_cast<const bf16x8*>(&st.a[r][a_piece(r, 8 * h + 4 * kg + j) * 8]);
-                    acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, w), acc[a], 0, 0, 0);
-                }
+            for (int a = 0; a < TM; ++a) {
+                const int r = 32 * a + n32;
+                x[z][a] = *reinterpret_cast<const bf16x8*>(&st.a[r][a_piece(r, 8 * (z >> 2) + 4 * kg + (z & 3)) * 8]);
             }
+        };
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z) read(z);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) sc[h] = 64 * h + 32 * kg < left ? sc[h] : 0;
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+            const float e = (z & 2) ? scale_value<1>(sc[z >> 2]) : scale_value<0>(sc[z >> 2]);
+            const u32x4 w = dequant8(code[z >> 2][z & 3], e);
+            if (z + kAhead < 8) read(z + kAhead);
+#pragma unroll
+            for (int a = 0; a < TM; ++a)
+                acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[z][a], __builtin_bit_cast(bf16x8, w), acc[a], 0, 0, 0);
         }
     }
 

@@ -105,12 +105,13 @@ bool wide(const void* p, int64_t ld, bool f32) {
 }
 
 // Bias gradients. A workgroup sums 64 columns over a share of a matrix's rows, each of its four waves every
-// fourth row; the shares' sums are added in binary64 by a second kernel. The order is fixed.
-constexpr int kShareRows = 256;      // rows of a share at least, where there are few matrices
+// fourth row, eight rows' loads at a time; the shares' sums are added in binary64 by a second kernel. The order is fixed.
+constexpr int kShareRows = 32;       // rows of a share at least
 int64_t bias_shares(int64_t tokens, int64_t batch, int64_t cols) {
     const int64_t groups = batch * ((cols + 63) / 64);
-    const int64_t want = (1024 + groups - 1) / groups, most = (tokens + kShareRows - 1) / kShareRows;
-    const int64_t n = want < most ? want : most;
+    const int64_t want = (2048 + groups - 1) / groups, most = (tokens / batch + kShareRows - 1) / kShareRows;
+    int64_t n = want < most ? want : most;
+    if (n > 64) n = 64;
     return n < 1 ? 1 : n;
 }
 
@@ -126,16 +127,20 @@ __global__ __launch_bounds__(kThreads) void k_product_bias(ProductSlopes p, int 
     const int64_t last = min(first + each, hi);
     float sum = 0.0f;
     if (n < p.cols) {
-        for (int64_t t0 = first + wave; t0 < last; t0 += 64) {        // 16 rows summed by themselves
+        for (int64_t t0 = first + wave; t0 < last; t0 += 32) {        // 8 rows summed by themselves
+            float d[8], z[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int64_t t = min(t0 + 4 * k, last - 1);
+                d[k] = load_value(p.dY, t * p.lddy + n, F32);
+                z[k] = p.Z ? load_value(p.Z, t * p.ldz + n, F32) : 0.0f;
+            }
             float part = 0.0f;
-#pragma unroll 4
-            for (int k = 0; k < 16; ++k) {
-                const int64_t t = t0 + 4 * k;
-                if (t < last) {
-                    float a, slope = 1.0f;
-                    if (p.Z) act_slope<F32>(p.act, load_value(p.Z, t * p.ldz + n, F32), a, slope);
-                    part += load_value(p.dY, t * p.lddy + n, F32) * slope;
-                }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float a, slope = 1.0f;
+                if (p.Z) act_slope<F32>(p.act, z[k], a, slope);
+                part += t0 + 4 * k < last ? d[k] * slope : 0.0f;
             }
             sum += part;
         }

@@ -33,15 +33,11 @@ struct Shape {
 // Piece c (8 values) of LDS row r sits at c ^ swizzle(r).
 __device__ __forceinline__ int swizzle(int r) { return (r ^ (r >> 3)) & 7; }
 
-// A thread's codes. Forward, of two steps: 32 columns of each, two scale bytes of each. Backward, of one step: 8
-// columns of four rows, their scale bytes.
-template <bool BACKWARD>
+// A thread's codes of two steps, as loaded and, once exchanged, by step. Forward: 32 columns, two scale bytes (in one
+// or two words). Backward: 8 columns of four rows, four scale bytes (as loaded in four words of the first row, then
+// packed in the first word of each).
 struct Raw {
-    uint32_t code[2][4], scale[2][2];
-};
-template <>
-struct Raw<true> {
-    uint32_t code[4], scale[4];
+    uint32_t code[2][4], scale[2][4];
 };
 
 template <typename F>
@@ -147,17 +143,21 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         copy16_unseen(from.p, xrow[r] + from.at[r % kPieces], &lds_a[buf][(S::kThreads * r + 64 * wave) >> 3][0]);
     };
 
-    // forward: row b_row of lds_b, half b_half of its 64 values. The codes of two steps are loaded together, 64
-    // bytes of a row by four lanes (32 bytes by two cost 8% of the whole): a lane loads a quarter of row lane / 4 and
-    // of the row 16 behind, and lanes 2 apart then exchange so that each has half a row of either step.
+    // The codes of two steps are loaded together and lanes two apart exchange half of theirs, so that each has its
+    // share of either step: half as many loads, of twice the length. (64 bytes of a row by four lanes instead of 32
+    // by two took 4 to 8% off the whole.)
     const bool b_high = lane & 2;
+    // forward: a lane loads a quarter of 128 columns of row lane / 4 of the wave's 32 and of the row 16 behind; it has
+    // half b_half of row b_row of lds_b
     const int b_row = 32 * wave + (lane >> 2) + (b_high ? 16 : 0), b_half = lane & 1;
-    // backward: columns 8 b_block .. + 7, values 8 b_octet + 4 b_quad .. + 3
-    const int b_block = (tid >> 1) % (BN / 8), b_octet = (tid >> 1) / (BN / 8), b_quad = tid & 1;
+    // backward: a lane loads 16 columns of 4 rows of one of the steps; it has columns 8 b_block .. + 7, values
+    // 8 b_octet + 4 b_quad .. + 3
+    const int b_block = (tid >> 2) % (BN / 16) * 2 + (b_high ? 1 : 0), b_octet = (tid >> 2) / (BN / 16), b_quad = tid & 1;
+    const int b_first = (b_high ? BK : 0) + b_octet * 8 + b_quad * 4;
     uint32_t b_code[2], b_scale[2];                      // of the thread's first codes: bytes from the windows' start
     const uint8_t *codes, *scales;                       // forward: from row n0 (of the wave's matrix)
     if constexpr (MODE == kBackward) {
-        const uint32_t at = (uint32_t)(b_octet * 8 + b_quad * 4) * (uint32_t)N + (uint32_t)min(n0 + b_block * 8, N - 8);
+        const uint32_t at = (uint32_t)b_first * (uint32_t)N + (uint32_t)min(n0 + (b_block >> 1) * 16, N - 16);
         b_code[0] = at / 2;
         b_scale[0] = at / 16;
     } else {
@@ -172,18 +172,20 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
             b_code[h] = b_scale[h] * 8;
         }
     }
-    const auto load_b = [&](Raw<MODE == kBackward>& raw, const Cursor& c, int step) {
+    const auto load_b = [&](Raw& raw, const Cursor& c, int step) {
         const int left = K - c.kt * BK;                  // of the reduction
         const uint32_t reach = step < steps ? kReach : 0;              // no codes past the last step
         if constexpr (MODE == kBackward) {
             const ProductMatrix& w = p.w[c.m];
             const int64_t at = rows.e * w.stride + (int64_t)c.kt * BK * N;
             const __amdgpu_buffer_rsrc_t from = window(w.packed + at / 2, reach), bytes = window(w.scales + at / 16, reach);
-            const int mine = left - (b_octet * 8 + b_quad * 4);
+            const int mine = left - b_first;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {                // N / 2 and N / 16 are whole
-                raw.code[r] = load4(from, offset_if(r < mine, b_code[0]), (uint32_t)r * (uint32_t)(N / 2));
-                raw.scale[r] = load1(bytes, offset_if(r < mine, b_scale[0]), (uint32_t)r * (uint32_t)(N / 16));
+                const u32x2 w2 = load8(from, offset_if(r < mine, b_code[0]), (uint32_t)r * (uint32_t)(N / 2));
+                raw.code[0][r] = w2[0];
+                raw.code[1][r] = w2[1];
+                raw.scale[0][r] = load1(bytes, offset_if(r < mine, b_scale[0]), (uint32_t)r * (uint32_t)(N / 16));
             }
         } else {
             const __amdgpu_buffer_rsrc_t from = window(codes, reach), bytes = window(scales, reach);
@@ -212,14 +214,24 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         a = b_high ? got : a;
         b = b_high ? b : got;
     };
-    // a quarter of a thread's weights of a step, converted and written: piece 0 .. 3. Forward, of the even or odd step of
-    // the two; the even step's come first and make the exchange.
-    const auto store_b = [&](int buf, Raw<MODE == kBackward>& raw, auto odd, auto which) {
+    // a quarter of a thread's weights of the even or odd step of two, converted and written: piece 0 .. 3; the even
+    // step's come first and make the exchange
+    const auto store_b = [&](int buf, Raw& raw, auto odd, auto which) {
         constexpr int I = decltype(which)::value, ODD = decltype(odd)::value;
         if constexpr (MODE == kBackward) {
+            if constexpr (ODD == 0 && I == 0) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) exchange(raw.code[0][r], raw.code[1][r]);
+                const uint32_t mine = raw.scale[0][0] | raw.scale[0][1] << 8 | raw.scale[0][2] << 16 | raw.scale[0][3] << 24;
+                const uint32_t other = swap_pairs(mine);
+                raw.scale[0][0] = b_high ? other : mine;
+                raw.scale[1][0] = b_high ? mine : other;
+            }
+            const uint32_t bytes = raw.scale[ODD][0];
+            const float s[4] = {scale_value<0>(bytes), scale_value<1>(bytes), scale_value<2>(bytes), scale_value<3>(bytes)};
             float x[4][2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) code_values<I>(raw.code[r], scale_value<0>(raw.scale[r]), x[r][0], x[r][1]);
+            for (int r = 0; r < 4; ++r) code_values<I>(raw.code[ODD][r], s[r], x[r][0], x[r][1]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = b_block * 8 + 2 * I + j;
@@ -292,13 +304,12 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     Cursor ca, cb;
     cb.at(begin, nk, p.planes);
     ca = cb;
-    constexpr int kAhead = MODE == kBackward ? 1 : 2;    // steps that one load of codes serves
-    Raw<MODE == kBackward> raw[2];
+    Raw raw[2];
     int loaded = 0;
-    const auto load_next = [&](Raw<MODE == kBackward>& r) {
+    const auto load_next = [&](Raw& r) {
         load_b(r, cb, loaded);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) cb.next(++loaded < steps, nk, p.planes);
+        cb.next(++loaded < steps, nk, p.planes);
+        cb.next(++loaded < steps, nk, p.planes);
     };
     int copied = 0;
     const auto source_next = [&]() {
@@ -318,18 +329,16 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     load_next(raw[1]);
     load_all(1);
     unroll4([&](auto i) { store_b(0, raw[0], even, i); });
-    if constexpr (MODE == kBackward) load_next(raw[0]);
     wait_copies<0>();
     barrier();
     Frag f[2];
     read(f[0], 0, 0);
-    store_b(1, MODE == kBackward ? raw[1] : raw[0], odd, even);
+    store_b(1, raw[0], odd, even);
     __builtin_amdgcn_sched_barrier(0);
     const auto step = [&](int s, auto which) {
         constexpr int J = decltype(which)::value, buf = J & 1;
         // where step s + 1's codes are, and step s + 2's
-        constexpr int X = MODE == kBackward ? (J + 1) & 1 : ((J + 1) >> 1) & 1;
-        constexpr int Y = MODE == kBackward ? J & 1 : ((J + 2) >> 1) & 1;
+        constexpr int X = ((J + 1) >> 1) & 1, Y = ((J + 2) >> 1) & 1;
         const std::integral_constant<int, (J + 1) & 1> x_odd;
         const std::integral_constant<int, J & 1> y_odd;
         if constexpr (MODE == kBackward) {
@@ -368,8 +377,7 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
 #pragma unroll
             for (int r = a * S::kLoads / TM; r < (a + 1) * S::kLoads / TM; ++r) load_a(buf, from, r);
             if (a == TM - 1) {
-                // raw[X] has been used up, forward every other step
-                if constexpr (MODE == kBackward || J % 2 == 0) load_next(raw[X]);
+                if constexpr (J % 2 == 0) load_next(raw[X]);           // it has been used up
                 store_b(buf, raw[Y], y_odd, even);
             }
             __builtin_amdgcn_sched_barrier(0);
