@@ -8,7 +8,7 @@
 namespace {
 
 constexpr int64_t kInt32 = (int64_t)1 << 31;
-constexpr int64_t kMaxSide = (int64_t)1 << 24;
+constexpr int64_t kMaxSide = (int64_t)1 << 22;     // 32-bit offsets inside a tile
 constexpr int64_t kMaxSpan = (int64_t)1 << 56;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -62,9 +62,9 @@ nvfp4_status check_call(int dtype, const nvfp4_matrix* w, const nvfp4_matrix* w2
     return NVFP4_OK;
 }
 
-// Rows [tokens, cols] of row stride ld; `to`: the bytes that rows are aligned to.
+// Rows [tokens, cols] of row stride ld; `to`: the bytes that rows are aligned to (16: a product reads them as they are).
 nvfp4_status check_rows(const void* p, int esz, int64_t tokens, int64_t cols, int64_t ld, int64_t to) {
-    if (ld < cols || !span_ok(tokens, ld)) return NVFP4_ERR_SHAPE;
+    if (ld < cols || !span_ok(tokens, ld) || (to == 16 && ld >= kMaxSide)) return NVFP4_ERR_SHAPE;
     if (p == nullptr) return NVFP4_ERR_NULL;
     if (!aligned(p, to) || (tokens > 1 && ld * esz % to != 0)) return NVFP4_ERR_ALIGN;
     return NVFP4_OK;
@@ -320,6 +320,7 @@ nvfp4_status nvfp4_gated_backward(const nvfp4_matrix* W_gate, const nvfp4_matrix
     if (st == NVFP4_OK) st = check_rows(dU, esz, tokens, out, lddu, to);
     if (st == NVFP4_OK) st = check_rows(dX, esz, tokens, W_gate->in, lddx, esz);
     if (st != NVFP4_OK) return st;
+    if (!s.parts && lddg != lddu) return NVFP4_ERR_SHAPE;
     st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::ProductSlopes g = {};

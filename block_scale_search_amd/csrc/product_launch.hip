@@ -163,10 +163,9 @@ hipError_t launch_product(const Product& given, hipStream_t stream) {
     p.wide = wide(p.y, p.ldy) && wide(p.pre[0], p.ldpre[0]) && wide(p.pre[1], p.ldpre[1]) &&
              wide(p.residual, p.ldr) && wide(p.bias, p.out);
     ProductPlan plan = product_plan(p.rows.tokens, p.rows.batch, p.out, p.in, p.matrices, p.backward, p.f32);
-    // the tile kernel asks for less: alignment beyond what codes and scale bytes need have, and rows close enough
-    // together for 32-bit offsets
+    // the tile kernel asks for less alignment than the copies of codes and scale bytes into LDS
     const auto at = [](const void* q, uintptr_t to) { return (reinterpret_cast<uintptr_t>(q) & (to - 1)) == 0; };
-    bool fits = plan.kernel != ProductKernel::kRows || p.a[0].ld < (int64_t)1 << 24;
+    bool fits = true;
     for (int m = 0; plan.kernel == ProductKernel::kMid && m < p.matrices; ++m)
         fits = fits && at(p.w[m].packed, 16) && at(p.w[m].scales, 4) && p.w[m].stride % 64 == 0;
     if (!fits) plan = ProductPlan{ProductKernel::kTiles, 128, 128, 1, 0};   // no smaller tiles: no larger map

@@ -108,6 +108,7 @@ bool wide(const void* p, int64_t ld, bool f32) {
 // fourth row, eight rows' loads at a time; the shares' sums are added in binary64 by a second kernel. The order is fixed.
 constexpr int kShareRows = 32;       // rows of a share at least
 int64_t bias_shares(int64_t tokens, int64_t batch, int64_t cols) {
+    if (batch < 1) return 1;
     const int64_t groups = batch * ((cols + 63) / 64);
     const int64_t want = (2048 + groups - 1) / groups, most = (tokens / batch + kShareRows - 1) / kShareRows;
     int64_t n = want < most ? want : most;

@@ -474,8 +474,9 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  * a NaN or an infinity has unspecified results in that row (rows, never others). A tensor of outputs may
  * not overlap any other tensor of the call, but Y may be the residual itself (same address, same stride).
  *
- * Requires in % 16 == 0, in >= 16, out >= 1 (a product with an empty matrix is refused), in and out < 2^24, out * in / 16 < 2^31,
- * tokens < 2^31, batch <= 65,535, packed 8-byte aligned, stride a multiple of 16. tokens == 0 is valid.
+ * Requires in % 16 == 0, in >= 16, out >= 1 (a product with an empty matrix is refused), in and out < 2^22, out * in / 16 < 2^31,
+ * tokens < 2^31, batch <= 65,535, packed 8-byte aligned, stride a multiple of 16; rows that a product reads 16
+ * bytes at a time (X, and where a call says so) have a stride < 2^22. tokens == 0 is valid.
  * Workspaces: 16-byte aligned, no initialisation needed, of at least the size that the query of the same
  * name gives for the same sizes (NULL is valid where that is 0).
  * ------------------------------------------------------------------------------------------- */
@@ -543,7 +544,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
 /* Gradients of nvfp4_gated:
  *   dG = dH * U * act'(G),  dU = dH * act(G),  dX = dG W_gate + dU W_up
  * dH, G, U, dG, dU  [tokens, out]; dX [tokens, in]. dG and dU enter the product as dtype holds them.
- * bf16 with out % 8 == 0: rows of dG and dU are 16-byte aligned. */
+ * bf16 with out % 8 == 0: rows of dG and dU are 16-byte aligned and lddg == lddu. */
 size_t nvfp4_gated_backward_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out,
                                            int64_t in);
 

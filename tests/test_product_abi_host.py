@@ -61,7 +61,7 @@ CALLS = [_linear, _gated, _linear_backward, _gated_backward]
 BAD_MATRICES = [
     (dict(out=0), "SHAPE"), (dict(out=-1), "SHAPE"), (dict(in_=0), "SHAPE"), (dict(in_=40), "SHAPE"),
     (dict(in_=-16), "SHAPE"), (dict(batch=-1), "SHAPE"), (dict(batch=65536), "SHAPE"),
-    (dict(out=1 << 31), "SHAPE"), (dict(in_=1 << 31), "SHAPE"), (dict(out=1 << 27, in_=256), "SHAPE"),
+    (dict(out=1 << 31), "SHAPE"), (dict(in_=1 << 22, out=1), "SHAPE"), (dict(in_=16, out=1 << 22), "SHAPE"), (dict(out=1 << 27, in_=256), "SHAPE"),
     (dict(batch=2, stride=40 * 64 - 16), "SHAPE"), (dict(batch=2, stride=BIG), "SHAPE"),
     (dict(packed=None), "NULL"), (dict(scales=None), "NULL"), (dict(S=None), "NULL"),
     (dict(packed=FAKE + 4), "ALIGN"), (dict(S=FAKE + 2), "ALIGN"), (dict(batch=2, stride=40 * 64 + 8), "ALIGN")]
@@ -80,7 +80,7 @@ def test_matrices(n, call):
     assert call(n, _matrix(n, batch=2, stride=4096)) == n.ERR_NULL               # a batch needs seg_offsets
     assert call(n, seg=FAKE + 4) == n.ERR_ALIGN
     # a grid beyond 2^31 workgroups
-    assert call(n, _matrix(n, out=1 << 24, in_=1024), tokens=(1 << 31) - 1) == n.ERR_SHAPE
+    assert call(n, _matrix(n, out=1 << 21, in_=8192), tokens=(1 << 31) - 1) == n.ERR_SHAPE
     # nothing to do
     assert call(n, _matrix(n, batch=0)) == n.ERR_NULL
     assert call(n, _matrix(n, batch=0), seg=FAKE) == n.OK
@@ -118,6 +118,8 @@ def test_optional_row_tensors(n):
     assert _linear(n, dt=0, ldx=66) == n.ERR_ALIGN
     assert _linear_backward(n, act=0, lddy=44) == n.ERR_ALIGN
     assert _linear_backward(n, lddz=44) == n.ERR_ALIGN
+    assert _gated_backward(n, lddg=48) == n.ERR_SHAPE                            # dG and dU unlike
+    assert _linear(n, ldx=1 << 22) == n.ERR_SHAPE
     assert _gated_backward(n, lddg=44) == n.ERR_ALIGN and _gated_backward(n, dU=FAKE + 2) == n.ERR_ALIGN
 
 
@@ -133,6 +135,7 @@ def test_workspaces(n):
     assert back(bf16, 100, 1, 41, 64, False) >= 2 * 100 * 48
     assert back(bf16, 100, 3, 40, 64, True) >= 4 * 3 * 40
     assert n.nvfp4_gated_backward_workspace_size(f32, 100, 1, 40, 64) >= 2 * 3 * 2 * 100 * 40
+    assert back(bf16, 100, 0, 40, 64, True) >= 0 and back(f32, 0, 0, 40, 64, True) >= 0      # no matrix
     with pytest.raises(TypeError):
         n.nvfp4_linear_workspace_size(torch.float16, 100, 1, 40, 64)
     # short, missing, misaligned
