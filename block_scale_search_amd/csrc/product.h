@@ -84,7 +84,7 @@ struct ProductPlan {
     int32_t tile_rows;       // rows of X a workgroup
     int32_t tile_cols;       // matrix rows (backward: columns) a workgroup
     int32_t splits;
-    int64_t blocks;          // workgroups
+    int64_t threads;         // of all workgroups
 };
 ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in, int32_t matrices,
                          bool backward, bool f32);

@@ -10,6 +10,7 @@ namespace {
 constexpr int64_t kInt32 = (int64_t)1 << 31;
 constexpr int64_t kMaxSide = (int64_t)1 << 22;     // 32-bit offsets inside a tile
 constexpr int64_t kMaxSpan = (int64_t)1 << 56;
+constexpr int64_t kThreads32 = ((int64_t)1 << 32) - 256;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool span_ok(int64_t n, int64_t stride) {
@@ -52,10 +53,11 @@ nvfp4_status check_call(int dtype, const nvfp4_matrix* w, const nvfp4_matrix* w2
     }
     if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_RELU) return NVFP4_ERR_ARG;
     if (!sizes_ok(tokens, w->batch, w->out, w->in)) return NVFP4_ERR_SHAPE;
-    // one thread per 8 values in the element-wise kernels, and the product's grid
-    if (tokens * ((w->out > w->in ? w->out : w->in) / 8 + 1) >= (int64_t)1 << 38 ||
+    // a launch has fewer than 2^32 threads: one per 8 values of a row or per bias, and the product's own
+    const int64_t pieces = ((w->out > w->in ? w->out : w->in) + 7) / 8;
+    if (tokens * pieces > kThreads32 || w->batch * w->out > kThreads32 ||
         nvfp4::product_plan(tokens, w->batch, w->out, w->in, two ? 2 : 1, backward,
-                            dtype == NVFP4_DTYPE_F32).blocks >= kInt32)
+                            dtype == NVFP4_DTYPE_F32).threads > kThreads32)
         return NVFP4_ERR_SHAPE;
     if (seg == nullptr && w->batch != 1) return NVFP4_ERR_NULL;
     if (!aligned(seg, 8)) return NVFP4_ERR_ALIGN;

@@ -109,7 +109,8 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
         plan.tile_rows = 4;
         plan.tile_cols = 16;
         plan.splits = 1;
-        plan.blocks = product_row_tiles(tokens, batch, 4) * ((out * matrices + 15) / 16);
+        const int64_t slices = (K + 1023) / 1024, most = f32 ? 8 : 16;
+        plan.threads = product_row_tiles(tokens, batch, 4) * ((out + 15) / 16) * 64 * (slices < most ? slices : most);
         return plan;
     }
     if (!backward && !f32 && in % 64 == 0 && each <= (batch > 1 ? 128 : 64)) {
@@ -140,7 +141,7 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
     const int64_t share = ((steps + splits - 1) / splits + unit - 1) / unit * unit;
     splits = (steps + share - 1) / share;                // none empty
     plan.splits = (int32_t)splits;
-    plan.blocks = tiles * splits;
+    plan.threads = tiles * splits * (plan.tile_rows == 256 ? 512 : 256);
     return plan;
 }
 

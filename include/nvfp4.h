@@ -470,13 +470,16 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  * Row tensors are bf16 or f32 (dtype, the same for all of a call; bias too), with a row stride in elements
  * of at least their columns. Sums are binary32: level * E4M3 is exact in bf16, a bf16 value enters the MFMA
  * products as it is and an f32 value as three bf16 parts (exact for magnitudes that are zero or above 2^-100), so
- * the products themselves are exact. Outputs are rounded once (to nearest even), from binary32. A row with
- * a NaN or an infinity has unspecified results in that row (rows, never others). A tensor of outputs may
+ * the products themselves are exact. Outputs are rounded once (to nearest even), from binary32. Where a row
+ * that enters a product holds a NaN or an infinity, all sums of that row (z, g, u, dX) are infinite or NaN (which of
+ * the two is not specified); other rows are not touched by it. A tensor of outputs may
  * not overlap any other tensor of the call, but Y may be the residual itself (same address, same stride).
  *
  * Requires in % 16 == 0, in >= 16, out >= 1 (a product with an empty matrix is refused), in and out < 2^22, out * in / 16 < 2^31,
  * tokens < 2^31, batch <= 65,535, packed 8-byte aligned, stride a multiple of 16; rows that a product reads 16
- * bytes at a time (X, and where a call says so) have a stride < 2^22. tokens == 0 is valid.
+ * bytes at a time (X, and where a call says so) have a stride < 2^22. A call that would need a launch of 2^32 threads
+ * is refused (NVFP4_ERR_SHAPE): tokens times the pieces of 8 of the larger of in and out, batch * out and the
+ * product's tiles are below 2^32 - 256 each. tokens == 0 is valid.
  * Workspaces: 16-byte aligned, no initialisation needed, of at least the size that the query of the same
  * name gives for the same sizes (NULL is valid where that is 0).
  * ------------------------------------------------------------------------------------------- */

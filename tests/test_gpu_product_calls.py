@@ -166,6 +166,20 @@ def test_what_is_no_number_stays_in_its_row(nv, T, out, inp, dtype):
 
 
 @DTYPES
+@SHAPES
+@pytest.mark.parametrize("value", (float("nan"), float("inf"), -float("inf")))
+def test_no_sum_of_a_row_hides_what_is_no_number(nv, T, out, inp, value, dtype):
+    w, v = Weights(1, out, inp, 1, whole=True), Weights(1, out, inp, 2, whole=True)
+    m, n = w.matrix(nv), v.matrix(nv)
+    x, d, z = rows((T, inp), dtype, 3, whole=True), rows((T, out), dtype, 4, whole=True), rows((T, out), dtype, 5, whole=True)
+    x[0, 0] = x[1, inp - 1] = d[0, 0] = d[1, out - 1] = value
+    g, u = nv.gated(m, n, x.to(DEV), with_pre=True)[1:]
+    for y in (nv.linear(m, x.to(DEV)), g, u, nv.linear_backward(m, d.to(DEV))["dX"],
+              nv.gated_backward(m, n, d.to(DEV), z.to(DEV), z.to(DEV))["dX"]):
+        assert not torch.isfinite(y[:2]).any() and torch.isfinite(y[2:]).all()
+
+
+@DTYPES
 @pytest.mark.parametrize("seg", ([0, 40, 10, 90], [0, -5, 30, 1 << 40], [50, 20, 10, 0], [0, 0, 0, 0], [0, 1 << 62, -1, 90]))
 def test_offsets_that_are_no_partition(nv, seg, dtype):
     """Unspecified values in the rows, nothing outside them; every call ends."""

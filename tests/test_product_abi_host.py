@@ -186,3 +186,14 @@ def test_model_gradients_by_differences():
         e[t, i] = h
         assert abs((loss(x + e) - loss(x - e)) / (2 * h) - dx[t, i]) <= 1e-5 * (1 + dx[t, i].abs())
     assert [e for e, _ in spans(counts)] == [0, 2]
+
+
+@pytest.mark.parametrize("call, rows", [(_linear, "X"), (_gated, "X"), (_linear_backward, "dY"), (_gated_backward, "dH")])
+def test_launches_beyond_32_bits(n, call, rows):
+    most = ((1 << 32) - 256) // 8                        # 8 pieces of 8 columns a row
+    assert call(n, tokens=most, **{rows: None}) == n.ERR_NULL
+    assert call(n, tokens=most + 1, **{rows: None}) == n.ERR_SHAPE
+    many = dict(batch=65535, in_=16)
+    assert call(n, _matrix(n, out=1 << 17, stride=1 << 21, **many), seg=FAKE) == n.ERR_SHAPE          # biases
+    if call in (_linear, _gated):                        # tiles of 4 rows by 16
+        assert call(n, _matrix(n, out=1 << 15, stride=1 << 19, **many), tokens=65536, seg=FAKE) == n.ERR_SHAPE
