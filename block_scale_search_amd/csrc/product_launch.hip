@@ -100,10 +100,8 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
     const int64_t each = batch > 0 ? (tokens + batch - 1) / batch : 0;
     int64_t steps, tiles;
     // rows of a matrix (on average): up to 4 of them pass through the kernel that keeps them in registers (8192 x 28672:
-    // 39.2 us at 4 rows, 48.3 at 8; by tiles of 32 rows 46.1 and 45.7), up to 64 through tiles whose weights are
-    // converted where they are used (64 rows 57 us, 128 rows 106 us; by tiles through LDS 83 and 93; several
-    // matrices leave part of a tile empty each: 128 rows on average of 128 matrices of 2048 x 768 118 us, by tiles of 128
-    // rows 150)
+    // 39.2 us at 4 rows, 48.3 at 8; by tiles of 32 rows 46.1 and 45.7), up to 96 through tiles whose weights are
+    // converted where they are used (96 rows 70 us, 128 rows 106; by tiles through LDS 88 and 93)
     if (!backward && each <= 4) {
         plan.kernel = ProductKernel::kRows;
         plan.tile_rows = 4;
@@ -113,9 +111,15 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
         plan.threads = product_row_tiles(tokens, batch, 4) * ((out + 15) / 16) * 64 * (slices < most ? slices : most);
         return plan;
     }
-    if (!backward && !f32 && in % 64 == 0 && each <= (batch > 1 ? 128 : 64)) {
+    // Several matrices leave part of a tile empty each, which costs the kernel of smaller tiles less: 128 rows on average
+    // of 128 matrices of 2048 x 768 119 us and 150, 256 rows 210 and 259, of 8 matrices of 2 x 14336 x 4096 701 and 821;
+    // but 192 rows of 8 of 4096 x 14336 317 and 282, and from some 400 rows on it is the slower one. Tiles of 64
+    // rows, since three workgroups share a compute unit then (64 rows on average of 128 matrices of 2048 x 768 79
+    // us, by tiles of 96 rows 95); for one matrix, whose rows fill it, one of 96 (80 rows by 8192 x 28672 71.5 us, by two
+    // of 64 96.6).
+    if (!backward && !f32 && in % 64 == 0 && each <= (batch <= 1 ? 96 : in <= 4096 ? 256 : 128)) {
         plan.kernel = ProductKernel::kMid;
-        plan.tile_rows = each <= 32 ? 32 : 64;
+        plan.tile_rows = each <= 32 ? 32 : each <= 64 || batch > 1 ? 64 : 96;
         plan.tile_cols = 128;
         steps = (K + 127) / 128;
         tiles = product_row_tiles(tokens, batch, plan.tile_rows) * ((N * matrices + 127) / 128);

@@ -176,7 +176,8 @@ void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
 template <bool GATED>
 void launch(const Product& p, const ProductPlan& plan, hipStream_t stream) {
     if (plan.tile_rows == 32) launch<32, 3, GATED>(p, plan, stream);
-    else launch<64, 2, GATED>(p, plan, stream);
+    else if (plan.tile_rows == 64) launch<64, 2, GATED>(p, plan, stream);
+    else launch<96, 2, GATED>(p, plan, stream);
 }
 
 }  // namespace

@@ -210,3 +210,36 @@ def test_experts(nv, counts, behind, dtype):
     check(dG, dg, "dG")
     check(dU, du, "dU")
     check(dX, product(dg, w, counts, False)[0] + product(du, v, counts, False)[0], "dX of two")
+
+
+@pytest.mark.parametrize("shift", (0, 1))
+@pytest.mark.parametrize("T, out, inp", [(64, 129, 192), (65, 70, 64), (80, 201, 1088), (95, 128, 320), (96, 40, 2112),
+                                         (97, 129, 192)])
+def test_tens_of_rows(nv, T, out, inp, shift):
+    """Tiles of 64 and 96 rows, whole and not; with rows laid out for 16-byte stores and not."""
+    w, v = Weights(1, out, inp, T + out, whole=True), Weights(1, out, inp, T + inp, whole=True)
+    x, r = rows((T, inp), BF16, 1, whole=True), rows((T, out), BF16, 2, whole=True)
+    b = rows((1, out), BF16, 3, whole=True)
+    wide = torch.zeros((T, out + 8 + shift), dtype=BF16, device=DEV)
+    wide[:, shift:out + shift] = r.to(DEV)
+    z = product(x, w, [T])[0] + b.double()
+    y, pre = nv.linear(w.matrix(nv), x.to(DEV), bias=b.to(DEV), activation=nv.ACT_RELU,
+                       residual=wide[:, shift:out + shift], with_pre=True)
+    same(pre, z, BF16, "Z")
+    same(y, z.clamp(min=0) + r.double(), BF16, "Y")
+    _, g, u = nv.gated(w.matrix(nv), v.matrix(nv), x.to(DEV), with_pre=True)
+    same(g, product(x, w, [T])[0], BF16, "G")
+    same(u, product(x, v, [T])[0], BF16, "U")
+
+
+@pytest.mark.parametrize("counts", ([65, 0, 130, 64], [300, 255, 1, 0, 200], [257, 256, 256], [200] * 3, [0, 0, 700, 1, 65],
+                                    [70] + [0, 1, 200] * 50))
+def test_experts_of_many_rows(nv, counts):
+    E, T, out, inp = len(counts), sum(counts), 72, 192
+    w, v = Weights(E, out, inp, 1, whole=True), Weights(E, out, inp, 2, whole=True)
+    x, b, seg = rows((T, inp), BF16, 3, whole=True), rows((E, out), BF16, 4, whole=True), offsets(counts).to(DEV)
+    z = product(x, w, counts)[0]
+    same(nv.linear(w.matrix(nv), x.to(DEV), bias=b.to(DEV), seg_offsets=seg), z + by_row(b, counts), BF16, "Y")
+    _, g, u = nv.gated(w.matrix(nv), v.matrix(nv), x.to(DEV), seg_offsets=seg, with_pre=True)
+    same(g, z, BF16, "G")
+    same(u, product(x, v, counts)[0], BF16, "U")
