@@ -4,9 +4,9 @@
 // Arithmetic. level * E4M3(scale) has at most 2 + 4 significant bits and lies in 2^-10 .. 2880, so it is
 // exact in bf16, and its product with a bf16 value is exact in binary32: the MFMA's sums are the only
 // roundings before the global scale S, which multiplies the sum. A scale byte is masked to 7 bits; the
-// codes of groups past the matrix's edge are multiplied by a scale of zero. (f16 operands would be a
-// third cheaper to make, but bf16 activations fit f16's range only after a scaling of each row, which
-// loses what is 2^-39 of the row's largest value even where that value meets zeros.)
+// codes of groups past the matrix's edge are multiplied by a scale of zero. f16 operands take half the
+// instructions, but bf16 rows fit f16's range only after a scaling: the kernel for few rows, which has a row's values in
+// registers, does that by itself; the others would need a pass over the rows before them.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -7,7 +7,15 @@
 // pieces: of the 16 x 16 sums the quarter where the pieces are the same is wanted. What that wastes of the matrix units
 // is idle here anyway, and it lets four neighbouring lanes read neighbouring bytes of a row (16 rows side by
 // side, a lane each, took 1.5 to 2 times as long: the loads' addresses were the bound). A lane converts 64
-// codes of 4 groups a step (level * E4M3 is exact in bf16). The slices' sums meet in LDS, in a fixed order.
+// codes of 4 groups a step. The slices' sums meet in LDS, in a fixed order.
+//
+// Operands. bf16 rows enter as f16 ones, a row's slice times a power of two, since f16 weights (level * E4M3 is exact in
+// them too) take half the instructions of bf16 ones: 2 to 8% of the whole. A value keeps all its bits
+// down to 2^-31 of the largest of its slice, below that those above 2^-39 of it: less than the binary32 sums round where
+// that largest value meets any weight but zero. The parts of f32 rows enter as bf16.
+//
+// Measured: gate and up of 2 x 28672 x 8192, one row, 52.7 us = 5.0 TB/s, a large copy's rate; 8192 x 28672 29 us (4.6);
+// 4096 x 14336, 256 workgroups of 14 waves, 11.2 us (2.9), bound by launch and first codes.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"
@@ -23,10 +31,55 @@ constexpr int kWaves = F32 ? 8 : 16; // at most (registers)
 constexpr int kDepth = 4;            // groups of 4 matrix rows in flight
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 
+template <bool F32>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
-                                                   c, 0, 0, 0);
+    if constexpr (F32)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a), __builtin_bit_cast(half8v, b),
+                                                      c, 0, 0, 0);
+}
+
+// Scale byte B (masked) times 2^-8 as f16, twice: E4M3's fields are f16's upper ones.
+template <int B>
+__device__ __forceinline__ half2v scale_half(uint32_t bytes) {
+    return __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0u, bytes, 0x0C000C00u | B | B << 16) << 7);
+}
+// Eight codes times their scale (as scale_half gives it) as f16, exact.
+__device__ __forceinline__ u32x4 dequant8_half(uint32_t w, half2v scale) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 0) * scale),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 1) * scale),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 2) * scale),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 3) * scale)};
+}
+
+// Makes bf16 values f16 ones times 2^k, the largest magnitude of the row's slice (that of the 16 lanes with the same
+// n4) coming to 2^14 .. 2^15; returns k. A slice with an infinity or a NaN keeps it, whatever becomes of the others.
+__device__ __forceinline__ int to_half(u32x4 (&x)[8]) {
+    ushort2v most = {0, 0};
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2v, x[s][j] & 0x7FFF7FFFu));
+    int m = max((int)most[0], (int)most[1]);
+    m = max(m, __builtin_amdgcn_update_dpp(0, m, 0xB1, 0xF, 0xF, true));
+    m = max(m, __builtin_amdgcn_update_dpp(0, m, 0x4E, 0xF, 0xF, true));
+    m = max(m, __shfl_xor(m, 16, 64));
+    m = max(m, __shfl_xor(m, 32, 64));
+    const int e = m >> 7, k = e == 255 ? 0 : 141 - max(e, 1);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[s][j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_ldexpf(bf16_lo(x[s][j]), k),
+                                                                              __builtin_amdgcn_ldexpf(bf16_hi(x[s][j]), k)));
+    return k;
 }
 
 // Sum over four neighbouring lanes, in each of them.
@@ -75,6 +128,8 @@ __global__ __launch_bounds__(64 * kWaves<F32>) void k_product_rows(Product p, in
 #pragma unroll
             for (int s = 0; s < 8; ++s) x[i][s] = load16(from, n4 < rows.rows && k + 8 * s < K ? at + 16 * s : kNowhere);
         }
+        int raised = 0;
+        if constexpr (!F32) raised = to_half(x[0]);
         const uint32_t first = (uint32_t)n4 * (uint32_t)(K / 16) + (uint32_t)(k / 16);   // in groups of 16 weights
         const auto load = [&](Codes& b, int g) {
             const int j = GATED && g >= half ? g - half : g;
@@ -112,18 +167,31 @@ __global__ __launch_bounds__(64 * kWaves<F32>) void k_product_rows(Product p, in
             for (int d = 0; d < kDepth; ++d) {
                 Codes& b = buf[d];
                 f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-                const float e[4] = {scale_value<0>(b.scale), scale_value<1>(b.scale), scale_value<2>(b.scale),
-                                    scale_value<3>(b.scale)};
+                const auto multiply = [&](const auto (&e)[4]) {
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const u32x4 w = dequant8(b.code[s >> 2][s & 3], e[s >> 1]);
+                    for (int s = 0; s < 8; ++s) {
+                        u32x4 w;
+                        if constexpr (F32) w = dequant8(b.code[s >> 2][s & 3], e[s >> 1]);
+                        else w = dequant8_half(b.code[s >> 2][s & 3], e[s >> 1]);
 #pragma unroll
-                    for (int i = 0; i < P; ++i) acc[s & 1] = mfma(w, x[i][s], acc[s & 1]);
+                        for (int i = 0; i < P; ++i) acc[s & 1] = mfma<F32>(w, x[i][s], acc[s & 1]);
+                    }
+                };
+                if constexpr (F32) {
+                    const float e[4] = {scale_value<0>(b.scale), scale_value<1>(b.scale), scale_value<2>(b.scale),
+                                        scale_value<3>(b.scale)};
+                    multiply(e);
+                } else {
+                    const uint32_t bytes = b.scale & 0x7F7F7F7Fu;
+                    const half2v e[4] = {scale_half<0>(bytes), scale_half<1>(bytes), scale_half<2>(bytes),
+                                         scale_half<3>(bytes)};
+                    multiply(e);
                 }
                 load(b, g0 + d + kDepth);
                 // register r of a lane holds piece r of matrix row kg; the lane's own piece is seg
                 const f32x4 a = acc[0] + acc[1];
-                const float v = sum_quad(seg < 2 ? (seg == 0 ? a[0] : a[1]) : (seg == 2 ? a[2] : a[3]));
+                float v = sum_quad(seg < 2 ? (seg == 0 ? a[0] : a[1]) : (seg == 2 ? a[2] : a[3]));
+                if constexpr (!F32) v = __builtin_amdgcn_ldexpf(v, -raised);
                 float* to = sums + (wave * groups + g0 + d) * 64 + lane;
                 *to = slice == wave ? v : *to + v;
                 __builtin_amdgcn_sched_barrier(0);       // else all loads are issued together, and waited for together
@@ -158,11 +226,15 @@ template <bool GATED, bool F32>
 void launch(const Product& p, hipStream_t stream) {
     const int64_t slices = (p.in + kSlice - 1) / kSlice;
     const int waves = (int)(slices < kWaves<F32> ? slices : kWaves<F32>);
-    // 32 matrix rows a workgroup where that makes enough of them, else 16 (one row, 8192 x 28672: 30.1 us, with 16
-    // rows 35.5; 4096 x 14336 11.6, with 32 rows 15.9)
+    // As many matrix rows a workgroup, 16 to 128, as leave each compute unit the waves of one full workgroup, gated two:
+    // fewer start and end (one row, 8192 x 28672: 32 rows 30 us, 16 35.5, 64 no better than 32; 4096 x 14336: 16 rows 11.2,
+    // 32 15.9; rows of 128 gated experts 2 x 768 x 2048: 64 rows 65 us, 16 72; of 64 of 4096 x 1024: 128 rows 41.5, 16
+    // and 32 46; gated with one: 1 x 2 x 28672 x 8192 64 rows 56 us, 32 and 16 52.7)
     const int64_t tiles = product_row_tiles(p.rows.tokens, p.rows.batch, kRows);
-    const bool wide = tiles * ((p.out * p.matrices + 31) / 32) >= 256;
-    const int block = wide && !GATED ? 32 : 16;
+    int block = 16;
+    while (block < 128 && waves * 2 * block * (GATED ? 2 : 1) <= 1024 &&
+           tiles * ((p.out + 2 * block - 1) / (2 * block)) * waves >= (GATED ? 512 : 256) * kWaves<F32>)
+        block *= 2;
     const int64_t nn = (p.out + block - 1) / block;
     const dim3 grid((uint32_t)(tiles * nn)), threads(64 * waves);
     const size_t lds = (size_t)waves * (GATED ? 2 : 1) * block * 64;

@@ -5,6 +5,7 @@ import torch
 
 from product_helpers import (ACTS, DEV, HALF_STEP, Weights, act, act_error, act_model, by_row, close, offsets,
                              product, rows, sum_error)
+from product_helpers import _E4M3 as E4M3, _LEVELS as LEVELS
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -243,3 +244,45 @@ def test_experts_of_many_rows(nv, counts):
     _, g, u = nv.gated(w.matrix(nv), v.matrix(nv), x.to(DEV), seg_offsets=seg, with_pre=True)
     same(g, z, BF16, "G")
     same(u, product(x, v, counts)[0], BF16, "U")
+
+
+@DTYPES
+@pytest.mark.parametrize("T", (1, 4, 40, 140))
+def test_every_weight_is_exact(nv, T, dtype):
+    """Every code under every scale byte, met by a one: the output is the weight."""
+    out, inp = 127 * 16, 128
+    w = Weights(1, out, inp, 1)
+    o, i = torch.arange(out)[:, None], torch.arange(inp)[None]
+    code = ((o // 127 + i) % 16).to(torch.uint8)[None]
+    w.packed, w.scales = code[..., ::2] | code[..., 1::2] << 4, (o % 127 + 0 * i[:, ::16]).to(torch.uint8)[None].contiguous()
+    w.S = torch.ones(1)
+    w.values = LEVELS[code.long()] * E4M3[w.scales.long()].repeat_interleave(16, -1)
+    x = torch.zeros((T, inp), dtype=dtype)
+    at = torch.arange(T) * 37 % inp
+    x[torch.arange(T), at] = 1
+    same(nv.linear(w.matrix(nv), x.to(DEV)), w.values[0][:, at].t(), dtype, "Y")
+    g, u = nv.gated(w.matrix(nv), w.matrix(nv), x.to(DEV), with_pre=True)[1:]
+    same(g, w.values[0][:, at].t(), dtype, "G")
+    assert torch.equal(g, u)
+
+
+@pytest.mark.parametrize("inp", (64, 1040, 2064, 17408))
+@pytest.mark.parametrize("power", (-90, -20, 0, 9, 90))
+def test_few_rows_of_any_magnitude(nv, power, inp):
+    """A row times a power of two; and small values beside one of 2^29 times theirs that meets weights of zero."""
+    T, out = 4, 70
+    w = Weights(1, out, inp, inp, whole=True)
+    w.packed[..., 0] &= 0xF0                             # column 0: zeros
+    w.values[..., 0] = 0
+    x = rows((T, inp), BF16, 1, whole=True).double()
+    if inp > 2064:                                       # whole numbers that bf16 holds
+        x[torch.rand(x.shape, generator=torch.Generator().manual_seed(2)) < 0.9] = 0
+    x[:2] *= 2.0 ** power
+    x[2] *= 2.0 ** -power
+    x[1:3, 0] = x[1:3].abs().amax(1) * 2.0 ** 29
+    b = x.to(BF16)
+    assert torch.equal(b.double(), x)
+    z = product(x, w, [T])[0]
+    same(nv.linear(w.matrix(nv), b.to(DEV)), z, BF16, "Y")
+    g = nv.gated(w.matrix(nv), w.matrix(nv), b.to(DEV), with_pre=True)[1]
+    same(g, z, BF16, "G")
