@@ -123,10 +123,9 @@ struct ProductSlopes {
     uint16_t* parts[2];
     int64_t ld, plane;
 };
-hipError_t launch_product_slopes(const ProductSlopes& p, hipStream_t stream);
-
-// dbias[e] = sum of dY act'(Z) over matrix e's rows, [batch, cols].
+// With dbias: dbias[e] = sum of dY act'(Z) over matrix e's rows, [batch, cols], in the same launch; without `slopes`
+// only that.
 size_t product_bias_workspace_bytes(int64_t tokens, int64_t batch, int64_t cols);
-hipError_t launch_product_bias(const ProductSlopes& p, float* dbias, void* workspace, hipStream_t stream);
+hipError_t launch_product_slopes(const ProductSlopes& p, bool slopes, float* dbias, void* workspace, hipStream_t stream);
 
 }  // namespace nvfp4

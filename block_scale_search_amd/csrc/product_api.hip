@@ -10,6 +10,7 @@ namespace {
 constexpr int64_t kInt32 = (int64_t)1 << 31;
 constexpr int64_t kMaxSide = (int64_t)1 << 22;     // 32-bit offsets inside a tile
 constexpr int64_t kMaxSpan = (int64_t)1 << 56;
+constexpr int64_t kMaxBiases = (int64_t)1 << 29;   // gradients of biases: 4 threads each
 constexpr int64_t kThreads32 = ((int64_t)1 << 32) - 256;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -146,7 +147,7 @@ nvfp4::Product product_of(const nvfp4_matrix* w, const nvfp4_matrix* w2, bool ba
 }
 
 // Gradients of two or one matrices' outputs: the element-wise pass where it is needed, then the product.
-nvfp4_status backward(nvfp4::Product& p, nvfp4::ProductSlopes& g, const Space& s, void* workspace,
+nvfp4_status backward(nvfp4::Product& p, nvfp4::ProductSlopes& g, float* dbias, const Space& s, void* workspace,
                       hipStream_t stream) {
     p.planes = s.planes;
     p.plane = s.plane;
@@ -164,11 +165,12 @@ nvfp4_status backward(nvfp4::Product& p, nvfp4::ProductSlopes& g, const Space& s
     }
     g.ld = s.ld;
     g.plane = s.plane;
-    if (s.parts || g.Z) {
-        const hipError_t e = nvfp4::launch_product_slopes(g, stream);
-        if (e != hipSuccess) return NVFP4_ERR_HIP;
+    const bool slopes = p.rows.tokens > 0 && (s.parts || g.Z);
+    if (slopes || dbias) {
+        void* sums = ws + p.matrices * s.operand + s.partial + s.map;
+        if (nvfp4::launch_product_slopes(g, slopes, dbias, sums, stream) != hipSuccess) return NVFP4_ERR_HIP;
     }
-    return hip_status(nvfp4::launch_product(p, stream));
+    return p.rows.tokens > 0 ? hip_status(nvfp4::launch_product(p, stream)) : NVFP4_OK;
 }
 
 }  // namespace
@@ -271,6 +273,7 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
         if (st != NVFP4_OK) return st;
     }
     if (!aligned(dbias, 4)) return NVFP4_ERR_ALIGN;
+    if (dbias && W->batch * W->out > kMaxBiases) return NVFP4_ERR_SHAPE;
     st = check_workspace(s.total, workspace, workspace_bytes);
     if (st != NVFP4_OK) return st;
     nvfp4::ProductSlopes g = {};
@@ -284,17 +287,10 @@ nvfp4_status nvfp4_linear_backward(const nvfp4_matrix* W, const void* dY, int dt
     g.ldz = ldz;
     g.d[0] = act ? dZ : nullptr;
     g.ldd[0] = lddz;
-    const hipStream_t on = static_cast<hipStream_t>(stream);
-    if (dbias) {
-        const hipError_t e =
-            nvfp4::launch_product_bias(g, dbias, static_cast<uint8_t*>(workspace) + s.operand + s.partial + s.map, on);
-        if (e != hipSuccess) return NVFP4_ERR_HIP;
-    }
-    if (tokens == 0) return NVFP4_OK;
     nvfp4::Product p = product_of(W, nullptr, true, dtype, tokens, seg_offsets, NVFP4_ACT_NONE);
     p.y = dX;
     p.ldy = lddx;
-    return backward(p, g, s, workspace, on);
+    return backward(p, g, dbias, s, workspace, static_cast<hipStream_t>(stream));
 }
 
 size_t nvfp4_gated_backward_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out,
@@ -343,7 +339,7 @@ nvfp4_status nvfp4_gated_backward(const nvfp4_matrix* W_gate, const nvfp4_matrix
     nvfp4::Product p = product_of(W_gate, W_up, true, dtype, tokens, seg_offsets, NVFP4_ACT_NONE);
     p.y = dX;
     p.ldy = lddx;
-    return backward(p, g, s, workspace, static_cast<hipStream_t>(stream));
+    return backward(p, g, nullptr, s, workspace, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -139,6 +139,7 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
     const int64_t unit = plan.kernel == ProductKernel::kTiles ? 4 : 1;
     const int64_t want = plan.kernel == ProductKernel::kTiles && plan.tile_rows == 256 ? 256 : 512;
     int64_t splits = tiles > 0 ? want / tiles : 1;
+    if (plan.kernel == ProductKernel::kTiles && tiles >= 256) splits = 1;       // 1024 rows by 4096 x 4096 50 us, in 2 shares 56
     if (splits > steps / (2 * unit)) splits = steps / (2 * unit);
     if (splits > 32) splits = 32;
     if (splits < 1) splits = 1;

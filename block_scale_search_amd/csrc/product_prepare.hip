@@ -63,13 +63,91 @@ __global__ __launch_bounds__(kThreads) void k_product_parts(const void* X, int64
     store_parts<F32>(x, parts, t * ld + c, plane);
 }
 
+// Bias gradients. A workgroup sums COLS columns over a share of a matrix's rows; its lanes take COLS columns by 64 / COLS
+// rows, eight rows' loads at a time, and their sums are added in binary64. Up to kWhole rows a matrix (on average)
+// there is one share, and 16 columns a workgroup, so that no second launch is needed; else 64 columns, and a second
+// kernel adds the shares' sums in binary64. The order is fixed.
+constexpr int kWhole = 512;
+constexpr int kShareRows = 32;       // rows of a share at least
+struct Bias {
+    float* to;                       // dbias, or the shares' sums
+    int32_t shares, blocks, groups;  // workgroups, and those of a share of a matrix
+    bool narrow;
+};
+Bias bias_of(int64_t tokens, int64_t batch, int64_t cols) {
+    Bias b{nullptr, 1, 0, 0, batch < 1 || (tokens <= kWhole * batch && batch * cols <= 1 << 24)};
+    b.groups = (int32_t)((cols + (b.narrow ? 15 : 63)) / (b.narrow ? 16 : 64));
+    if (!b.narrow) {
+        const int64_t groups = batch * b.groups;
+        const int64_t want = (2048 + groups - 1) / groups, most = (tokens / batch + kShareRows - 1) / kShareRows;
+        b.shares = (int32_t)(want < most ? (want < 64 ? want : 64) : (most < 64 ? most : 64));
+    }
+    b.blocks = (int32_t)(b.groups * batch * b.shares);
+    return b;
+}
+
+template <bool F32, int COLS>
+__device__ __forceinline__ void bias_sums(const ProductSlopes& p, const Bias& b, int block) {
+    constexpr int kRows = 64 / COLS * (kThreads / 64);   // rows side by side
+    __shared__ float sums[kRows][COLS];
+    const int column = threadIdx.x % COLS, row = threadIdx.x / COLS;
+    const int group = block % b.groups, share = block / b.groups % b.shares;
+    const int64_t e = block / b.groups / b.shares, n = (int64_t)group * COLS + column;
+    int64_t lo = 0, hi = p.rows.tokens;
+    if (p.rows.seg) segment(p.rows, (int)e, lo, hi);
+    const int64_t each = (hi - lo + b.shares - 1) / b.shares, first = lo + each * share;
+    const int64_t last = min(first + each, hi);
+    float sum = 0.0f;
+    if (n < p.cols) {
+        for (int64_t t0 = first + row; t0 < last; t0 += 8 * kRows) {  // 8 rows summed by themselves
+            float d[8], z[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int64_t t = min(t0 + kRows * k, last - 1);
+                d[k] = load_value(p.dY, t * p.lddy + n, F32);
+                z[k] = p.Z ? load_value(p.Z, t * p.ldz + n, F32) : 0.0f;
+            }
+            float part = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float a, slope = 1.0f;
+                if (p.Z) act_slope<F32>(p.act, z[k], a, slope);
+                part += t0 + kRows * k < last ? d[k] * slope : 0.0f;
+            }
+            sum += part;
+        }
+    }
+    sums[row][column] = sum;
+    __syncthreads();
+    if (row == 0 && n < p.cols) {
+        double s = 0.0;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) s += (double)sums[k][column];
+        b.to[(e * b.shares + share) * p.cols + n] = (float)s;
+    }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void k_product_bias(ProductSlopes p, Bias b) {
+    if (b.narrow) bias_sums<F32, 16>(p, b, blockIdx.x);
+    else bias_sums<F32, 64>(p, b, blockIdx.x);
+}
+
 struct Wide {
     bool dY, Z, U, d[2];
 };
 
+// One thread per piece of 8 values. The first workgroups make the bias gradient (b.blocks, none if it is not asked for).
 template <bool F32, bool GATED>
-__global__ __launch_bounds__(kThreads) void k_product_slopes(ProductSlopes p, Wide w, int64_t pieces, int64_t total) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+__global__ __launch_bounds__(kThreads) void k_product_slopes(ProductSlopes p, Wide w, int64_t pieces, int64_t total, Bias b) {
+    if constexpr (!GATED) {
+        if (blockIdx.x < (uint32_t)b.blocks) {
+            if (b.narrow) bias_sums<F32, 16>(p, b, blockIdx.x);
+            else bias_sums<F32, 64>(p, b, blockIdx.x);
+            return;
+        }
+    }
+    const int64_t i = ((int64_t)blockIdx.x - b.blocks) * kThreads + threadIdx.x;
     if (i >= total) return;
     const int64_t t = i / pieces, c = (i - t * pieces) * 8;
     if (t >= rows_end(p.rows)) return;
@@ -104,55 +182,6 @@ bool wide(const void* p, int64_t ld, bool f32) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % (f32 ? 4 : 8) == 0;
 }
 
-// Bias gradients. A workgroup sums 64 columns over a share of a matrix's rows, each of its four waves every
-// fourth row, eight rows' loads at a time; the shares' sums are added in binary64 by a second kernel. The order is fixed.
-constexpr int kShareRows = 32;       // rows of a share at least
-int64_t bias_shares(int64_t tokens, int64_t batch, int64_t cols) {
-    if (batch < 1) return 1;
-    const int64_t groups = batch * ((cols + 63) / 64);
-    const int64_t want = (2048 + groups - 1) / groups, most = (tokens / batch + kShareRows - 1) / kShareRows;
-    int64_t n = want < most ? want : most;
-    if (n > 64) n = 64;
-    return n < 1 ? 1 : n;
-}
-
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void k_product_bias(ProductSlopes p, int shares, float* partial) {
-    __shared__ float sums[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
-    const int64_t e = blockIdx.y;
-    int64_t lo = 0, hi = p.rows.tokens;
-    if (p.rows.seg) segment(p.rows, (int)e, lo, hi);
-    const int64_t each = (hi - lo + shares - 1) / shares, first = lo + each * blockIdx.z;
-    const int64_t last = min(first + each, hi);
-    float sum = 0.0f;
-    if (n < p.cols) {
-        for (int64_t t0 = first + wave; t0 < last; t0 += 32) {        // 8 rows summed by themselves
-            float d[8], z[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int64_t t = min(t0 + 4 * k, last - 1);
-                d[k] = load_value(p.dY, t * p.lddy + n, F32);
-                z[k] = p.Z ? load_value(p.Z, t * p.ldz + n, F32) : 0.0f;
-            }
-            float part = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float a, slope = 1.0f;
-                if (p.Z) act_slope<F32>(p.act, z[k], a, slope);
-                part += t0 + 4 * k < last ? d[k] * slope : 0.0f;
-            }
-            sum += part;
-        }
-    }
-    sums[wave][lane] = sum;
-    __syncthreads();
-    if (wave == 0 && n < p.cols)
-        partial[(e * shares + blockIdx.z) * p.cols + n] =
-            (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
-}
-
 __global__ __launch_bounds__(kThreads) void k_product_bias_join(const float* partial, int64_t cols, int64_t total,
                                                                 int shares, float* dbias) {
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -179,40 +208,44 @@ hipError_t launch_product_parts(const void* X, bool f32, int64_t tokens, int64_t
     return hipGetLastError();
 }
 
-hipError_t launch_product_slopes(const ProductSlopes& p, hipStream_t stream) {
-    const int64_t pieces = (p.cols + 7) / 8, total = p.rows.tokens * pieces;
-    const dim3 grid((uint32_t)((total + kThreads - 1) / kThreads));
+size_t product_bias_workspace_bytes(int64_t tokens, int64_t batch, int64_t cols) {
+    const Bias b = bias_of(tokens, batch, cols);
+    return batch > 0 ? (size_t)(batch * b.shares * cols) * 4 : 0;
+}
+
+hipError_t launch_product_slopes(const ProductSlopes& p, bool slopes, float* dbias, void* workspace, hipStream_t stream) {
+    const int64_t pieces = (p.cols + 7) / 8, total = slopes ? p.rows.tokens * pieces : 0;
+    if (dbias && total >= (int64_t)1 << 31) {            // a launch has fewer than 2^32 threads
+        const hipError_t e = launch_product_slopes(p, false, dbias, workspace, stream);
+        return e == hipSuccess ? launch_product_slopes(p, true, nullptr, nullptr, stream) : e;
+    }
+    Bias b{};
+    if (dbias) {
+        b = bias_of(p.rows.tokens, p.rows.batch, p.cols);
+        b.to = b.shares > 1 ? static_cast<float*>(workspace) : dbias;
+    }
+    const dim3 grid((uint32_t)(b.blocks + (total + kThreads - 1) / kThreads));
     const Wide w{wide(p.dY, p.lddy, p.f32), wide(p.Z, p.ldz, p.f32), wide(p.U, p.ldu, p.f32),
                  {wide(p.d[0], p.ldd[0], p.f32), wide(p.d[1], p.ldd[1], p.f32)}};
+    const auto launch = [&](auto* kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, w, pieces, total, b);
+    };
     if (p.U) {
-        if (p.f32)
-            hipLaunchKernelGGL((k_product_slopes<true, true>), grid, dim3(kThreads), 0, stream, p, w, pieces, total);
-        else
-            hipLaunchKernelGGL((k_product_slopes<false, true>), grid, dim3(kThreads), 0, stream, p, w, pieces, total);
+        if (p.f32) launch(k_product_slopes<true, true>);
+        else launch(k_product_slopes<false, true>);
+    } else if (slopes) {
+        if (p.f32) launch(k_product_slopes<true, false>);
+        else launch(k_product_slopes<false, false>);
+    } else if (p.f32) {
+        hipLaunchKernelGGL(k_product_bias<true>, grid, dim3(kThreads), 0, stream, p, b);
     } else {
-        if (p.f32)
-            hipLaunchKernelGGL((k_product_slopes<true, false>), grid, dim3(kThreads), 0, stream, p, w, pieces, total);
-        else
-            hipLaunchKernelGGL((k_product_slopes<false, false>), grid, dim3(kThreads), 0, stream, p, w, pieces, total);
+        hipLaunchKernelGGL(k_product_bias<false>, grid, dim3(kThreads), 0, stream, p, b);
     }
-    return hipGetLastError();
-}
-
-size_t product_bias_workspace_bytes(int64_t tokens, int64_t batch, int64_t cols) {
-    return (size_t)(batch * bias_shares(tokens, batch, cols) * cols) * 4;
-}
-
-hipError_t launch_product_bias(const ProductSlopes& p, float* dbias, void* workspace, hipStream_t stream) {
-    const int64_t shares = bias_shares(p.rows.tokens, p.rows.batch, p.cols);
-    float* partial = static_cast<float*>(workspace);
-    const dim3 grid((uint32_t)((p.cols + 63) / 64), (uint32_t)p.rows.batch, (uint32_t)shares);
-    if (p.f32)
-        hipLaunchKernelGGL(k_product_bias<true>, grid, dim3(kThreads), 0, stream, p, (int)shares, partial);
-    else
-        hipLaunchKernelGGL(k_product_bias<false>, grid, dim3(kThreads), 0, stream, p, (int)shares, partial);
-    const int64_t total = p.rows.batch * p.cols;
-    hipLaunchKernelGGL(k_product_bias_join, dim3((uint32_t)((total + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                       stream, partial, p.cols, total, (int)shares, dbias);
+    if (b.shares > 1) {
+        const int64_t all = p.rows.batch * p.cols;
+        hipLaunchKernelGGL(k_product_bias_join, dim3((uint32_t)((all + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                           stream, b.to, p.cols, all, b.shares, dbias);
+    }
     return hipGetLastError();
 }
 

@@ -533,7 +533,7 @@ nvfp4_status nvfp4_gated(const nvfp4_matrix* W_gate, const nvfp4_matrix* W_up, c
  *   dZ = dY * act'(Z),   dX[t, i] = sum_o dZ[t, o] w[e, o, i],   dbias[e, o] = sum of dZ over e's rows
  * dY       [tokens, out]. Z, dZ: [tokens, out], not used with NVFP4_ACT_NONE (may be NULL), where dZ is
  *          dY. dZ enters dX's product as dtype holds it (bf16: rounded); dbias sums the unrounded.
- * dbias    float [batch, out] or NULL (0 for a matrix without rows).
+ * dbias    float [batch, out] or NULL (0 for a matrix without rows); at most 2^29 values.
  * dX       [tokens, in].
  * bf16 with out % 8 == 0: rows of dY (NVFP4_ACT_NONE) or of dZ are 16-byte aligned. RELU's slope at 0 is 0. */
 size_t nvfp4_linear_backward_workspace_size(int dtype, int64_t tokens, int64_t batch, int64_t out,

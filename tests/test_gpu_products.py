@@ -286,3 +286,25 @@ def test_few_rows_of_any_magnitude(nv, power, inp):
     same(nv.linear(w.matrix(nv), b.to(DEV)), z, BF16, "Y")
     g = nv.gated(w.matrix(nv), w.matrix(nv), b.to(DEV), with_pre=True)[1]
     same(g, z, BF16, "G")
+
+
+@DTYPES
+@pytest.mark.parametrize("name", ("none", "gelu"))
+@pytest.mark.parametrize("counts, out", [([1], 16), ([33], 17), ([512], 40), ([513], 40), ([2000], 129), ([0, 3, 600, 1], 70),
+                                         ([0, 3, 2700, 0, 1], 70), ([1, 0] * 90, 24), ([7000], 1)])
+def test_bias_gradients(nv, counts, out, name, dtype):
+    """One share of the rows and several, alone and beside the slopes."""
+    E, T, inp = len(counts), sum(counts), 32
+    w = Weights(E, out, inp, 1, whole=True)
+    d, z = rows((T, out), dtype, 2, whole=True), rows((T, out), dtype, 3)
+    seg = None if E == 1 else offsets(counts).to(DEV)
+    got = nv.linear_backward(w.matrix(nv), d.to(DEV), Z=None if name == "none" else z.to(DEV), activation=act(nv, name),
+                             seg_offsets=seg, with_bias=True)["dbias"].cpu()
+    g = d.double() * act_model(z.double(), name)[1]
+    want, size = torch.zeros((E, out), dtype=torch.float64), torch.zeros((E, out), dtype=torch.float64)
+    at = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    want.index_add_(0, at, g)
+    size.index_add_(0, at, d.double().abs())
+    # whole numbers: exact; else slopes of at most 1.2, off by at most 16 steps, and sums of T of them
+    off = 0 if name == "none" else (16 + T) * 2.0 ** -23 * 1.2 * size
+    assert bool(((got.double() - want).abs() <= off).all())
