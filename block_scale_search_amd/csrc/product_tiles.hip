@@ -8,6 +8,13 @@
 // LDS row are permuted by the row so that the reads of MFMA operands and the writes use all banks.
 // Gated: the columns of a tile are 32 of the gate, the same 32 of the other matrix, and so on, so that
 // both values of an output are in the same lane.
+//
+// What bounds it. Tiles of 256 x 256: the matrix units, 67 to 69% busy forward and 56 to 59% backward at the clock that the
+// power limit leaves (1.8 GHz); their LDS traffic (192 KB read, 64 KB written a step) takes as long as they do, and runs
+// beside them. 8192 rows by 2 x 14336 x 4096 1560 us (1.23 PFLOP/s), of which the matrix instructions alone take 1217 to
+// 1254, LDS, conversion and barriers 150, copies of the rows 130, loads of codes 150. Tiles of 128 x 128: latencies of
+// short reductions (two workgroups a compute unit); gradients of 16384 rows of 128 experts 2 x 768 x 2048 255 us (0.4
+// PFLOP/s), matrix units 30% busy, vector units 41%, neither 43%.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
