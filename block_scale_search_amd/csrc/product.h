@@ -70,10 +70,11 @@ inline int64_t product_row_tiles(int64_t tokens, int64_t batch, int64_t size) {
     return tokens / size + (batch < tokens ? batch : tokens);
 }
 
-// Rows of tiles in the tile kernel's grid: with several matrices, whole turns of the 8 XCDs.
+// Rows of tiles in the tile kernel's grid: with many of several matrices, whole turns of the 8 XCDs.
+constexpr int kManyRowTiles = 64;
 inline int64_t product_tile_rows(int64_t tokens, int64_t batch, int64_t size) {
     const int64_t n = product_row_tiles(tokens, batch, size);
-    return batch > 1 ? (n + 7) / 8 * 8 : n;
+    return batch > 1 && n >= kManyRowTiles ? (n + 7) / 8 * 8 : n;
 }
 
 // Which kernel computes a product, and in how many shares of its reduction (more than one: their sums go to the

@@ -130,7 +130,10 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
         // tiles of 256 x 256 where they have work of 32 steps a compute unit at least (512 rows by 8192 x 8192 89 us, by
         // tiles of 128 x 128 96; 1024 by 4096 x 4096 63 and 56; 4096 by 4096 x 14336 400 and 560)
         const int64_t big = product_tile_rows(tokens, batch, 256) * ((cols + 255) / 256);
-        const int side = each >= 256 && big * steps >= 256 * 32 ? 256 : 128;
+        // and where their last round, one tile a compute unit, is not left too empty (of one matrix; of several it is not known
+        // how many there are): 272 tiles 205 us, by tiles of 128 x 128 188; 544 324 and 337
+        const bool even = batch > 1 || big <= 256 || 2 * ((big + 255) / 256 * 256) <= 3 * big;
+        const int side = each >= 256 && big * steps >= 256 * 32 && even ? 256 : 128;
         plan.tile_rows = plan.tile_cols = side;
         tiles = side == 256 ? big : product_tile_rows(tokens, batch, 128) * ((cols + 127) / 128);
     }

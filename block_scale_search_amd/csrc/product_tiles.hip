@@ -74,21 +74,24 @@ struct Cursor {
 // Workgroup -> tile. Workgroups go to the 8 XCDs in turn. One matrix: XCD x takes a run of tiles, and a run walks down 4
 // row tiles before the next column tile, so that the 32 workgroups on an XCD read 4 row tiles and 8 column tiles together.
 // Several: how many row tiles there are is not known here, and rows of different matrices share nothing but their own
-// column tiles: XCD x takes every eighth row tile (with runs, 2048 x 768 by 128 rows each of 128 matrices left half
-// of the XCDs without work, 165 us).
+// column tiles. From kManyRowTiles on XCD x takes every eighth row tile (with runs, 2048 x 768 by 128 rows each of 128
+// matrices left half of the XCDs without work, 165 us); fewer would leave XCDs without work that way, so a run walks down all
+// row tiles before the next column tile (gradients of 512 rows by 2 of 2 x 14336 x 4096 224 us, by every eighth
+// row tile 378; 48 row tiles 74.6 and 79; 64 150 and 137).
 __device__ __forceinline__ void tile_of(uint32_t id, uint32_t nm, uint32_t nn, bool several, int& tm, int& tn) {
     const uint32_t xcd = id & 7, j = id >> 3;
-    if (several) {
+    if (several && nm >= (uint32_t)kManyRowTiles) {
         tm = (int)(j / nn * 8 + xcd);
         tn = (int)(j % nn);
         return;
     }
     const uint32_t blocks = nm * nn, rest = blocks & 7;
     const uint32_t q = xcd * (blocks >> 3) + min(xcd, rest) + j;
-    const uint32_t group = q / (4 * nn), l = q - group * 4 * nn;
-    const uint32_t high = min(4u, nm - 4 * group);
+    const uint32_t down = several ? nm : 4;
+    const uint32_t group = q / (down * nn), l = q - group * down * nn;
+    const uint32_t high = min(down, nm - down * group);
     tn = (int)(l / high);
-    tm = (int)(4 * group + l - (uint32_t)tn * high);
+    tm = (int)(down * group + l - (uint32_t)tn * high);
 }
 
 // WHOLE (forward): in is a multiple of 32, so a thread's 32 columns are all inside the matrix or all outside.

@@ -308,3 +308,19 @@ def test_bias_gradients(nv, counts, out, name, dtype):
     # whole numbers: exact; else slopes of at most 1.2, off by at most 16 steps, and sums of T of them
     off = 0 if name == "none" else (16 + T) * 2.0 ** -23 * 1.2 * size
     assert bool(((got.double() - want).abs() <= off).all())
+
+
+@pytest.mark.parametrize("counts, out, inp", [([300, 260, 200, 400], 4096, 4096), ([70, 130], 264, 1040),
+                                              ([129, 1, 200, 64], 136, 2064), ([140] * 40, 136, 272), ([140] * 70, 72, 272)])
+def test_tiles_of_several_matrices(nv, counts, out, inp):
+    """Few and many tiles of rows, large and small ones, in both directions."""
+    E, T = len(counts), sum(counts)
+    w, v = Weights(E, out, inp, 1, whole=True), Weights(E, out, inp, 2, whole=True)
+    d, seg = rows((T, out), BF16, 3, whole=True), offsets(counts).to(DEV)
+    want = product(d, w, counts, transposed=False)[0]
+    same(nv.linear_backward(w.matrix(nv), d.to(DEV), seg_offsets=seg)["dX"], want, BF16, "dX")
+    if out < 4096:
+        x = rows((T, inp), F32, 4, whole=True)
+        _, g, u = nv.gated(w.matrix(nv), v.matrix(nv), x.to(DEV), seg_offsets=seg, with_pre=True)
+        same(g, product(x, w, counts)[0], F32, "G")
+        same(u, product(x, v, counts)[0], F32, "U")
