@@ -100,8 +100,8 @@ ProductPlan product_plan(int64_t tokens, int64_t batch, int64_t out, int64_t in,
     const int64_t each = batch > 0 ? (tokens + batch - 1) / batch : 0;
     int64_t steps, tiles;
     // rows of a matrix (on average): up to 4 of them pass through the kernel that keeps them in registers (8192 x 28672:
-    // 39.2 us at 4 rows, 48.3 at 8; by tiles of 32 rows 46.1 and 45.7), up to 96 through tiles whose weights are
-    // converted where they are used (96 rows 70 us, 128 rows 106; by tiles through LDS 88 and 93)
+    // 37.6 us at 4 rows, by tiles of 32 rows 46; twice 4 take 48.3 and 47, of 2 x 14336 x 4096 34 and 28.7), up to 96
+    // through tiles whose weights are converted where they are used (96 rows 70 us, 128 rows 106; by tiles through LDS 88 and 93)
     if (!backward && each <= 4) {
         plan.kernel = ProductKernel::kRows;
         plan.tile_rows = 4;
