@@ -81,7 +81,8 @@ Bias bias_of(int64_t tokens, int64_t batch, int64_t cols) {
     if (!b.narrow) {
         const int64_t groups = batch * b.groups;
         const int64_t want = (2048 + groups - 1) / groups, most = (tokens / batch + kShareRows - 1) / kShareRows;
-        b.shares = (int32_t)(want < most ? (want < 64 ? want : 64) : (most < 64 ? most : 64));
+        const int64_t shares = want < most ? want : most;
+        b.shares = (int32_t)(shares < 1 ? 1 : shares < 64 ? shares : 64);   // with fewer rows than matrices too: zeros
     }
     b.blocks = (int32_t)(b.groups * batch * b.shares);
     return b;
