@@ -10,7 +10,7 @@ namespace {
 constexpr int64_t kInt32 = (int64_t)1 << 31;
 constexpr int64_t kMaxSide = (int64_t)1 << 22;     // 32-bit offsets inside a tile
 constexpr int64_t kMaxSpan = (int64_t)1 << 56;
-constexpr int64_t kMaxBiases = (int64_t)1 << 29;   // gradients of biases: 4 threads each
+constexpr int64_t kMaxBiases = (int64_t)1 << 29;   // gradients of biases: 4 threads each, matrices rounded up to 256
 constexpr int64_t kThreads32 = ((int64_t)1 << 32) - 256;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }

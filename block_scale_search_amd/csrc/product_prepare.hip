@@ -217,14 +217,14 @@ size_t product_bias_workspace_bytes(int64_t tokens, int64_t batch, int64_t cols)
 
 hipError_t launch_product_slopes(const ProductSlopes& p, bool slopes, float* dbias, void* workspace, hipStream_t stream) {
     const int64_t pieces = (p.cols + 7) / 8, total = slopes ? p.rows.tokens * pieces : 0;
-    if (dbias && total >= (int64_t)1 << 31) {            // a launch has fewer than 2^32 threads
-        const hipError_t e = launch_product_slopes(p, false, dbias, workspace, stream);
-        return e == hipSuccess ? launch_product_slopes(p, true, nullptr, nullptr, stream) : e;
-    }
     Bias b{};
     if (dbias) {
         b = bias_of(p.rows.tokens, p.rows.batch, p.cols);
         b.to = b.shares > 1 ? static_cast<float*>(workspace) : dbias;
+    }
+    if (total > 0 && b.blocks > ((((int64_t)1 << 32) - 256) - total) / kThreads) {   // a launch has fewer than 2^32 threads
+        const hipError_t e = launch_product_slopes(p, false, dbias, workspace, stream);
+        return e == hipSuccess ? launch_product_slopes(p, true, nullptr, nullptr, stream) : e;
     }
     const dim3 grid((uint32_t)(b.blocks + (total + kThreads - 1) / kThreads));
     const Wide w{wide(p.dY, p.lddy, p.f32), wide(p.Z, p.ldz, p.f32), wide(p.U, p.ldu, p.f32),

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from product_helpers import DEV, act, act_model, offsets, rows
+from product_helpers import DEV, act, act_model, close, offsets, rows, sum_error
+from product_helpers import _E4M3 as E4M3, _LEVELS as LEVELS
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -14,6 +15,13 @@ def matrices(nv, E, out, inp):
     p = torch.randint(0, 256, (E, out, inp // 2), generator=g, dtype=torch.uint8, device=DEV)
     s = torch.randint(40, 70, (E, out, inp // 16), generator=g, dtype=torch.uint8, device=DEV)
     return nv.Matrix(p, s, torch.ones(E, device=DEV))
+
+
+def values(m, e):
+    """Matrix e's weights [out, in] in 64 bits, on the CPU."""
+    p, s = m.packed[e].cpu(), m.scales[e].cpu()
+    code = torch.stack([p & 15, p >> 4], -1).flatten(-2).long()
+    return LEVELS[code] * E4M3[s.long()].repeat_interleave(16, -1) * m.S[e].double().cpu()
 
 
 def backward(nv, m, d, name, z, seg, dbias):
@@ -46,3 +54,32 @@ def test_many_biases_of_few_rows(nv, E, out, having, name, dtype):
     dz = d.double() * act_model(z.double(), name)[1]
     want = torch.zeros((E, out), dtype=torch.float64).index_add_(0, at, dz)
     assert torch.equal(dbias.cpu(), want.float())
+
+
+def test_slopes_and_many_biases_beyond_one_launch(nv):
+    """Values by the slopes' pass and bias workgroups that have more than 2^32 threads between them: the call is one of
+    those that the sizes allow (the rows that belong to no matrix are never written: what they hold does not matter)."""
+    E, out, inp = 65528, 8193, 16
+    T = (2 ** 31 - 1) // ((out + 7) // 8)
+    assert E * out <= 2 ** 29 and T * ((out + 7) // 8) < 2 ** 31
+    assert E * ((out + 63) // 64) * 256 + T * ((out + 7) // 8) > 2 ** 32
+    m = matrices(nv, E, out, inp)
+    having = {0: 3, 40000: 50, E - 1: 4}
+    counts = [having.get(e, 0) for e in range(E)]
+    n = sum(counts)
+    d = torch.empty((T, out), dtype=BF16, device=DEV)
+    head = rows((n, out), BF16, 1, whole=True)
+    d[:n] = head.to(DEV)
+    dbias = torch.full((E, out), float("nan"), device=DEV)
+    dX = backward(nv, m, d, "none", None, offsets(counts).to(DEV), dbias)
+    at = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    for e in having:
+        assert torch.equal(dbias[e].cpu(), head[at == e].double().sum(0).float())
+        dbias[e] = 0
+    assert int(torch.count_nonzero(dbias)) == 0
+    for e in having:
+        w = values(m, e)
+        want, size = head[at == e].double() @ w, head[at == e].double().abs() @ w.abs()
+        close(dX[:n].cpu()[at == e], want, sum_error(size, out, BF16), BF16, f"dX of matrix {e}")
+    del d, dX, dbias, m
+    torch.cuda.empty_cache()
