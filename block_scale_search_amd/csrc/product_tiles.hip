@@ -120,7 +120,12 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     const int nk = (K + 2 * BK - 1) / (2 * BK) * 2;      // steps go in pairs: the last one may be empty
     const int matrices = MODE == kBackward ? p.matrices : 1;
     const int begin = split * each, steps = min(each, nk * p.planes * matrices - begin);
-    const int to_switch = nk * p.planes - begin;         // the step at which the second matrix begins
+    const int to_switch = nk * p.planes - begin;         // the step at which the next matrix begins
+    // Of two matrices the one of the smaller S goes first, so that the quotient of the S by which its sums go over to the
+    // other's is at most 1: the sums of two matrices do not overflow where dX does not.
+    int swapped = 0;
+    if constexpr (MODE == kBackward)
+        swapped = __builtin_amdgcn_readfirstlane(matrices == 2 && p.w[0].S[rows.e] > p.w[1].S[rows.e]);
 
     // copies of the rows' side: a thread's piece is the same in each of its rows
     const uint16_t* const a0 = p.a[0].p + rows.first * p.a[0].ld;
@@ -139,7 +144,7 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
     };
     const auto source = [&](const Cursor& c) {
         // pieces past the edge read the row's last: they meet weights of zero
-        const uint16_t* base = MODE == kBackward && c.m ? a1 : a0;
+        const uint16_t* base = MODE == kBackward && (c.m ^ swapped) ? a1 : a0;
         const int kt = min(c.kt, (K - 1) / BK);
         base += c.plane * p.plane + kt * BK;
         const int last = (k_pad - kt * BK) * 2 - 16;
@@ -186,7 +191,7 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         const int left = K - c.kt * BK;                  // of the reduction
         const uint32_t reach = step < steps ? kReach : 0;              // no codes past the last step
         if constexpr (MODE == kBackward) {
-            const ProductMatrix& w = p.w[c.m];
+            const ProductMatrix& w = p.w[c.m ^ swapped];
             const int64_t at = rows.e * w.stride + (int64_t)c.kt * BK * N;
             const __amdgpu_buffer_rsrc_t from = window(w.packed + at / 2, reach), bytes = window(w.scales + at / 16, reach);
             const int mine = left - b_first;
@@ -352,8 +357,8 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
         const std::integral_constant<int, (J + 1) & 1> x_odd;
         const std::integral_constant<int, J & 1> y_odd;
         if constexpr (MODE == kBackward) {
-            if (s == to_switch && s > 0 && s < steps) {  // the second matrix's sums carry its S
-                const float r = p.w[0].S[rows.e] / p.w[1].S[rows.e];
+            if (s == to_switch && s > 0 && s < steps) {  // the sums carry the S of the matrix met last
+                const float r = p.w[swapped].S[rows.e] / p.w[1 - swapped].S[rows.e];
 #pragma unroll
                 for (int a = 0; a < TM; ++a)
 #pragma unroll
@@ -404,7 +409,7 @@ __global__ __launch_bounds__(64 * WM_ * WN_) void k_product_tiles(Product p, int
 
     // a lane holds rows 8 (e / 4) + 4 kg + e % 4 of column r32 of each 32 x 32 tile; backward, the sums are over the
     // S of the last matrix met
-    const int at = MODE == kBackward && to_switch < steps ? 1 : 0;
+    const int at = swapped ^ (MODE == kBackward && to_switch < steps ? 1 : 0);
     const float S0 = p.w[at].S[rows.e];
     const float S1 = MODE == kGated ? p.w[1].S[rows.e] : 0.0f;
     // 32 rows at a time by way of the wave's own part of LDS, so that a lane has 8 columns of a row
