@@ -10,13 +10,15 @@
 // codes of 4 groups a step. The slices' sums meet in LDS, in a fixed order.
 //
 // Operands. bf16 rows enter as f16 ones, a row's slice times a power of two, since f16 weights (level * E4M3 is exact in
-// them too) take half the instructions of bf16 ones: 2 to 8% of the whole. A value keeps all its bits
-// down to 2^-31 of the largest of its slice, below that those above 2^-39 of it: less than the binary32 sums round where
-// that largest value meets any weight but zero. The parts of f32 rows enter as bf16.
+// them too) take half the instructions of bf16 ones: 2 to 8% of the whole. f16 holds a value's bits down to 2^-31
+// of the largest of its slice; a wave that meets values below that, or an infinity or a NaN, takes that slice as bf16
+// instead (looking costs 1 to 2% of 4096 x 14336, nothing of larger ones). So do the parts of f32 rows enter.
 //
 // Measured: gate and up of 2 x 28672 x 8192, one row, 52.7 us = 5.0 TB/s, a large copy's rate; 8192 x 28672 29 us (4.6);
 // 4096 x 14336, 256 workgroups of 14 waves, 11.2 us (2.9), bound by launch and first codes.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "product_device.h"
@@ -35,9 +37,9 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 
-template <bool F32>
+template <bool HALF>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-    if constexpr (F32)
+    if constexpr (!HALF)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
     else
@@ -59,27 +61,44 @@ __device__ __forceinline__ u32x4 dequant8_half(uint32_t w, half2v scale) {
 }
 
 // Makes bf16 values f16 ones times 2^k, the largest magnitude of the row's slice (that of the 16 lanes with the same
-// n4) coming to 2^14 .. 2^15; returns k. A slice with an infinity or a NaN keeps it, whatever becomes of the others.
-__device__ __forceinline__ int to_half(u32x4 (&x)[8]) {
-    ushort2v most = {0, 0};
+// n4) coming to 2^14 .. 2^15; k to `raised`. Where a value of the wave would lose bits (f16's last bit is 2^-24, a bf16
+// value has eight) or is no number, false, and all stay as they are.
+__device__ __forceinline__ bool to_half(u32x4 (&x)[8], int& raised) {
+    ushort2v most = {0, 0}, least = {0xFFFF, 0xFFFF};
 #pragma unroll
     for (int s = 0; s < 8; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2v, x[s][j] & 0x7FFF7FFFu));
+        for (int j = 0; j < 4; ++j) {
+            const ushort2v a = __builtin_bit_cast(ushort2v, x[s][j] & 0x7FFF7FFFu);
+            most = __builtin_elementwise_max(most, a);
+            least = __builtin_elementwise_min(least, a);
+        }
     int m = max((int)most[0], (int)most[1]);
     m = max(m, __builtin_amdgcn_update_dpp(0, m, 0xB1, 0xF, 0xF, true));
     m = max(m, __builtin_amdgcn_update_dpp(0, m, 0x4E, 0xF, 0xF, true));
     m = max(m, __shfl_xor(m, 16, 64));
     m = max(m, __shfl_xor(m, 32, 64));
-    const int e = m >> 7, k = e == 255 ? 0 : 141 - max(e, 1);
+    const int e = m >> 7;
+    int low = min((int)least[0], (int)least[1]) >> 7;
+    if (__ballot(low < e - 31)) {                        // zeros, most often: the least of the others
+        least = ushort2v{0xFFFF, 0xFFFF};
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                least = __builtin_elementwise_min(
+                    least, (ushort2v)(__builtin_bit_cast(ushort2v, x[s][j] & 0x7FFF7FFFu) - (ushort2v){1, 1}));
+        low = (min((int)least[0], (int)least[1]) + 1) >> 7;
+    }
+    raised = 141 - max(e, 1);
+    if (__ballot(e == 255 || low < e - 31)) return false;
 #pragma unroll
     for (int s = 0; s < 8; ++s)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            x[s][j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_ldexpf(bf16_lo(x[s][j]), k),
-                                                                              __builtin_amdgcn_ldexpf(bf16_hi(x[s][j]), k)));
-    return k;
+            x[s][j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__builtin_amdgcn_ldexpf(bf16_lo(x[s][j]), raised),
+                                                                              __builtin_amdgcn_ldexpf(bf16_hi(x[s][j]), raised)));
+    return true;
 }
 
 // Sum over four neighbouring lanes, in each of them.
@@ -128,8 +147,6 @@ __global__ __launch_bounds__(64 * kWaves<F32>) void k_product_rows(Product p, in
 #pragma unroll
             for (int s = 0; s < 8; ++s) x[i][s] = load16(from, n4 < rows.rows && k + 8 * s < K ? at + 16 * s : kNowhere);
         }
-        int raised = 0;
-        if constexpr (!F32) raised = to_half(x[0]);
         const uint32_t first = (uint32_t)n4 * (uint32_t)(K / 16) + (uint32_t)(k / 16);   // in groups of 16 weights
         const auto load = [&](Codes& b, int g) {
             const int j = GATED && g >= half ? g - half : g;
@@ -156,47 +173,63 @@ __global__ __launch_bounds__(64 * kWaves<F32>) void k_product_rows(Product p, in
                 b.code[1] = u32x4{w[2][0], w[2][1], w[3][0], w[3][1]};
             }
         };
+        constexpr int kFirst = F32 ? kDepth : kDepth / 2;            // under way while the operands are made
         Codes buf[kDepth];
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
+        for (int d = 0; d < kFirst; ++d) {
             load(buf[d], d);
             __builtin_amdgcn_sched_barrier(0);
         }
-        for (int g0 = 0; g0 < groups; g0 += kDepth) {
+        // the slice's sums of all the workgroup's matrix rows; bf16 operands of a bf16 row, a rare case, with half as many codes
+        // in flight (registers)
+        const auto multiply_all = [&](auto half_operands, int raised) {
+            constexpr bool HALF = decltype(half_operands)::value;
+            constexpr int kAhead = HALF || F32 ? kDepth : kFirst;
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                Codes& b = buf[d];
-                f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-                const auto multiply = [&](const auto (&e)[4]) {
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        u32x4 w;
-                        if constexpr (F32) w = dequant8(b.code[s >> 2][s & 3], e[s >> 1]);
-                        else w = dequant8_half(b.code[s >> 2][s & 3], e[s >> 1]);
-#pragma unroll
-                        for (int i = 0; i < P; ++i) acc[s & 1] = mfma<F32>(w, x[i][s], acc[s & 1]);
-                    }
-                };
-                if constexpr (F32) {
-                    const float e[4] = {scale_value<0>(b.scale), scale_value<1>(b.scale), scale_value<2>(b.scale),
-                                        scale_value<3>(b.scale)};
-                    multiply(e);
-                } else {
-                    const uint32_t bytes = b.scale & 0x7F7F7F7Fu;
-                    const half2v e[4] = {scale_half<0>(bytes), scale_half<1>(bytes), scale_half<2>(bytes),
-                                         scale_half<3>(bytes)};
-                    multiply(e);
-                }
-                load(b, g0 + d + kDepth);
-                // register r of a lane holds piece r of matrix row kg; the lane's own piece is seg
-                const f32x4 a = acc[0] + acc[1];
-                float v = sum_quad(seg < 2 ? (seg == 0 ? a[0] : a[1]) : (seg == 2 ? a[2] : a[3]));
-                if constexpr (!F32) v = __builtin_amdgcn_ldexpf(v, -raised);
-                float* to = sums + (wave * groups + g0 + d) * 64 + lane;
-                *to = slice == wave ? v : *to + v;
-                __builtin_amdgcn_sched_barrier(0);       // else all loads are issued together, and waited for together
+            for (int d = kFirst; d < kAhead; ++d) {
+                load(buf[d], d);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
+            for (int g0 = 0; g0 < groups; g0 += kAhead) {
+#pragma unroll
+                for (int d = 0; d < kAhead; ++d) {
+                    Codes& b = buf[d];
+                    f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+                    const auto multiply = [&](const auto (&e)[4]) {
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) {
+                            u32x4 w;
+                            if constexpr (HALF) w = dequant8_half(b.code[s >> 2][s & 3], e[s >> 1]);
+                            else w = dequant8(b.code[s >> 2][s & 3], e[s >> 1]);
+#pragma unroll
+                            for (int i = 0; i < P; ++i) acc[s & 1] = mfma<HALF>(w, x[i][s], acc[s & 1]);
+                        }
+                    };
+                    if constexpr (!HALF) {
+                        const float e[4] = {scale_value<0>(b.scale), scale_value<1>(b.scale), scale_value<2>(b.scale),
+                                            scale_value<3>(b.scale)};
+                        multiply(e);
+                    } else {
+                        const uint32_t bytes = b.scale & 0x7F7F7F7Fu;
+                        const half2v e[4] = {scale_half<0>(bytes), scale_half<1>(bytes), scale_half<2>(bytes),
+                                             scale_half<3>(bytes)};
+                        multiply(e);
+                    }
+                    load(b, g0 + d + kAhead);
+                    // register r of a lane holds piece r of matrix row kg; the lane's own piece is seg
+                    const f32x4 a = acc[0] + acc[1];
+                    float v = sum_quad(seg < 2 ? (seg == 0 ? a[0] : a[1]) : (seg == 2 ? a[2] : a[3]));
+                    if constexpr (HALF) v = __builtin_amdgcn_ldexpf(v, -raised);
+                    float* to = sums + (wave * groups + g0 + d) * 64 + lane;
+                    *to = slice == wave ? v : *to + v;
+                    __builtin_amdgcn_sched_barrier(0);       // else all loads are issued together, and waited for together
+                }
+            }
+        };
+        int raised = 0;
+        if constexpr (F32) multiply_all(std::false_type{}, 0);
+        else if (to_half(x[0], raised)) multiply_all(std::true_type{}, raised);
+        else multiply_all(std::false_type{}, 0);
     }
     __syncthreads();
 

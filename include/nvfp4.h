@@ -470,8 +470,7 @@ nvfp4_status nvfp4_output_error(const void* X, int x_dtype, int64_t tokens, int6
  * Row tensors are bf16 or f32 (dtype, the same for all of a call; bias too), with a row stride in elements
  * of at least their columns. Sums are binary32: level * E4M3 is exact in bf16, a bf16 value enters the MFMA
  * products as it is and an f32 value as three bf16 parts (exact for magnitudes that are zero or above 2^-100), so
- * the products themselves are exact. (Forward, with up to 4 rows a matrix on average, a bf16 value below 2^-31 of the
- * largest among 1024 columns of its row is taken to within 2^-38 of that largest.) Outputs are rounded once (to nearest even), from binary32. Where a row
+ * the products themselves are exact. Outputs are rounded once (to nearest even), from binary32. Where a row
  * that enters a product holds a NaN or an infinity, all sums of that row (z, g, u, dX) are infinite or NaN (which of
  * the two is not specified); other rows are not touched by it. A tensor of outputs may
  * not overlap any other tensor of the call, but Y may be the residual itself (same address, same stride).
