@@ -17,9 +17,12 @@ struct ProductMatrix {
 };
 
 // Which rows meet which matrix: rows seg[e] .. seg[e+1] - 1 matrix e; no seg: all rows matrix 0.
-// map: with more than kMapped matrices, what each tile of rows is (filled by a kernel of its own, which costs what
-// searching the offsets in each workgroup does at about 128: gate and up of 128 matrices of 768 x 2048, 512 rows, 71.6
-// us with a map and 65.6 without); else not used.
+// map: with more than kMapped matrices, what each tile of rows is, filled by a kernel of its own (some 2 us); else not
+// used, and each workgroup searches the offsets, 64 at a time. Gradients are as fast either way at 128 matrices, forward products
+// at some 256, and in between each loses 4% at most by the other's limit. Us without a map and with it, of 4 rows a matrix by
+// gate and up of 768 x 2048, 64 by 512 x 768, and 64 back through 2 x 512 x 1024: 128 matrices 63.3 and 66.3, 28.2 and 29.7,
+// 87.7 and 87.8; 256 matrices 110.6 and 114.4, 48.1 and 47.5, 164.6 and 158.6; 512 matrices 245 and 235, 93.5 and 83.9, 351
+// and 319.
 constexpr int kMapped = 128;
 struct RowTile {
     int32_t e, rows;         // rows 0: none
