@@ -4,6 +4,10 @@
 // Parts. A binary32 value is the sum of three bf16 values, each the truncation of what the earlier ones leave
 // (8 + 8 + 8 bits: exact, but for what lies below 2^-133); an infinity or NaN is its first part. Each part's
 // product with a weight is exact in binary32, as that of a bf16 value is.
+// Slopes. dZ, dG and dU are rounded once, to the outputs' type, and the product reads those: dX is the product of what
+// the caller gets, as in a program of separate calls. So bf16 dX of a pair is off by 2.3e-3 of its norm; from unrounded
+// values, as two bf16 parts and thus by twice the product, it would be 1.7e-3, its own rounding. A bias's gradient sums
+// the unrounded.
 // All of these kernels read and write once: they are bound by memory (dG and dU of 4096 x 14336 from three such tensors 94 us,
 // 6.2 TB/s with what the cache still holds) or, small, by their chain of loads (333 x 1003 in binary32 with a bias 12 us).
 #include <hip/hip_runtime.h>

@@ -14,8 +14,8 @@
 // of the largest of its slice; a wave that meets values below that, or an infinity or a NaN, takes that slice as bf16
 // instead (looking costs 1 to 2% of 4096 x 14336, nothing of larger ones). So do the parts of f32 rows enter.
 //
-// Measured: gate and up of 2 x 28672 x 8192, one row, 52.7 us = 5.0 TB/s, a large copy's rate; 8192 x 28672 29 us (4.6);
-// 4096 x 14336, 256 workgroups of 14 waves, 11.2 us (2.9), bound by launch and first codes.
+// Measured: gate and up of 2 x 28672 x 8192, one row, 52.3 us = 5.0 TB/s, a large copy's rate; 8192 x 28672 29 us (4.6);
+// 4096 x 14336, 256 workgroups of 14 waves, 11.4 us (2.9), bound by launch and first codes.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
